@@ -87,7 +87,7 @@ def draw(rng):
                     packed=rng.choice([0, 0, 1, 2]), inplace=rng.random() < 0.4, max_pos=_log(rng, 1, 32768))
     if op == "rope_table":
         dim = rng.choice([64, 128, 256, 512])
-        return dict(op=op, max_pos=_log(rng, 1, 200000), rot=2 * rng.randint(1, min(dim, 256) // 2), dim=dim,
+        return dict(op=op, max_pos=_log(rng, 16, 200000), rot=2 * rng.randint(1, min(dim, 256) // 2), dim=dim,
                     theta=rng.choice([1e4, 5e5, 1e6]), kind=rng.choice(["none", "linear", "ntk", "ramp"]),
                     factor=rng.uniform(1.0, 32.0), low=rng.uniform(0.5, 2.0), high=rng.uniform(8.0, 40.0),
                     orig=_log(rng, 2048, 32768), amplitude=rng.uniform(1.0, 1.4))
@@ -100,9 +100,11 @@ def draw(rng):
                     decay=rng.choice([0.0, 0.9, 1.0]))
     budget = rng.randint(1, max_len)
     if op == "select":
-        sinks = rng.randint(0, min(64, budget))
+        max_len = max(64, max_len)
+        budget = rng.randint(8, max_len // 2)
+        sinks = rng.randint(0, min(64, budget // 4))
         return dict(op=op, batch=batch, min_len=min_len, max_len=max_len, budget=budget, sinks=sinks,
-                    recent=rng.randint(0, budget - sinks))
+                    recent=rng.randint(0, budget // 2))
     return dict(op=op, layout=rng.choice(list(LAYOUT)), batch=batch, min_len=min_len, max_len=max_len,
                 budget=budget, copy=rng.random() < 0.4)
 

@@ -184,6 +184,92 @@ gw_status gw_kv_append(const gw_kv_pool* pool, const void* k, const void* v, int
 gw_status gw_rope_cs(float* rope_cs, double theta, int32_t rot_dim, int32_t head_dim, int32_t max_pos,
                      void* stream);
 
+/* ---- rotation of other rows than the append's ---------------------------- */
+#define GW_ELEM_BF16 0
+#define GW_ELEM_F16 1
+#define GW_ELEM_F32 2
+
+#define GW_PAIRS_HALF 0        /* pair i is (x[i], x[i + rot_dim/2])          */
+#define GW_PAIRS_INTERLEAVED 1 /* pair i is (x[2i], x[2i + 1])                */
+
+/*
+ * gw_rope_rows - rotate rows by their positions: the q rows that the attention
+ * calls take, or any rows whose rotation gw_kv_append does not do itself.
+ *
+ * For row r, head h and pair i in [0, rot_dim/2), with (c, s) =
+ * rope_cs[pos[r]][i] and (x0, x1) the pair's two elements (exact fp32):
+ *
+ *   y0 = fl(fl(x0*c) - fl(x1*s)),  y1 = fl(fl(x1*c) + fl(x0*s))
+ *
+ * in binary32 without fused multiply-add, rounded once to the element type:
+ * on half pairs of bf16 rows the bits that gw_kv_append stores in a bf16 pool.
+ * With `inverse` the angle is negated, which undoes the rotation and is its
+ * gradient (the map is orthogonal up to the table's amplitude).  Elements
+ * [rot_dim, head_dim) are copied.
+ *
+ *   x, y      element (r, h, d) at x[r*x_row_stride + h*x_head_stride + d]
+ *             (strides in elements), so x may be a slice of a packed
+ *             projection, or head-major.  y == x with the same strides rotates
+ *             in place and touches the rotated dims only; otherwise the two
+ *             extents must not overlap.  y's rows must not overlap one another;
+ *             x's may (a stride of 0 broadcasts).
+ *   elem      GW_ELEM_*; x and y aligned to it.  Rows at 16-byte boundaries
+ *             take a faster path with the same results.
+ *   pairs     GW_PAIRS_*.
+ *   pos       int32 [num_rows], 4-byte aligned.  A row whose position is
+ *             outside [0, max_pos) is left as it was in y (GW_DEV_POS_RANGE).
+ *   rope_cs   float32 [max_pos][rot_dim/2][2], 16-byte aligned (gw_rope_cs,
+ *             gw_rope_cs_scaled).
+ *   head_dim in [2, 1024], rot_dim even in [2, head_dim].  num_rows or
+ *   num_heads of 0 is a no-op.
+ * K rows that are to be cached with interleaved pairs: rotate them here, then
+ * append them at position 0, whose angle is 0 (gw_kv_append then stores them
+ * as they are; their slot says where they go).
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_rope_rows(const void* x, int64_t x_row_stride, int64_t x_head_stride, void* y, int64_t y_row_stride,
+                       int64_t y_head_stride, int32_t elem, int32_t num_rows, int32_t num_heads, int32_t head_dim,
+                       int32_t rot_dim, int32_t pairs, int32_t inverse, const int32_t* pos, const float* rope_cs,
+                       int32_t max_pos, int32_t* dev_status, void* stream);
+
+#define GW_ROPE_NONE 0
+#define GW_ROPE_LINEAR 1
+#define GW_ROPE_NTK 2
+#define GW_ROPE_RAMP 3
+
+/* How a table is scaled for contexts longer than the trained one. */
+typedef struct gw_rope_scaling {
+  int32_t kind;      /* GW_ROPE_*                                             */
+  int32_t reserved;  /* 0                                                     */
+  double factor;     /* > 0: the context's growth (all kinds but NONE)        */
+  double low, high;  /* RAMP: turns below / above which a pair is fully / not
+                        at all interpolated; 0 <= low < high                  */
+  double orig_max_pos; /* RAMP: the trained context, > 0                      */
+  double amplitude;  /* > 0: multiplies cos and sin (1 for none)              */
+} gw_rope_scaling;
+
+/*
+ * gw_rope_cs_scaled - gw_rope_cs for scaled contexts: fills
+ *
+ *   rope_cs[p][i] = amplitude * (cos(p * f_i), sin(p * f_i)),  f_i from
+ *   inv_f_i = theta^((-2 i) / head_dim):
+ *
+ *   NONE    f_i = inv_f_i
+ *   LINEAR  f_i = inv_f_i / factor                (positions interpolated)
+ *   NTK     theta replaced by theta * factor^(head_dim / (head_dim - 2)), so
+ *           that the lowest frequency of a full head is divided by factor
+ *   RAMP    n_i = orig_max_pos * inv_f_i / (2 pi) turns over the trained
+ *           context, g_i = clamp((n_i - low) / (high - low), 0, 1),
+ *           f_i = inv_f_i * (g_i + (1 - g_i) / factor)
+ *
+ * with frequencies and angles in float64 and one rounding to float32.
+ * Arguments as gw_rope_cs, rot_dim at most 512; `scaling` is host memory.
+ * Errors: GW_ERR_INVALID_ARG (those of gw_rope_cs, a scaling NULL or outside
+ * the ranges above), GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32_t head_dim, int32_t max_pos,
+                            const gw_rope_scaling* scaling, void* stream);
+
 /*
  * gw_decode_attn_local - sliding-window attention on a LOCAL pool.
  *

@@ -197,6 +197,112 @@ gw_status gw_rope_cs(float* rope_cs, double theta, int32_t rot_dim, int32_t head
                      fn);
 }
 
+gw_status gw_rope_rows(const void* x, int64_t x_row_stride, int64_t x_head_stride, void* y, int64_t y_row_stride,
+                       int64_t y_head_stride, int32_t elem, int32_t num_rows, int32_t num_heads, int32_t head_dim,
+                       int32_t rot_dim, int32_t pairs, int32_t inverse, const int32_t* pos, const float* rope_cs,
+                       int32_t max_pos, int32_t* dev_status, void* stream) {
+  const char* fn = "gw_rope_rows";
+  g_err[0] = 0;
+  if (elem != GW_ELEM_BF16 && elem != GW_ELEM_F16 && elem != GW_ELEM_F32)
+    return fail(GW_ERR_INVALID_ARG, fn, "unknown elem %d", elem);
+  if (pairs != GW_PAIRS_HALF && pairs != GW_PAIRS_INTERLEAVED)
+    return fail(GW_ERR_INVALID_ARG, fn, "unknown pairs %d", pairs);
+  if (num_rows < 0 || num_heads < 0) return fail(GW_ERR_INVALID_ARG, fn, "num_rows < 0 or num_heads < 0");
+  if (head_dim < 2 || head_dim > 1024 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2)
+    return fail(GW_ERR_INVALID_ARG, fn, "need head_dim in [2, 1024] and an even rot_dim in [2, head_dim] (%d, %d)",
+                head_dim, rot_dim);
+  if (max_pos < 1) return fail(GW_ERR_INVALID_ARG, fn, "max_pos must be >= 1");
+  if (num_rows == 0 || num_heads == 0) return GW_OK;
+  const size_t size = elem == GW_ELEM_F32 ? 4 : 2;
+  if (!x || !y || !aligned(x, size) || !aligned(y, size)) return fail(GW_ERR_INVALID_ARG, fn, "x/y NULL or misaligned");
+  if (!pos || !aligned(pos, 4)) return fail(GW_ERR_INVALID_ARG, fn, "pos NULL or misaligned");
+  if (!rope_cs || !aligned(rope_cs, 16)) return fail(GW_ERR_INVALID_ARG, fn, "rope_cs NULL or not 16-byte aligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  constexpr int64_t kMaxStride = int64_t{1} << 40;  // extents below stay within 64 bits
+  if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0 || x_row_stride > kMaxStride ||
+      x_head_stride > kMaxStride || y_row_stride > kMaxStride || y_head_stride > kMaxStride)
+    return fail(GW_ERR_INVALID_ARG, fn, "a stride is negative or above 2^40");
+  using wide = unsigned __int128;
+  const wide rows1 = num_rows - 1, heads1 = num_heads - 1, dim = head_dim;
+  // y: heads within rows, or rows within heads (a dimension of one never overlaps)
+  const bool by_row = (num_heads == 1 || y_head_stride >= head_dim) &&
+                      (num_rows == 1 || wide(y_row_stride) >= heads1 * y_head_stride + dim);
+  const bool by_head = (num_rows == 1 || y_row_stride >= head_dim) &&
+                       (num_heads == 1 || wide(y_head_stride) >= rows1 * y_row_stride + dim);
+  if (!by_row && !by_head) return fail(GW_ERR_INVALID_ARG, fn, "rows of y overlap one another");
+  const bool inplace = x == y;
+  if (inplace) {
+    if ((num_rows > 1 && x_row_stride != y_row_stride) || (num_heads > 1 && x_head_stride != y_head_stride))
+      return fail(GW_ERR_INVALID_ARG, fn, "in place, x and y need the same strides");
+  } else {
+    const wide x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
+    const wide x1 = x0 + (rows1 * x_row_stride + heads1 * x_head_stride + dim) * size;
+    const wide y1 = y0 + (rows1 * y_row_stride + heads1 * y_head_stride + dim) * size;
+    if (x0 < y1 && y0 < x1) return fail(GW_ERR_INVALID_ARG, fn, "x and y overlap and are not the same rows");
+  }
+  RopeRowsArgs a{};
+  a.x = x;
+  a.y = y;
+  a.x_row = x_row_stride;
+  a.x_head = x_head_stride;
+  a.y_row = y_row_stride;
+  a.y_head = y_head_stride;
+  a.num_rows = num_rows;
+  a.num_heads = num_heads;
+  a.head_dim = head_dim;
+  a.rot_dim = rot_dim;
+  a.pairs = pairs;
+  a.inverse = inverse != 0;
+  a.inplace = inplace;
+  a.pos = pos;
+  a.rope_cs = rope_cs;
+  a.max_pos = max_pos;
+  a.status = dev_status;
+  a.early_inputs = g_early_inputs ? 1 : 0;
+  return cuda_status(launch_rope_rows(elem, a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32_t head_dim, int32_t max_pos,
+                            const gw_rope_scaling* scaling, void* stream) {
+  const char* fn = "gw_rope_cs_scaled";
+  g_err[0] = 0;
+  if (!rope_cs || !aligned(rope_cs, 16)) return fail(GW_ERR_INVALID_ARG, fn, "rope_cs NULL or not 16-byte aligned");
+  if (!(theta > 0.0) || !std::isfinite(theta)) return fail(GW_ERR_INVALID_ARG, fn, "theta must be finite and > 0");
+  if (head_dim < 2 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 || rot_dim > 2 * kMaxRopePairs)
+    return fail(GW_ERR_INVALID_ARG, fn, "need an even rot_dim in [2, min(head_dim, %d)] (rot_dim %d, head_dim %d)",
+                2 * kMaxRopePairs, rot_dim, head_dim);
+  if (max_pos < 1) return fail(GW_ERR_INVALID_ARG, fn, "max_pos must be >= 1");
+  if (!scaling) return fail(GW_ERR_INVALID_ARG, fn, "scaling is NULL");
+  const gw_rope_scaling& sc = *scaling;
+  if (sc.kind < GW_ROPE_NONE || sc.kind > GW_ROPE_RAMP || sc.reserved != 0)
+    return fail(GW_ERR_INVALID_ARG, fn, "unknown scaling kind %d, or reserved not 0", sc.kind);
+  auto positive = [](double v) { return v > 0.0 && std::isfinite(v); };
+  if (!positive(sc.amplitude)) return fail(GW_ERR_INVALID_ARG, fn, "amplitude must be finite and > 0");
+  if (sc.kind != GW_ROPE_NONE && !positive(sc.factor))
+    return fail(GW_ERR_INVALID_ARG, fn, "factor must be finite and > 0");
+  if (sc.kind == GW_ROPE_NTK && head_dim <= 2) return fail(GW_ERR_INVALID_ARG, fn, "NTK needs head_dim > 2");
+  if (sc.kind == GW_ROPE_RAMP &&
+      (!positive(sc.orig_max_pos) || !(sc.low >= 0.0) || !(sc.high > sc.low) || !std::isfinite(sc.high)))
+    return fail(GW_ERR_INVALID_ARG, fn, "RAMP needs orig_max_pos > 0 and 0 <= low < high, all finite");
+  if (sc.kind == GW_ROPE_NTK) theta *= std::pow(sc.factor, static_cast<double>(head_dim) / (head_dim - 2));
+  RopeFreqs fr{};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(theta, (-2.0 * i) / head_dim);
+    if (sc.kind == GW_ROPE_LINEAR) f /= sc.factor;
+    if (sc.kind == GW_ROPE_RAMP) {
+      const double turns = sc.orig_max_pos * f / 6.283185307179586;
+      double g = (turns - sc.low) / (sc.high - sc.low);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f *= g + (1.0 - g) / sc.factor;
+    }
+    if (!std::isfinite(f)) return fail(GW_ERR_INVALID_ARG, fn, "frequency %d is not finite", i);
+    fr.f[i] = f;
+  }
+  return cuda_status(launch_rope_cs_scaled(rope_cs, fr, sc.amplitude, rot_dim / 2, max_pos,
+                                           static_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
 size_t gw_attn_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch, int32_t max_seq_len,
                                int32_t max_q_rows, int32_t window) {
   (void)max_q_rows;

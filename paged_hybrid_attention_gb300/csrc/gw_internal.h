@@ -162,6 +162,27 @@ struct MergeArgs {
 cudaError_t launch_merge_lse(const MergeArgs& m, cudaStream_t st);
 // (cos, sin) table of gw_rope_cs: float32 [max_pos][rot_dim / 2][2].
 cudaError_t launch_rope_cs(float* out, double theta, int rot_dim, int head_dim, int max_pos, cudaStream_t st);
+// gw_rope_rows: strides in elements; `inplace` rows keep their unrotated dims.
+struct RopeRowsArgs {
+  const void* x;
+  void* y;
+  int64_t x_row, x_head, y_row, y_head;
+  int32_t num_rows, num_heads, head_dim, rot_dim;
+  int32_t pairs, inverse, inplace;
+  const int32_t* pos;
+  const float* rope_cs;
+  int32_t max_pos;
+  int32_t* status;
+  int32_t early_inputs;  // gw_set_early_inputs: pos and RoPE rows read before the wait
+};
+cudaError_t launch_rope_rows(int elem, const RopeRowsArgs& a, cudaStream_t st);
+// The pairs' frequencies of gw_rope_cs_scaled, computed on the host in float64.
+constexpr int kMaxRopePairs = 256;
+struct RopeFreqs {
+  double f[kMaxRopePairs];
+};
+cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amplitude, int half, int max_pos,
+                                  cudaStream_t st);
 cudaError_t launch_bw_probe(const void* buf, int64_t chunks, int32_t* status, cudaStream_t st);
 cudaError_t launch_bw_probe_tma(const void* buf, int64_t pages, int32_t* status, cudaStream_t st);
 cudaError_t launch_wait_selftest(int32_t* status, int32_t* result, int64_t limit_ns, cudaStream_t st);

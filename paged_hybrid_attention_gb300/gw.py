@@ -33,7 +33,12 @@ EXPORTS = ["gw_pool_page_bytes", "gw_kv_append", "gw_decode_attn_local", "gw_dec
            "gw_noalloc_scratch_bytes", "gw_bw_probe", "gw_set_max_ctas", "gw_set_early_launch",
            "gw_set_early_inputs", "gw_rope_cs", "gw_wait_selftest", "gw_bw_probe_tma",
            "gw_decode_attn_global_lse", "gw_merge_lse", "gw_append_decode_attn_local",
-           "gw_append_decode_attn_global"]
+           "gw_append_decode_attn_global", "gw_rope_rows", "gw_rope_cs_scaled"]
+
+
+ELEMS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+PAIRS_HALF, PAIRS_INTERLEAVED = 0, 1
+ROPE_KINDS = {"none": 0, "linear": 1, "ntk": 2, "ramp": 3}
 
 
 class GwError(RuntimeError):
@@ -46,6 +51,12 @@ class PoolDesc(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int32), ("dtype", ctypes.c_int32), ("base", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("orig_max_pos", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
 
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -73,6 +84,11 @@ _lib.gw_merge_lse.argtypes = [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
 _lib.gw_merge_lse.restype = _i32
 _lib.gw_rope_cs.argtypes = [_vp, ctypes.c_double, _i32, _i32, _i32, _vp]
 _lib.gw_rope_cs.restype = _i32
+_lib.gw_rope_rows.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                              _i32, _vp, _vp]
+_lib.gw_rope_rows.restype = _i32
+_lib.gw_rope_cs_scaled.argtypes = [_vp, ctypes.c_double, _i32, _i32, _i32, ctypes.POINTER(RopeScaling), _vp]
+_lib.gw_rope_cs_scaled.restype = _i32
 _lib.gw_attn_workspace_bytes.argtypes = [_P, _i32, _i32, _i32, _i32, _i32]
 _lib.gw_attn_workspace_bytes.restype = _sz
 _lib.gw_decode_attn_local_noalloc.argtypes = [_P, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _f32,
@@ -125,6 +141,34 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _invalid(fn, what):
+    raise GwError(GW_ERR_INVALID_ARG, "%s: %s" % (fn, what))
+
+
+def _on_device(fn, stream, *tensors):
+    """Every tensor on one CUDA device, which the stream (the current one if
+    None) belongs to and which is the current device: the library launches
+    on the current device."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            _invalid(fn, "tensors on %s and %s" % (dev, t.device))
+    if dev.type != "cuda":
+        _invalid(fn, "tensors on %s, not on a CUDA device" % dev)
+    if dev.index != torch.cuda.current_device() or (stream is not None and stream.device != dev):
+        _invalid(fn, "tensors on %s, but the current device or the stream is another" % dev)
+
+
+def _dense(fn, name, t, dtype, *shape):
+    """`t` has this dtype and shape (None: any length) and is contiguous."""
+    if t is None:
+        _invalid(fn, "%s is None" % name)
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        _invalid(fn, "%s must be %s of shape %s (got %s %s)" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+    if not t.is_contiguous():
+        _invalid(fn, "%s must be contiguous" % name)
+
+
 # ---- pools ---------------------------------------------------------------------
 class KVPool:
     """A paged pool held in a torch uint8 device buffer plus its ABI descriptor."""
@@ -157,6 +201,48 @@ def rope_cs(theta, rot_dim, head_dim, max_pos, out=None, device="cuda", stream=N
     if out is None:
         out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
     _check(_lib.gw_rope_cs(_ptr(out), float(theta), int(rot_dim), int(head_dim), int(max_pos), _stream(stream)))
+    return out
+
+
+def rope_cs_scaled(theta, rot_dim, head_dim, max_pos, kind="none", factor=1.0, low=1.0, high=32.0, orig_max_pos=0,
+                   amplitude=1.0, out=None, device="cuda", stream=None):
+    """gw_rope_cs_scaled: rope_cs for a context longer than the trained one, by
+    `kind` "none", "linear", "ntk" or "ramp" (include/gw.h states each)."""
+    fn = "gw_rope_cs_scaled"
+    if kind not in ROPE_KINDS:
+        _invalid(fn, "unknown kind %r" % (kind,))
+    if out is None:
+        out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    _on_device(fn, stream, out)
+    _dense(fn, "out", out, torch.float32, max_pos, rot_dim // 2, 2)
+    sc = RopeScaling(ROPE_KINDS[kind], 0, factor, low, high, orig_max_pos, amplitude)
+    _check(_lib.gw_rope_cs_scaled(_ptr(out), float(theta), int(rot_dim), int(head_dim), int(max_pos),
+                                  ctypes.byref(sc), _stream(stream)))
+    return out
+
+
+def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, inverse=False, dev_status=None,
+              stream=None):
+    """gw_rope_rows: the rows x [rows, heads, head_dim] (bf16, fp16 or fp32;
+    any strides, the last one 1) rotated by pos int32 [rows] into `out` (x
+    itself: in place; a new contiguous tensor if None), which is returned."""
+    fn = "gw_rope_rows"
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _on_device(fn, stream, x, out, pos, rope_cs, dev_status)
+    if x.dim() != 3 or x.dtype not in ELEMS or out.dtype != x.dtype or out.shape != x.shape:
+        _invalid(fn, "x and out must be [rows, heads, head_dim] of one of bf16, fp16, fp32 (got %s %s and %s %s)" %
+                 (x.dtype, list(x.shape), out.dtype, list(out.shape)))
+    rows, heads, dim = x.shape
+    rot_dim = dim if rot_dim is None else int(rot_dim)
+    xs, ys = x.stride(), out.stride()
+    if dim > 1 and (xs[2] != 1 or ys[2] != 1):
+        _invalid(fn, "the last dimension of x and out must have stride 1")
+    _dense(fn, "pos", pos, torch.int32, rows)
+    _dense(fn, "rope_cs", rope_cs, torch.float32, None, rot_dim // 2, 2)
+    _check(_lib.gw_rope_rows(_ptr(x), xs[0], xs[1], _ptr(out), ys[0], ys[1], ELEMS[x.dtype], rows, heads, dim, rot_dim,
+                             PAIRS_INTERLEAVED if interleaved else PAIRS_HALF, 1 if inverse else 0, _ptr(pos),
+                             _ptr(rope_cs), int(rope_cs.shape[0]), _ptr(dev_status), _stream(stream)))
     return out
 
 

@@ -408,6 +408,45 @@ gw_status gw_decode_attn_global_lse(const gw_kv_pool* pool, const void* q, void*
                                     void* stream);
 
 /*
+ * gw_decode_attn_global_acc - gw_decode_attn_global for decode rows
+ * (max_q_rows 1) that also adds up how much attention each cached token gets:
+ *
+ *   w[h][j]   = exp(scale * q_h . K_j - lse_h)         (the softmax weights)
+ *   acc[b][j] = decay * acc[b][j] + sum_h w[h][j]      for j in [0, seq_lens[b])
+ *
+ * The sum over steps (and, with decay < 1, its fading form) is what
+ * gw_kv_evict_select ranks tokens by.  Weights, their normaliser and acc are
+ * float32 and the heads are added in a fixed order, so results do not depend
+ * on the batch.  Sequences without exactly one row, or of invalid length,
+ * keep their acc row; so does every acc[b][j] with j >= seq_lens[b].  With
+ * decay 0 the old values are not read (they may be anything).
+ *
+ *   acc        float32 [batch][acc_stride], 4-byte aligned, caller-owned;
+ *              acc_stride >= max_pages_per_seq * 16.  A token's entry is 0
+ *              before the step that appends it.
+ *   lse        float32 [total_rows][num_q_heads] as in
+ *              gw_decode_attn_global_lse, or NULL.
+ *   decay      finite, >= 0 (1: plain sum).
+ *   workspace  at least gw_attn_acc_workspace_bytes(...): the logits of the
+ *              step, float32 [batch][max_pages_per_seq * 16][num_q_heads],
+ *              beside the split-KV partials.
+ * The rows of one sequence may be asked for by several batch entries with the
+ * same block-table row (say, the last rows of a prompt, each with its own
+ * seq_len); each entry has its own acc row.
+ * Errors: those of gw_decode_attn_global; GW_ERR_INVALID_ARG for acc NULL or
+ * misaligned, lse misaligned, acc_stride or decay out of range.
+ */
+gw_status gw_decode_attn_global_acc(const gw_kv_pool* pool, const void* q, void* out, float* lse, float* acc,
+                                    int64_t acc_stride, float decay, int32_t num_q_heads, int32_t batch,
+                                    const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                                    int32_t max_pages_per_seq, float scale, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/* Workspace bytes of gw_decode_attn_global_acc; 0 on an invalid description. */
+size_t gw_attn_acc_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch,
+                                   int32_t max_pages_per_seq);
+
+/*
  * gw_merge_lse - merge n_parts attention results of the same rows computed
  * over disjoint key sets (the ranks of a context-parallel split), by their
  * log-sum-exp:

@@ -235,9 +235,24 @@ __device__ __noinline__ void append_unit_row(const LocalArgs& a, const int32_t* 
   if (lane == 0) st_release_shared(app_done, j + 1);
 }
 
-// kApp: the fused-append variant (a kernel of its own, so that the plain
-// call's code is unchanged).
-template <int LAYOUT, int HQ, bool kApp>
+// Stores the HQ logits of one token, 32 bytes at a time: the softmax's lanes
+// hold a token each, so a wider store fills whole sectors.
+template <int HQ>
+__device__ __forceinline__ void store_logits(float* dst, const float (&s)[HQ]) {
+#pragma unroll
+  for (int h = 0; h < HQ; h += 8)
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + h), "f"(s[h]), "f"(s[h + 1]),
+                 "f"(s[h + 2]), "f"(s[h + 3]), "f"(s[h + 4]), "f"(s[h + 5]), "f"(s[h + 6]), "f"(s[h + 7])
+                 : "memory");
+}
+
+// kApp: the fused-append variant; kAcc: the variant of
+// gw_decode_attn_global_acc, which stores every token's logits for the pass
+// that turns them into weights and sums the softmax's unrounded weights, since
+// that pass is held to float32 (the plain call sums the weights as rounded for
+// P.V, so that numerator and denominator round alike).  Each is a kernel of
+// its own, so that the plain call's code is unchanged.
+template <int LAYOUT, int HQ, bool kApp, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalArgs a) {
   using T = GTraits<LAYOUT>;
   using SM = GSmem<LAYOUT, HQ>;
@@ -676,6 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
         s[h] = valid ? __uint_as_float(r[h]) * sc : -INFINITY;
         need |= s[h] > m_run[h] + kLazyThreshold;
       }
+      if (kAcc && active && tabs < d.L)
+        store_logits<HQ>(a.score + (static_cast<int64_t>(d.s) * a.max_pages * kPage + tabs) * HQ, s);
       // A thread asking for a new max tags the flag of this tile's parity
       // with the tile; the other parity's flag may meanwhile be written for
       // the next tile (whose QK^T can complete before this softmax ends), and
@@ -749,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
               const __nv_fp8x2_storage_t lo2 =
                   __nv_cvt_float2_to_fp8x2(make_float2(p0 - hf.x, p1 - hf.y), __NV_SATFINITE, __NV_E4M3);
               const float2 lf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(lo2, __NV_E4M3)));
-              if (h0 < HQ) l_acc[i0] += hf.x + lf.x;
-              if (h0 + 1 < HQ) l_acc[i1] += hf.y + lf.y;
+              if (h0 < HQ) l_acc[i0] += kAcc ? p0 : hf.x + lf.x;
+              if (h0 + 1 < HQ) l_acc[i1] += kAcc ? p1 : hf.y + lf.y;
               hw |= static_cast<uint32_t>(hi2) << (16 * jj);
               lw |= static_cast<uint32_t>(lo2) << (16 * jj);
             }
@@ -775,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
             const float p0 = valid ? ex2(s[h0] - m_run[h0]) : 0.f;
             const float p1 = valid ? ex2(s[h0 + 1] - m_run[h0 + 1]) : 0.f;
             __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            l_acc[h0] += __low2float(pb);
-            l_acc[h0 + 1] += __high2float(pb);
+            l_acc[h0] += kAcc ? p0 : __low2float(pb);
+            l_acc[h0 + 1] += kAcc ? p1 : __high2float(pb);
             w[k] = *reinterpret_cast<uint32_t*>(&pb);
           }
           *reinterpret_cast<uint4*>(pdst + hb * 128) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -834,7 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
 
 template <int LAYOUT, int HQ>
 cudaError_t launch_layout(const LocalArgs& a, cudaStream_t stream) {
-  auto kern = a.k_new ? global_decode_kernel<LAYOUT, HQ, true> : global_decode_kernel<LAYOUT, HQ, false>;
+  auto kern = a.score   ? global_decode_kernel<LAYOUT, HQ, false, true>
+              : a.k_new ? global_decode_kernel<LAYOUT, HQ, true, false>
+                        : global_decode_kernel<LAYOUT, HQ, false, false>;
   const size_t smem = sizeof(GSmem<LAYOUT, HQ>);
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;

@@ -316,6 +316,40 @@ size_t gw_attn_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int3
       .total;
 }
 
+// Layout of a gw_decode_attn_global_acc workspace behind the attention's own:
+// the softmax statistics, then the logits.
+struct AccLayout {
+  size_t stat, score, total;
+};
+
+static AccLayout acc_layout(const WsLayout& w, int num_q_heads, int batch, int max_pages) {
+  AccLayout l{};
+  l.stat = round_up(w.total, 256);
+  l.score = l.stat + round_up(static_cast<size_t>(batch) * num_q_heads * 8, 256);
+  l.total = l.score + round_up(static_cast<size_t>(batch) * max_pages * 16 * num_q_heads * 4, 256);
+  return l;
+}
+
+size_t gw_attn_acc_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch,
+                                   int32_t max_pages_per_seq) {
+  const char* fn = "gw_attn_acc_workspace_bytes";
+  if (check_pool(pool, fn, false) != GW_OK) return 0;
+  if (pool->layout == GW_LAYOUT_LOCAL || num_q_heads < 1 || batch < 0 || max_pages_per_seq < 1 ||
+      max_pages_per_seq > 0x7fffffff / 16) {
+    fail(GW_ERR_INVALID_ARG, fn, "needs a global pool, num_q_heads >= 1, batch >= 0 and max_pages_per_seq in [1, 2^27)");
+    return 0;
+  }
+  const WsLayout w = ws_layout(pool->layout, pool->dtype, 1, num_q_heads, batch, max_pages_per_seq * 16, 0);
+  return acc_layout(w, num_q_heads, batch, max_pages_per_seq).total;
+}
+
+// What gw_decode_attn_global_acc adds to its attention call.
+struct AccOut {
+  float* acc;
+  int64_t stride;
+  float decay;
+};
+
 // The step's K/V rows of a gw_append_decode_attn_* call.
 struct FusedAppend {
   const void* k;
@@ -329,7 +363,7 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
                              const int32_t* block_table, int32_t max_pages_per_seq, int32_t max_q_rows,
                              int32_t window, float scale, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, void* stream, bool validate_only = false,
-                             float* lse = nullptr, const FusedAppend* app = nullptr) {
+                             float* lse = nullptr, const FusedAppend* app = nullptr, const AccOut* acc = nullptr) {
   g_err[0] = 0;
   gw_status s = check_pool(pool, fn);
   if (s != GW_OK) return s;
@@ -371,8 +405,22 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
   const int max_len = max_len64 > 0x7fffffff ? 0x7fffffff : static_cast<int>(max_len64);
   const WsLayout w = ws_layout(pool->layout, pool->dtype, pool->kv_heads, num_q_heads, batch, max_len,
                                local ? window : 0);
-  if (workspace_bytes < w.total)
-    return fail(GW_ERR_WORKSPACE, fn, "workspace_bytes %zu < %zu needed", workspace_bytes, w.total);
+  size_t ws_need = w.total;
+  AccLayout al{};
+  if (acc) {
+    if (!acc->acc || !aligned(acc->acc, 4)) return fail(GW_ERR_INVALID_ARG, fn, "acc NULL or misaligned");
+    if (lse && !aligned(lse, 4)) return fail(GW_ERR_INVALID_ARG, fn, "lse misaligned");
+    if (max_pages_per_seq > 0x7fffffff / 16) return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be < 2^27");
+    if (acc->stride < max_len64)
+      return fail(GW_ERR_INVALID_ARG, fn, "acc_stride %lld below max_pages_per_seq * 16 = %lld",
+                  static_cast<long long>(acc->stride), static_cast<long long>(max_len64));
+    if (!(acc->decay >= 0.f) || !std::isfinite(acc->decay))
+      return fail(GW_ERR_INVALID_ARG, fn, "decay must be finite and >= 0");
+    al = acc_layout(w, num_q_heads, batch, max_pages_per_seq);
+    ws_need = al.total;
+  }
+  if (workspace_bytes < ws_need)
+    return fail(GW_ERR_WORKSPACE, fn, "workspace_bytes %zu < %zu needed", workspace_bytes, ws_need);
   if (validate_only) return GW_OK;
 
   LocalArgs a{};
@@ -404,6 +452,13 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
     a.rope_cs = app->rope_cs;
     a.max_pos = app->max_pos;
   }
+  if (acc) {
+    a.score = reinterpret_cast<float*>(ws + al.score);
+    a.stat = reinterpret_cast<float2*>(ws + al.stat);
+    a.acc = acc->acc;
+    a.acc_stride = acc->stride;
+    a.decay = acc->decay;
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (local) {
@@ -412,6 +467,7 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
   } else {
     e = launch_global_decode(pool->layout, a, st);
     if (e == cudaSuccess && max_q_rows > 1) e = launch_global_prompt(pool->layout, a, max_q_rows, st);
+    if (e == cudaSuccess && acc) e = launch_attn_acc(a, st);
   }
   return cuda_status(e, fn);
 }
@@ -484,6 +540,17 @@ gw_status gw_decode_attn_global_lse(const gw_kv_pool* pool, const void* q, void*
   }
   return attn_common(fn, false, pool, q, out, num_q_heads, batch, cu_q_rows, seq_lens, block_table,
                      max_pages_per_seq, 1, 0, scale, workspace, workspace_bytes, dev_status, stream, false, lse);
+}
+
+gw_status gw_decode_attn_global_acc(const gw_kv_pool* pool, const void* q, void* out, float* lse, float* acc,
+                                    int64_t acc_stride, float decay, int32_t num_q_heads, int32_t batch,
+                                    const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                                    int32_t max_pages_per_seq, float scale, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, void* stream) {
+  const AccOut ao{acc, acc_stride, decay};
+  return attn_common("gw_decode_attn_global_acc", false, pool, q, out, num_q_heads, batch, cu_q_rows, seq_lens,
+                     block_table, max_pages_per_seq, 1, 0, scale, workspace, workspace_bytes, dev_status, stream, false,
+                     lse, nullptr, &ao);
 }
 
 gw_status gw_merge_lse(int32_t n_parts, const void* const* o_parts, const float* const* lse_parts, void* out,

@@ -101,6 +101,12 @@ struct LocalArgs {
   const float* rope_cs;
   int32_t max_pos;
   int32_t early_inputs;  // gw_set_early_inputs: plan before the wait on the previous kernel
+  // Attention weights (gw_decode_attn_global_acc); score null: none.
+  float* score;    // [batch][max_pages * 16][num_q_heads], logits in base-2 units
+  float2* stat;    // [batch][num_q_heads]: {max logit, 1 / sum} of the row's softmax
+  float* acc;      // [batch][acc_stride]
+  int64_t acc_stride;
+  float decay;
 };
 
 struct AppendArgs {
@@ -146,6 +152,10 @@ gw_status set_error(gw_status code, const char* fn, const char* fmt, ...);
 // dropped unwritten.
 cudaError_t launch_combine(const LocalArgs& a, int heads_per_unit, int head_dim, int max_chunks, bool discard,
                            cudaStream_t st);
+
+// acc = decay * acc + each token's softmax weights summed over the heads, from
+// a.score and a.stat (after launch_combine).
+cudaError_t launch_attn_acc(const LocalArgs& a, cudaStream_t st);
 
 cudaError_t launch_append(int layout, int dtype, const AppendArgs& a, cudaStream_t st);
 

@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(256, 2) combine_kernel(const LocalArgs a, int 
   *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(row0) * a.num_q_heads + h) * D + dim0) = w;
   // log-sum-exp of the row's logits, natural log (the partials are in base-2
   // units of the scaled logits): ln(sum_j e^{scale q.k_j}) = ln2 (M + log2 den)
+  if (a.stat && slice == 0 && lane == 0) a.stat[static_cast<int64_t>(s) * a.num_q_heads + h] = make_float2(M, inv);
   if (a.lse && slice == 0 && lane == 0)
     a.lse[static_cast<int64_t>(row0) * a.num_q_heads + h] = den > 0.f ? 0.6931471805599453f * (M + log2f(den)) : -INFINITY;
 }

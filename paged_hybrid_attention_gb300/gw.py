@@ -33,7 +33,8 @@ EXPORTS = ["gw_pool_page_bytes", "gw_kv_append", "gw_decode_attn_local", "gw_dec
            "gw_noalloc_scratch_bytes", "gw_bw_probe", "gw_set_max_ctas", "gw_set_early_launch",
            "gw_set_early_inputs", "gw_rope_cs", "gw_wait_selftest", "gw_bw_probe_tma",
            "gw_decode_attn_global_lse", "gw_merge_lse", "gw_append_decode_attn_local",
-           "gw_append_decode_attn_global", "gw_rope_rows", "gw_rope_cs_scaled"]
+           "gw_append_decode_attn_global", "gw_rope_rows", "gw_rope_cs_scaled",
+           "gw_decode_attn_global_acc", "gw_attn_acc_workspace_bytes"]
 
 
 ELEMS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -80,6 +81,11 @@ _lib.gw_decode_attn_global.restype = _i32
 _lib.gw_decode_attn_global_lse.argtypes = [_P, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _sz,
                                            _vp, _vp]
 _lib.gw_decode_attn_global_lse.restype = _i32
+_lib.gw_decode_attn_global_acc.argtypes = [_P, _vp, _vp, _vp, _vp, _i64, _f32, _i32, _i32, _vp, _vp, _vp, _i32, _f32,
+                                           _vp, _sz, _vp, _vp]
+_lib.gw_decode_attn_global_acc.restype = _i32
+_lib.gw_attn_acc_workspace_bytes.argtypes = [_P, _i32, _i32, _i32]
+_lib.gw_attn_acc_workspace_bytes.restype = _sz
 _lib.gw_merge_lse.argtypes = [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
 _lib.gw_merge_lse.restype = _i32
 _lib.gw_rope_cs.argtypes = [_vp, ctypes.c_double, _i32, _i32, _i32, _vp]
@@ -322,6 +328,46 @@ def decode_attn_global_lse(pool, q, out, lse, cu_q_rows, seq_lens, block_table, 
     scale = 1.0 / math.sqrt(512) if scale is None else scale
     _check(_lib.gw_decode_attn_global_lse(ctypes.byref(pool.desc), _ptr(q), _ptr(out), _ptr(lse), hq,
                                           int(seq_lens.numel()), _ptr(cu_q_rows), _ptr(seq_lens), _ptr(block_table),
+                                          int(block_table.shape[1]), float(scale), _ptr(workspace),
+                                          int(workspace.numel()), _ptr(dev_status), _stream(stream)))
+
+
+def alloc_workspace_acc(pool, num_q_heads, batch, max_pages_per_seq, device="cuda"):
+    """The workspace of decode_attn_global_acc calls of at most this size."""
+    n = _lib.gw_attn_acc_workspace_bytes(ctypes.byref(pool.desc), num_q_heads, batch, max_pages_per_seq)
+    if n == 0:
+        raise GwError(GW_ERR_INVALID_ARG, last_error() or "invalid workspace request")
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def decode_attn_global_acc(pool, q, out, lse, acc, cu_q_rows, seq_lens, block_table, workspace, decay=1.0, scale=None,
+                           dev_status=None, stream=None):
+    """gw_decode_attn_global_acc: decode rows, each row's log-sum-exp (lse
+    float32 [rows, heads] or None), and acc [batch, stride] = decay * acc +
+    each cached token's softmax weights summed over the heads."""
+    fn = "gw_decode_attn_global_acc"
+    _on_device(fn, stream, pool.data, q, out, lse, acc, cu_q_rows, seq_lens, block_table, workspace, dev_status)
+    batch = int(seq_lens.shape[0])
+    _dense(fn, "q", q, torch.bfloat16, None, None, 512)
+    rows, hq = int(q.shape[0]), int(q.shape[1])
+    _dense(fn, "out", out, torch.bfloat16, rows, hq, 512)
+    if lse is not None:
+        _dense(fn, "lse", lse, torch.float32, rows, hq)
+    if acc.dtype != torch.float32 or acc.dim() != 2 or acc.shape[0] != batch or (acc.shape[1] > 1 and
+                                                                                   acc.stride(1) != 1):
+        _invalid(fn, "acc must be float32 [%d, stride], its last stride 1 (got %s %s)" % (batch, acc.dtype,
+                                                                                         list(acc.shape)))
+    _dense(fn, "cu_q_rows", cu_q_rows, torch.int32, batch + 1)
+    _dense(fn, "seq_lens", seq_lens, torch.int32, batch)
+    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    if acc.shape[1] < 16 * block_table.shape[1]:
+        _invalid(fn, "acc has %d columns, the block table names %d tokens" % (acc.shape[1], 16 * block_table.shape[1]))
+    scale = 1.0 / math.sqrt(512) if scale is None else scale
+    stride = int(acc.stride(0)) if batch > 1 else int(acc.shape[1])
+    _check(_lib.gw_decode_attn_global_acc(ctypes.byref(pool.desc), _ptr(q), _ptr(out), _ptr(lse), _ptr(acc), stride,
+                                          float(decay), hq, batch, _ptr(cu_q_rows), _ptr(seq_lens), _ptr(block_table),
                                           int(block_table.shape[1]), float(scale), _ptr(workspace),
                                           int(workspace.numel()), _ptr(dev_status), _stream(stream)))
 

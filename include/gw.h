@@ -73,6 +73,9 @@ typedef int32_t gw_status;
 #define GW_DEV_TIMEOUT 16    /* a bounded wait gave up (work abandoned)       */
 #define GW_DEV_WORKSPACE 32  /* the step needs more split-KV partials than the
                                 workspace was sized for (nothing computed)    */
+#define GW_DEV_KEEP_RANGE 64 /* keep_idx not ascending or outside [0, seq_len),
+                                or keep_lens outside [0, min(keep_stride,
+                                seq_len)]                                     */
 
 /* ---- pool description --------------------------------------------------- */
 #define GW_KV_BF16 0
@@ -445,6 +448,86 @@ gw_status gw_decode_attn_global_acc(const gw_kv_pool* pool, const void* q, void*
 /* Workspace bytes of gw_decode_attn_global_acc; 0 on an invalid description. */
 size_t gw_attn_acc_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch,
                                    int32_t max_pages_per_seq);
+
+/* ---- eviction from a global cache ----------------------------------------
+ * Global layers keep every token, so their cache grows with the sequence.
+ * These two calls cut a sequence to the tokens that matter: by the attention
+ * that each has drawn (gw_decode_attn_global_acc), the first and the newest
+ * kept in any case.  A step then reads
+ *
+ *   gw_kv_evict_select(acc, ..., seq_lens, ..., keep_idx, keep_lens)
+ *   gw_kv_evict_compact(pool, ..., seq_lens, keep_idx, keep_lens, acc, ...)
+ *
+ * after which keep_lens holds the sequences' lengths in the cache.  Kept
+ * tokens keep their order and their rotation; a later token is appended with
+ * gw_kv_append at slot keep_len and its true position (gw_append_decode_attn_*
+ * takes the position from the length, so it is for caches without eviction).
+ * A layer's tokens are its own: each global layer is evicted by its own acc.
+ */
+
+/*
+ * gw_kv_evict_select - choose the tokens that each sequence keeps.
+ *
+ * Sequence b of length L = seq_lens[b] keeps all L tokens if L <= budget.
+ * Otherwise it keeps `budget`: the first `sinks`, the last `recent`, and of
+ * those between the budget - sinks - recent with the largest acc[b][j]; of
+ * equal values those with the lowest index (-0 equals 0; NaN ranks below
+ * everything, -inf included, and NaNs are equal).
+ *
+ *   acc        float32 [batch][acc_stride], 4-byte aligned.
+ *   seq_lens   int32 [batch]; outside [0, acc_stride]: GW_DEV_LEN_RANGE, and
+ *              the sequence gets keep_lens 0.
+ *   keep_idx   int32 [batch][keep_stride], keep_stride >= budget: the kept
+ *              tokens' indices, ascending; entries from keep_lens[b] on are
+ *              left as they were.
+ *   keep_lens  int32 [batch].
+ *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget;
+ *   batch 0 is a no-op.
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch, const int32_t* seq_lens,
+                             int32_t budget, int32_t sinks, int32_t recent, int32_t* keep_idx, int64_t keep_stride,
+                             int32_t* keep_lens, int32_t* dev_status, void* stream);
+
+/*
+ * gw_kv_evict_compact - move each sequence's kept tokens to the front.
+ *
+ * For sequence b and i in [0, keep_lens[b]): the row of token keep_idx[b][i]
+ * (in page block_table[b][keep_idx / 16]) is copied to token i, bytes as they
+ * are.  Global pools of every layout.
+ *
+ *   dst_block_table  NULL: token i lies in the same pages (in place; the
+ *              sequence's pages from ceil(keep_lens[b] / 16) on are then free,
+ *              and hold what they held).  A sequence's pages must be its own:
+ *              a page of two sequences is a race.  Otherwise int32
+ *              [batch][dst_max_pages], where token i lies in page
+ *              dst_block_table[b][i / 16]: pages that no sequence of the call
+ *              reads, or the sequence's own page of the same number (so pages
+ *              shared with another sequence can be left behind).
+ *   acc        NULL, or float32 [batch][acc_stride], acc_stride >=
+ *              max_pages_per_seq * 16: moves along in place, and
+ *              acc[b][keep_lens[b] .. seq_lens[b]) becomes 0, as a token
+ *              appended there expects.
+ *   keep_idx   as gw_kv_evict_select writes it (or any ascending choice).  An
+ *              entry that is not above the one before it, or outside
+ *              [0, seq_lens[b]), is skipped (GW_DEV_KEEP_RANGE); so is its
+ *              acc.  A sequence whose length is outside
+ *              [0, max_pages_per_seq * 16] (GW_DEV_LEN_RANGE), or whose
+ *              keep_lens is outside [0, min(keep_stride, seq_lens[b])] or needs
+ *              more than dst_max_pages pages (GW_DEV_KEEP_RANGE), is left as
+ *              it was.
+ *   A row whose source or destination page is outside [0, num_pages) is not
+ *   moved (GW_DEV_PAGE_RANGE).
+ *   batch in [0, 65535]; 0 is a no-op.  seq_lens and keep_lens must not be
+ *   the same array.
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED (a LOCAL pool: its window
+ * evicts), GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_kv_evict_compact(const gw_kv_pool* pool, int32_t batch, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* keep_idx,
+                              int64_t keep_stride, const int32_t* keep_lens, const int32_t* dst_block_table,
+                              int32_t dst_max_pages, float* acc, int64_t acc_stride, int32_t* dev_status,
+                              void* stream);
 
 /*
  * gw_merge_lse - merge n_parts attention results of the same rows computed

@@ -25,6 +25,9 @@ gw_status fail(gw_status code, const char* fn, const char* fmt, ...) {
   return code;
 }
 
+// Bound on the strides that callers give (elements): offsets stay in 64 bits.
+constexpr int64_t kMaxRowStride = int64_t{1} << 40;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -218,9 +221,8 @@ gw_status gw_rope_rows(const void* x, int64_t x_row_stride, int64_t x_head_strid
   if (!pos || !aligned(pos, 4)) return fail(GW_ERR_INVALID_ARG, fn, "pos NULL or misaligned");
   if (!rope_cs || !aligned(rope_cs, 16)) return fail(GW_ERR_INVALID_ARG, fn, "rope_cs NULL or not 16-byte aligned");
   if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
-  constexpr int64_t kMaxStride = int64_t{1} << 40;  // extents below stay within 64 bits
-  if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0 || x_row_stride > kMaxStride ||
-      x_head_stride > kMaxStride || y_row_stride > kMaxStride || y_head_stride > kMaxStride)
+  if (x_row_stride < 0 || x_head_stride < 0 || y_row_stride < 0 || y_head_stride < 0 || x_row_stride > kMaxRowStride ||
+      x_head_stride > kMaxRowStride || y_row_stride > kMaxRowStride || y_head_stride > kMaxRowStride)
     return fail(GW_ERR_INVALID_ARG, fn, "a stride is negative or above 2^40");
   using wide = unsigned __int128;
   const wide rows1 = num_rows - 1, heads1 = num_heads - 1, dim = head_dim;
@@ -551,6 +553,80 @@ gw_status gw_decode_attn_global_acc(const gw_kv_pool* pool, const void* q, void*
   return attn_common("gw_decode_attn_global_acc", false, pool, q, out, num_q_heads, batch, cu_q_rows, seq_lens,
                      block_table, max_pages_per_seq, 1, 0, scale, workspace, workspace_bytes, dev_status, stream, false,
                      lse, nullptr, &ao);
+}
+
+gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch, const int32_t* seq_lens,
+                             int32_t budget, int32_t sinks, int32_t recent, int32_t* keep_idx, int64_t keep_stride,
+                             int32_t* keep_lens, int32_t* dev_status, void* stream) {
+  const char* fn = "gw_kv_evict_select";
+  g_err[0] = 0;
+  if (batch < 0 || batch > 65535) return fail(GW_ERR_INVALID_ARG, fn, "batch (%d) outside [0, 65535]", batch);
+  if (budget < 1 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > budget)
+    return fail(GW_ERR_INVALID_ARG, fn, "need budget >= 1, sinks >= 0, recent >= 0 and sinks + recent <= budget (%d, %d, %d)",
+                budget, sinks, recent);
+  if (acc_stride < 1 || acc_stride > kMaxRowStride || keep_stride < budget || keep_stride > kMaxRowStride)
+    return fail(GW_ERR_INVALID_ARG, fn, "acc_stride < 1, keep_stride < budget, or one above 2^40");
+  if (batch == 0) return GW_OK;
+  if (!acc || !aligned(acc, 4)) return fail(GW_ERR_INVALID_ARG, fn, "acc NULL or misaligned");
+  if (!seq_lens || !keep_idx || !keep_lens || !aligned(seq_lens, 4) || !aligned(keep_idx, 4) || !aligned(keep_lens, 4))
+    return fail(GW_ERR_INVALID_ARG, fn, "seq_lens/keep_idx/keep_lens NULL or misaligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  SelectArgs a{};
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.batch = batch;
+  a.seq_lens = seq_lens;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.keep_idx = keep_idx;
+  a.keep_stride = keep_stride;
+  a.keep_lens = keep_lens;
+  a.status = dev_status;
+  return cuda_status(launch_evict_select(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+gw_status gw_kv_evict_compact(const gw_kv_pool* pool, int32_t batch, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* keep_idx,
+                              int64_t keep_stride, const int32_t* keep_lens, const int32_t* dst_block_table,
+                              int32_t dst_max_pages, float* acc, int64_t acc_stride, int32_t* dev_status,
+                              void* stream) {
+  const char* fn = "gw_kv_evict_compact";
+  g_err[0] = 0;
+  gw_status s = check_pool(pool, fn);
+  if (s != GW_OK) return s;
+  if (pool->layout == GW_LAYOUT_LOCAL)
+    return fail(GW_ERR_UNSUPPORTED, fn, "a LOCAL pool: sliding-window layers evict by their window");
+  if (batch < 0 || batch > 65535) return fail(GW_ERR_INVALID_ARG, fn, "batch (%d) outside [0, 65535]", batch);
+  if (max_pages_per_seq < 1 || max_pages_per_seq > 0x7fffffff / 16)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be in [1, 2^27)");
+  if (dst_block_table && (dst_max_pages < 1 || dst_max_pages > 0x7fffffff / 16))
+    return fail(GW_ERR_INVALID_ARG, fn, "dst_max_pages must be in [1, 2^27)");
+  if (keep_stride < 1 || keep_stride > kMaxRowStride) return fail(GW_ERR_INVALID_ARG, fn, "keep_stride < 1 or above 2^40");
+  if (acc && (!aligned(acc, 4) || acc_stride < static_cast<int64_t>(max_pages_per_seq) * 16 || acc_stride > kMaxRowStride))
+    return fail(GW_ERR_INVALID_ARG, fn, "acc misaligned, or acc_stride below max_pages_per_seq * 16 or above 2^40");
+  if (batch == 0) return GW_OK;
+  if (!block_table || !seq_lens || !keep_idx || !keep_lens || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(keep_idx, 4) || !aligned(keep_lens, 4) || !aligned(dst_block_table, 4))
+    return fail(GW_ERR_INVALID_ARG, fn, "block_table/seq_lens/keep_idx/keep_lens NULL or misaligned");
+  if (seq_lens == keep_lens) return fail(GW_ERR_INVALID_ARG, fn, "seq_lens and keep_lens are the same array");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  CompactArgs a{};
+  a.pool = static_cast<uint8_t*>(pool->base);
+  a.num_pages = pool->num_pages;
+  a.batch = batch;
+  a.block_table = block_table;
+  a.max_pages = max_pages_per_seq;
+  a.seq_lens = seq_lens;
+  a.keep_idx = keep_idx;
+  a.keep_stride = keep_stride;
+  a.keep_lens = keep_lens;
+  a.dst_table = dst_block_table ? dst_block_table : block_table;
+  a.dst_max_pages = dst_block_table ? dst_max_pages : max_pages_per_seq;
+  a.acc = acc;
+  a.acc_stride = acc_stride;
+  a.status = dev_status;
+  return cuda_status(launch_evict_compact(pool->layout, a, static_cast<cudaStream_t>(stream)), fn);
 }
 
 gw_status gw_merge_lse(int32_t n_parts, const void* const* o_parts, const float* const* lse_parts, void* out,

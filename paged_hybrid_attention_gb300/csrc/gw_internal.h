@@ -193,6 +193,37 @@ struct RopeFreqs {
 };
 cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amplitude, int half, int max_pos,
                                   cudaStream_t st);
+// gw_kv_evict_select
+struct SelectArgs {
+  const float* acc;
+  int64_t acc_stride;
+  int32_t batch;
+  const int32_t* seq_lens;
+  int32_t budget, sinks, recent;
+  int32_t* keep_idx;
+  int64_t keep_stride;
+  int32_t* keep_lens;
+  int32_t* status;
+};
+cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t st);
+// gw_kv_evict_compact
+struct CompactArgs {
+  uint8_t* pool;
+  int64_t num_pages;
+  int32_t batch;
+  const int32_t* block_table;
+  int32_t max_pages;
+  const int32_t* seq_lens;
+  const int32_t* keep_idx;
+  int64_t keep_stride;
+  const int32_t* keep_lens;
+  const int32_t* dst_table;  // == block_table in place
+  int32_t dst_max_pages;
+  float* acc;
+  int64_t acc_stride;
+  int32_t* status;
+};
+cudaError_t launch_evict_compact(int layout, const CompactArgs& a, cudaStream_t st);
 cudaError_t launch_bw_probe(const void* buf, int64_t chunks, int32_t* status, cudaStream_t st);
 cudaError_t launch_bw_probe_tma(const void* buf, int64_t pages, int32_t* status, cudaStream_t st);
 cudaError_t launch_wait_selftest(int32_t* status, int32_t* result, int64_t limit_ns, cudaStream_t st);

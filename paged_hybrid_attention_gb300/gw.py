@@ -22,7 +22,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ---- constants (mirror include/gw.h) -----------------------------------------
 GW_OK, GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED, GW_ERR_WORKSPACE, GW_ERR_CUDA = 0, 1, 2, 3, 4
 GW_DEV_SLOT_RANGE, GW_DEV_POS_RANGE, GW_DEV_PAGE_RANGE, GW_DEV_LEN_RANGE = 1, 2, 4, 8
-GW_DEV_TIMEOUT, GW_DEV_WORKSPACE = 16, 32
+GW_DEV_TIMEOUT, GW_DEV_WORKSPACE, GW_DEV_KEEP_RANGE = 16, 32, 64
 KV_BF16, KV_E4M3 = 0, 1
 LAYOUT_LOCAL, LAYOUT_GLOBAL_FOLDED, LAYOUT_GLOBAL_FULL, LAYOUT_GLOBAL_FOLDED_E4M3 = 0, 1, 2, 3
 LAYOUTS = {"local": LAYOUT_LOCAL, "folded": LAYOUT_GLOBAL_FOLDED, "full": LAYOUT_GLOBAL_FULL,
@@ -34,7 +34,7 @@ EXPORTS = ["gw_pool_page_bytes", "gw_kv_append", "gw_decode_attn_local", "gw_dec
            "gw_set_early_inputs", "gw_rope_cs", "gw_wait_selftest", "gw_bw_probe_tma",
            "gw_decode_attn_global_lse", "gw_merge_lse", "gw_append_decode_attn_local",
            "gw_append_decode_attn_global", "gw_rope_rows", "gw_rope_cs_scaled",
-           "gw_decode_attn_global_acc", "gw_attn_acc_workspace_bytes"]
+           "gw_decode_attn_global_acc", "gw_attn_acc_workspace_bytes", "gw_kv_evict_select", "gw_kv_evict_compact"]
 
 
 ELEMS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -86,6 +86,10 @@ _lib.gw_decode_attn_global_acc.argtypes = [_P, _vp, _vp, _vp, _vp, _i64, _f32, _
 _lib.gw_decode_attn_global_acc.restype = _i32
 _lib.gw_attn_acc_workspace_bytes.argtypes = [_P, _i32, _i32, _i32]
 _lib.gw_attn_acc_workspace_bytes.restype = _sz
+_lib.gw_kv_evict_select.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp, _i64, _vp, _vp, _vp]
+_lib.gw_kv_evict_select.restype = _i32
+_lib.gw_kv_evict_compact.argtypes = [_P, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
+_lib.gw_kv_evict_compact.restype = _i32
 _lib.gw_merge_lse.argtypes = [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
 _lib.gw_merge_lse.restype = _i32
 _lib.gw_rope_cs.argtypes = [_vp, ctypes.c_double, _i32, _i32, _i32, _vp]
@@ -173,6 +177,21 @@ def _dense(fn, name, t, dtype, *shape):
         _invalid(fn, "%s must be %s of shape %s (got %s %s)" % (name, dtype, list(shape), t.dtype, list(t.shape)))
     if not t.is_contiguous():
         _invalid(fn, "%s must be contiguous" % name)
+
+
+def _row_stride(fn, name, t, dtype, rows):
+    """The row stride of `t`, [rows, columns] of this dtype whose columns are
+    adjacent and whose rows do not overlap; each row, the last one too, has
+    the stride's length of memory behind it."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows:
+        _invalid(fn, "%s must be %s [%d, columns] (got %s %s)" % (name, dtype, rows, t.dtype, list(t.shape)))
+    cols = int(t.shape[1])
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        _invalid(fn, "%s must have adjacent columns and rows that do not overlap" % name)
+    stride = int(t.stride(0)) if rows > 1 else cols
+    if stride > cols and t.storage_offset() + rows * stride > t.untyped_storage().nbytes() // t.element_size():
+        _invalid(fn, "%s: the last row ends before its stride" % name)
+    return stride
 
 
 # ---- pools ---------------------------------------------------------------------
@@ -355,21 +374,61 @@ def decode_attn_global_acc(pool, q, out, lse, acc, cu_q_rows, seq_lens, block_ta
     _dense(fn, "out", out, torch.bfloat16, rows, hq, 512)
     if lse is not None:
         _dense(fn, "lse", lse, torch.float32, rows, hq)
-    if acc.dtype != torch.float32 or acc.dim() != 2 or acc.shape[0] != batch or (acc.shape[1] > 1 and
-                                                                                   acc.stride(1) != 1):
-        _invalid(fn, "acc must be float32 [%d, stride], its last stride 1 (got %s %s)" % (batch, acc.dtype,
-                                                                                         list(acc.shape)))
+    stride = _row_stride(fn, "acc", acc, torch.float32, batch)
     _dense(fn, "cu_q_rows", cu_q_rows, torch.int32, batch + 1)
     _dense(fn, "seq_lens", seq_lens, torch.int32, batch)
     _dense(fn, "block_table", block_table, torch.int32, batch, None)
     if acc.shape[1] < 16 * block_table.shape[1]:
         _invalid(fn, "acc has %d columns, the block table names %d tokens" % (acc.shape[1], 16 * block_table.shape[1]))
     scale = 1.0 / math.sqrt(512) if scale is None else scale
-    stride = int(acc.stride(0)) if batch > 1 else int(acc.shape[1])
     _check(_lib.gw_decode_attn_global_acc(ctypes.byref(pool.desc), _ptr(q), _ptr(out), _ptr(lse), _ptr(acc), stride,
                                           float(decay), hq, batch, _ptr(cu_q_rows), _ptr(seq_lens), _ptr(block_table),
                                           int(block_table.shape[1]), float(scale), _ptr(workspace),
                                           int(workspace.numel()), _ptr(dev_status), _stream(stream)))
+
+
+def kv_evict_select(acc, seq_lens, budget, keep_idx, keep_lens, sinks=0, recent=0, dev_status=None, stream=None):
+    """gw_kv_evict_select: the indices of the `budget` tokens that each
+    sequence keeps (the first `sinks`, the last `recent`, the largest acc
+    between), ascending, into keep_idx int32 [batch, >= budget], and their
+    number into keep_lens int32 [batch]."""
+    fn = "gw_kv_evict_select"
+    _on_device(fn, stream, acc, seq_lens, keep_idx, keep_lens, dev_status)
+    batch = int(seq_lens.shape[0])
+    _dense(fn, "seq_lens", seq_lens, torch.int32, batch)
+    _dense(fn, "keep_lens", keep_lens, torch.int32, batch)
+    acc_stride = _row_stride(fn, "acc", acc, torch.float32, batch)
+    keep_stride = _row_stride(fn, "keep_idx", keep_idx, torch.int32, batch)
+    if keep_idx.shape[1] < budget:
+        _invalid(fn, "keep_idx has %d columns, the budget is %d" % (keep_idx.shape[1], budget))
+    _check(_lib.gw_kv_evict_select(_ptr(acc), acc_stride, batch, _ptr(seq_lens), int(budget), int(sinks), int(recent),
+                                   _ptr(keep_idx), keep_stride, _ptr(keep_lens), _ptr(dev_status), _stream(stream)))
+
+
+def kv_evict_compact(pool, block_table, seq_lens, keep_idx, keep_lens, acc=None, dst_block_table=None,
+                     dev_status=None, stream=None):
+    """gw_kv_evict_compact: each sequence's kept rows moved to its front, in
+    its own pages or into those of dst_block_table; acc moves along in place."""
+    fn = "gw_kv_evict_compact"
+    _on_device(fn, stream, pool.data, block_table, seq_lens, keep_idx, keep_lens, acc, dst_block_table, dev_status)
+    batch = int(seq_lens.shape[0])
+    _dense(fn, "seq_lens", seq_lens, torch.int32, batch)
+    _dense(fn, "keep_lens", keep_lens, torch.int32, batch)
+    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    keep_stride = _row_stride(fn, "keep_idx", keep_idx, torch.int32, batch)
+    acc_stride, dst_pages = 0, 0
+    if acc is not None:
+        acc_stride = _row_stride(fn, "acc", acc, torch.float32, batch)
+        if acc.shape[1] < 16 * block_table.shape[1]:
+            _invalid(fn, "acc has %d columns, the block table names %d tokens" % (acc.shape[1],
+                                                                                  16 * block_table.shape[1]))
+    if dst_block_table is not None:
+        _dense(fn, "dst_block_table", dst_block_table, torch.int32, batch, None)
+        dst_pages = int(dst_block_table.shape[1])
+    _check(_lib.gw_kv_evict_compact(ctypes.byref(pool.desc), batch, _ptr(block_table), int(block_table.shape[1]),
+                                    _ptr(seq_lens), _ptr(keep_idx), keep_stride, _ptr(keep_lens),
+                                    _ptr(dst_block_table), dst_pages, _ptr(acc), acc_stride, _ptr(dev_status),
+                                    _stream(stream)))
 
 
 def merge_lse(outs, lses, out, lse_out=None, stream=None):

@@ -6,13 +6,12 @@
 // evaluated as the append evaluates it (explicitly rounded binary32 multiply
 // and add, no fused multiply-add), so that q and K of one position are turned
 // by the same arithmetic.
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 
 namespace gw {
 namespace {
 
+// ---- rows ---------------------------------------------------------------------
 template <int ELEM>
 struct Elem;
 template <>
@@ -41,76 +40,292 @@ __device__ __forceinline__ void rotate(float& x0, float& x1, float c, float s) {
   x1 = y1;
 }
 
-// One item is a pair or a copied element of one (row, head).
-template <int ELEM>
-__global__ void __launch_bounds__(256) rope_rows_kernel(const RopeRowsArgs a) {
+// N elements in one access.
+template <class T, int N>
+struct alignas(sizeof(T) * N) Pack {
+  T v[N];
+};
+
+// How a call's rows are dealt to threads.
+struct RowsPlan {
+  int per_head;  // items of a (row, head): rot_items rotations, then copies
+  int rot_items;
+  int lanes;     // heads that a block takes at a time: thread t has item t % per_head of head t / per_head
+  int sweeps;    // times it takes `lanes` heads
+  int groups;    // blocks' tasks per row
+  int64_t tasks;
+};
+
+// An item is the pairs of one VB-byte access (half pairs: of two, one in each
+// half of the rotated dims), or as many copied elements.  A thread keeps its
+// item and so its (cos, sin) entries for all heads of its row that it takes,
+// kUn of them in flight, which leaves the rows themselves as the only traffic
+// beyond L1.  VB is the widest access that pointers, strides and the widths of
+// the two parts allow: 16 bytes where the model's dims are multiples of 8.
+// Bound by memory: 8192 x 32 x 512 bf16 rows with 128 dims rotated, 541 MB.
+template <int ELEM, bool INTER, int VB>
+__global__ void __launch_bounds__(VB == 16 ? 256 : 1024)
+    rope_rows_kernel(const RopeRowsArgs a, const RowsPlan p) {
   using E = Elem<ELEM>;
   using T = typename E::T;
-  pdl_wait();
-  pdl_trigger();
+  constexpr int kE = VB / static_cast<int>(sizeof(T));        // elements per access
+  constexpr bool kTwo = !INTER || kE == 1;                    // the pairs' elements come from two accesses
+  constexpr int kP = kTwo ? kE : kE / 2;                      // pairs per item
+  constexpr int kUn = 4;
+  using V = Pack<T, kE>;
+  bool waited = a.early_inputs == 0;  // pos and the table rows may be read before the wait
+  auto pass = [&]() {
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+  };
+  if (waited) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const int half = a.rot_dim / 2;
-  const int per_head = half + (a.inplace ? 0 : a.head_dim - a.rot_dim);
-  const int64_t total = static_cast<int64_t>(a.num_rows) * a.num_heads * per_head;
-  for (int64_t w = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; w < total;
-       w += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int j = static_cast<int>(w % per_head);
-    const int64_t rh = w / per_head;
-    const int h = static_cast<int>(rh % a.num_heads);
-    const int64_t row = rh / a.num_heads;
+  const int t = threadIdx.x, item = t % p.per_head, lane = t / p.per_head;
+  const bool rotates = item < p.rot_items;
+  // offsets of the item's accesses within a head
+  const int d0 = !rotates ? a.rot_dim + (item - p.rot_items) * kE : INTER ? 2 * kP * item : kP * item;
+  const int d1 = INTER ? d0 + 1 : d0 + half;
+  for (int64_t task = blockIdx.x; task < p.tasks; task += gridDim.x) {
+    const int64_t row = task / p.groups;
+    const int h0 = static_cast<int>(task - row * p.groups) * p.lanes * p.sweeps + lane;
     const int32_t pos = a.pos[row];
     if (pos < 0 || pos >= a.max_pos) {
-      if (j == 0 && h == 0) set_status(a.status, GW_DEV_POS_RANGE);
+      pass();
+      if (t == 0 && task == row * p.groups) set_status(a.status, GW_DEV_POS_RANGE);
       continue;
     }
-    const T* x = static_cast<const T*>(a.x) + row * a.x_row + h * a.x_head;
-    T* y = static_cast<T*>(a.y) + row * a.y_row + h * a.y_head;
-    if (j >= half) {
-      const int d = a.rot_dim + j - half;
-      y[d] = x[d];
+    if (lane >= p.lanes) continue;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+    T* y = static_cast<T*>(a.y) + row * a.y_row;
+    if (!rotates) {
+      pass();
+      for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
+        V v[kUn];
+#pragma unroll
+        for (int k = 0; k < kUn; ++k) {
+          const int h = h0 + (k0 + k) * p.lanes;
+          if (k0 + k < p.sweeps && h < a.num_heads) v[k] = *reinterpret_cast<const V*>(x + h * a.x_head + d0);
+        }
+#pragma unroll
+        for (int k = 0; k < kUn; ++k) {
+          const int h = h0 + (k0 + k) * p.lanes;
+          if (k0 + k < p.sweeps && h < a.num_heads) *reinterpret_cast<V*>(y + h * a.y_head + d0) = v[k];
+        }
+      }
       continue;
     }
-    const float2 cs = reinterpret_cast<const float2*>(a.rope_cs)[static_cast<int64_t>(pos) * half + j];
-    const int d0 = a.pairs == GW_PAIRS_HALF ? j : 2 * j, d1 = a.pairs == GW_PAIRS_HALF ? j + half : 2 * j + 1;
-    float x0 = E::get(x[d0]), x1 = E::get(x[d1]);
-    rotate(x0, x1, cs.x, a.inverse ? -cs.y : cs.y);
-    y[d0] = E::put(x0);
-    y[d1] = E::put(x1);
+    float c[kP], s[kP];
+    const float* cs = a.rope_cs + (static_cast<int64_t>(pos) * half + kP * item) * 2;
+    if constexpr (kP == 1) {
+      const float2 e = *reinterpret_cast<const float2*>(cs);
+      c[0] = e.x;
+      s[0] = e.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kP; i += 2) {
+        const float4 e = *reinterpret_cast<const float4*>(cs + 2 * i);
+        c[i] = e.x;
+        s[i] = e.y;
+        c[i + 1] = e.z;
+        s[i + 1] = e.w;
+      }
+    }
+    if (a.inverse) {
+#pragma unroll
+      for (int i = 0; i < kP; ++i) s[i] = -s[i];
+    }
+    pass();
+    for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
+      V v0[kUn], v1[kUn];
+#pragma unroll
+      for (int k = 0; k < kUn; ++k) {
+        const int h = h0 + (k0 + k) * p.lanes;
+        if (k0 + k < p.sweeps && h < a.num_heads) {
+          const T* from = x + h * a.x_head;
+          v0[k] = *reinterpret_cast<const V*>(from + d0);
+          if constexpr (kTwo) v1[k] = *reinterpret_cast<const V*>(from + d1);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUn; ++k) {
+        const int h = h0 + (k0 + k) * p.lanes;
+        if (k0 + k < p.sweeps && h < a.num_heads) {
+          T* to = y + h * a.y_head;
+#pragma unroll
+          for (int i = 0; i < kP; ++i) {
+            T& e0 = kTwo ? v0[k].v[i] : v0[k].v[(2 * i) % kE];
+            T& e1 = kTwo ? v1[k].v[i] : v0[k].v[(2 * i + 1) % kE];
+            float x0 = E::get(e0), x1 = E::get(e1);
+            rotate(x0, x1, c[i], s[i]);
+            e0 = E::put(x0);
+            e1 = E::put(x1);
+          }
+          *reinterpret_cast<V*>(to + d0) = v0[k];
+          if constexpr (kTwo) *reinterpret_cast<V*>(to + d1) = v1[k];
+        }
+      }
+    }
   }
+  pass();
 }
 
-// One (cos, sin) entry per item, angle and values in float64.
-__global__ void __launch_bounds__(256)
-    rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, double amplitude, int half, int64_t total) {
+template <int ELEM, int VB>
+cudaError_t launch_rows_vb(const RopeRowsArgs& a, cudaStream_t st) {
+  constexpr int kE = VB / (ELEM == GW_ELEM_F32 ? 4 : 2);
+  const bool inter = a.pairs == GW_PAIRS_INTERLEAVED;
+  RowsPlan p{};
+  p.rot_items = inter && kE > 1 ? a.rot_dim / kE : a.rot_dim / 2 / kE;
+  p.per_head = p.rot_items + (a.inplace ? 0 : (a.head_dim - a.rot_dim) / kE);
+  const int block = p.per_head <= 256 ? 256 : (p.per_head + 31) / 32 * 32;
+  p.lanes = block / p.per_head < a.num_heads ? block / p.per_head : a.num_heads;
+  // Up to four sweeps a block (their loads in flight together), fewer while
+  // that leaves SMs without a block.
+  p.sweeps = 4;
+  const int64_t want = 4 * static_cast<int64_t>(grid_ctas());
+  auto tasks_of = [&](int sweeps) {
+    return static_cast<int64_t>(a.num_rows) * ((a.num_heads + p.lanes * sweeps - 1) / (p.lanes * sweeps));
+  };
+  while (p.sweeps > 1 && tasks_of(p.sweeps) < want) p.sweeps /= 2;
+  p.groups = (a.num_heads + p.lanes * p.sweeps - 1) / (p.lanes * p.sweeps);
+  p.tasks = tasks_of(p.sweeps);
+  const int64_t cap = static_cast<int64_t>(grid_ctas()) * 16;
+  const dim3 grid(static_cast<unsigned>(p.tasks < cap ? p.tasks : cap));
+  if (inter) return launch_pdl(rope_rows_kernel<ELEM, true, VB>, grid, dim3(block), 0, st, a, p);
+  return launch_pdl(rope_rows_kernel<ELEM, false, VB>, grid, dim3(block), 0, st, a, p);
+}
+
+template <int ELEM>
+cudaError_t launch_rows(const RopeRowsArgs& a, cudaStream_t st) {
+  constexpr int kSize = ELEM == GW_ELEM_F32 ? 4 : 2;
+  // every offset that an access can have, in bytes
+  uint64_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+  if (a.num_rows > 1) all |= static_cast<uint64_t>(a.x_row | a.y_row) * kSize;
+  if (a.num_heads > 1) all |= static_cast<uint64_t>(a.x_head | a.y_head) * kSize;
+  all |= static_cast<uint64_t>(a.pairs == GW_PAIRS_HALF ? a.rot_dim / 2 : a.rot_dim) * kSize;
+  if (!a.inplace) all |= static_cast<uint64_t>(a.head_dim - a.rot_dim) * kSize;
+  if (all % 16 == 0) return launch_rows_vb<ELEM, 16>(a, st);
+  if (all % 8 == 0) return launch_rows_vb<ELEM, 8>(a, st);
+  if (all % 4 == 0) return launch_rows_vb<ELEM, 4>(a, st);
+  if constexpr (kSize == 2) return launch_rows_vb<ELEM, 2>(a, st);
+  return cudaErrorInvalidValue;  // not reached: the entry point checks the alignment to an element
+}
+
+// ---- table --------------------------------------------------------------------
+// Entry (p, i) is amplitude * e^(i p f_i).  Float64 sine and cosine are slow
+// here (the FP64 pipes of this GPU have about 1/60 of the FP32 rate), so a
+// block computes two per pair, e^(i f) and e^(i p0 f) at its first position
+// p0, and gets the rest by complex products, e^(i (p+k) f) = e^(i p f) e^(i k f),
+// in pairs of floats (value = hi + lo, about 48 bits; products split exactly by
+// a fused multiply-add, sums by the two-sum).  A product adds an error of about
+// 2^-46 and squaring doubles what is there, so over a block's at most 1024
+// positions the values stay good to 2^-37, and each is rounded once to float32.
+// Writes are the floor: 262144 x 64 entries, 134 MB.
+struct Ff {
+  float h, l;
+};
+struct Cplx {
+  Ff re, im;
+};
+
+__device__ __forceinline__ Ff split(double v) {
+  const float h = __double2float_rn(v);
+  return Ff{h, __double2float_rn(v - static_cast<double>(h))};
+}
+
+// a b + sign c d in pairs of floats, sign = +-1
+template <int SIGN>
+__device__ __forceinline__ Ff dot2(const Ff& a, const Ff& b, const Ff& c, const Ff& d) {
+  const float ch = SIGN > 0 ? c.h : -c.h, cl = SIGN > 0 ? c.l : -c.l;
+  const float p = __fmul_rn(a.h, b.h), q = __fmul_rn(ch, d.h);
+  float low = __fadd_rn(__fmaf_rn(a.h, b.h, -p), __fmaf_rn(ch, d.h, -q));
+  const float s = __fadd_rn(p, q);
+  const float v = __fsub_rn(s, p);
+  low = __fadd_rn(low, __fadd_rn(__fsub_rn(p, __fsub_rn(s, v)), __fsub_rn(q, v)));
+  low = __fmaf_rn(a.h, b.l, low);
+  low = __fmaf_rn(a.l, b.h, low);
+  low = __fmaf_rn(ch, d.l, low);
+  low = __fmaf_rn(cl, d.h, low);
+  const float h = __fadd_rn(s, low);
+  return Ff{h, __fsub_rn(low, __fsub_rn(h, s))};
+}
+
+__device__ __forceinline__ Cplx mul(const Cplx& a, const Cplx& b) {
+  return Cplx{dot2<-1>(a.re, b.re, a.im, b.im), dot2<1>(a.re, b.im, a.im, b.re)};
+}
+
+constexpr int kTableThreads = 512;
+constexpr int kMaxRuns = 8;
+
+// Thread (pair i, run r) writes the `run` positions from p0 + r * run on, four
+// chains of every fourth position at a time.
+__global__ void __launch_bounds__(kTableThreads) rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, double amplitude,
+                                                                       int half, int run, int runs, int max_pos) {
+  __shared__ Cplx s_base[kMaxRopePairs], s_w[kMaxRopePairs], s_w4[kMaxRopePairs], s_run[kMaxRopePairs];
   pdl_wait();
   pdl_trigger();
-  for (int64_t w = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; w < total;
-       w += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  const int t = threadIdx.x;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * run * runs;
+  if (t < half) {
     double s, c;
-    sincos(static_cast<double>(w / half) * fr.f[w % half], &s, &c);
-    out[w] = make_float2(__double2float_rn(c * amplitude), __double2float_rn(s * amplitude));
+    sincos(fr.f[t], &s, &c);
+    Cplx w{split(c), split(s)};
+    s_w[t] = w;
+    for (int k = 1; k < run; k *= 2) {
+      w = mul(w, w);
+      if (k == 2) s_w4[t] = w;
+    }
+    s_run[t] = w;
+  } else if (t >= kTableThreads / 2 && t - kTableThreads / 2 < half) {
+    const int i = t - kTableThreads / 2;
+    double s, c;
+    sincos(static_cast<double>(p0) * fr.f[i], &s, &c);
+    s_base[i] = Cplx{split(c * amplitude), split(s * amplitude)};
   }
-}
-
-int grid_for(int64_t items, int block) {
-  const int64_t blocks = (items + block - 1) / block, cap = static_cast<int64_t>(grid_ctas()) * 16;
-  return static_cast<int>(blocks < cap ? blocks : cap);
+  __syncthreads();
+  const int r = t / half, i = t - r * half;
+  if (r >= runs) return;
+  const int64_t first = p0 + static_cast<int64_t>(r) * run;
+  if (first >= max_pos) return;
+  Cplx z[4];
+  z[0] = s_base[i];
+  for (int k = 0; k < r; ++k) z[0] = mul(z[0], s_run[i]);
+  const Cplx w = s_w[i], w4 = s_w4[i];
+#pragma unroll
+  for (int k = 1; k < 4; ++k) z[k] = mul(z[k - 1], w);
+  float2* o = out + first * half + i;
+  const int n = max_pos - first < run ? static_cast<int>(max_pos - first) : run;
+  for (int k0 = 0; k0 < n; k0 += 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k0 + k < n) o[static_cast<int64_t>(k0 + k) * half] = make_float2(z[k].re.h, z[k].im.h);
+      z[k] = mul(z[k], w4);
+    }
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_rope_rows(int elem, const RopeRowsArgs& a, cudaStream_t st) {
-  const int64_t per_head = a.rot_dim / 2 + (a.inplace ? 0 : a.head_dim - a.rot_dim);
-  const dim3 grid(grid_for(static_cast<int64_t>(a.num_rows) * a.num_heads * per_head, 256));
-  if (elem == GW_ELEM_BF16) return launch_pdl(rope_rows_kernel<GW_ELEM_BF16>, grid, dim3(256), 0, st, a);
-  if (elem == GW_ELEM_F16) return launch_pdl(rope_rows_kernel<GW_ELEM_F16>, grid, dim3(256), 0, st, a);
-  return launch_pdl(rope_rows_kernel<GW_ELEM_F32>, grid, dim3(256), 0, st, a);
+  if (elem == GW_ELEM_BF16) return launch_rows<GW_ELEM_BF16>(a, st);
+  if (elem == GW_ELEM_F16) return launch_rows<GW_ELEM_F16>(a, st);
+  return launch_rows<GW_ELEM_F32>(a, st);
 }
 
 cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amplitude, int half, int max_pos,
                                   cudaStream_t st) {
-  const int64_t total = static_cast<int64_t>(max_pos) * half;
-  return launch_pdl(rope_cs_scaled_kernel, dim3(grid_for(total, 256)), dim3(256), 0, st,
-                    reinterpret_cast<float2*>(out), freqs, amplitude, half, total);
+  // Long runs need fewer float64 sines, short ones keep every SM busy.
+  const int runs = kTableThreads / half < kMaxRuns ? kTableThreads / half : kMaxRuns;
+  int run = 128;
+  while (run > 16 && max_pos < static_cast<int64_t>(run) * runs * 2 * grid_ctas()) run /= 2;
+  const unsigned blocks = (max_pos + run * runs - 1) / (run * runs);
+  return launch_pdl(rope_cs_scaled_kernel, dim3(blocks), dim3(kTableThreads), 0, st, reinterpret_cast<float2*>(out),
+                    freqs, amplitude, half, run, runs, max_pos);
 }
 
 }  // namespace gw

@@ -56,22 +56,31 @@ struct RowsPlan {
   int64_t tasks;
 };
 
+// Most threads of a block: a head of 1024 elements has an item per access.
+template <int ELEM, int VB>
+constexpr int kRowThreads = (ELEM == GW_ELEM_F32 ? 4096 : 2048) / VB > 256 ? (ELEM == GW_ELEM_F32 ? 4096 : 2048) / VB : 256;
+
 // An item is the pairs of one VB-byte access (half pairs: of two, one in each
 // half of the rotated dims), or as many copied elements.  A thread keeps its
 // item and so its (cos, sin) entries for all heads of its row that it takes,
-// kUn of them in flight, which leaves the rows themselves as the only traffic
-// beyond L1.  VB is the widest access that pointers, strides and the widths of
-// the two parts allow: 16 bytes where the model's dims are multiples of 8.
-// Bound by memory: 8192 x 32 x 512 bf16 rows with 128 dims rotated, 541 MB.
+// which leaves the rows themselves as the only traffic beyond L1.  VB is the
+// widest access that pointers, strides and the widths of the two parts allow:
+// 16 bytes where the model's dims are multiples of 8.
+// Bound by memory: 8192 x 32 x 512 bf16 rows with 128 interleaved dims rotated
+// take 91 us for 541 MB (5.9 TB/s, 0.87 of a copy), 4093 x 16 x 256 fp32 rows
+// 25 us for 138 MB.  Two accesses in flight per thread and 32 warps per SM are
+// the best of the mixes: 4 in flight with 24 or fewer warps 102 us, 1 with 48
+// warps 104 us; separate loops for rotated and copied items 121 us, since a
+// head's 16 + 48 items share warps.
 template <int ELEM, bool INTER, int VB>
-__global__ void __launch_bounds__(VB == 16 ? 256 : 1024)
+__global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<ELEM, VB>)
     rope_rows_kernel(const RopeRowsArgs a, const RowsPlan p) {
   using E = Elem<ELEM>;
   using T = typename E::T;
   constexpr int kE = VB / static_cast<int>(sizeof(T));        // elements per access
   constexpr bool kTwo = !INTER || kE == 1;                    // the pairs' elements come from two accesses
   constexpr int kP = kTwo ? kE : kE / 2;                      // pairs per item
-  constexpr int kUn = 4;
+  constexpr int kUn = 2;
   using V = Pack<T, kE>;
   bool waited = a.early_inputs == 0;  // pos and the table rows may be read before the wait
   auto pass = [&]() {
@@ -103,44 +112,31 @@ __global__ void __launch_bounds__(VB == 16 ? 256 : 1024)
     if (lane >= p.lanes) continue;
     const T* x = static_cast<const T*>(a.x) + row * a.x_row;
     T* y = static_cast<T*>(a.y) + row * a.y_row;
-    if (!rotates) {
-      pass();
-      for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
-        V v[kUn];
-#pragma unroll
-        for (int k = 0; k < kUn; ++k) {
-          const int h = h0 + (k0 + k) * p.lanes;
-          if (k0 + k < p.sweeps && h < a.num_heads) v[k] = *reinterpret_cast<const V*>(x + h * a.x_head + d0);
-        }
-#pragma unroll
-        for (int k = 0; k < kUn; ++k) {
-          const int h = h0 + (k0 + k) * p.lanes;
-          if (k0 + k < p.sweeps && h < a.num_heads) *reinterpret_cast<V*>(y + h * a.y_head + d0) = v[k];
-        }
-      }
-      continue;
-    }
     float c[kP], s[kP];
-    const float* cs = a.rope_cs + (static_cast<int64_t>(pos) * half + kP * item) * 2;
-    if constexpr (kP == 1) {
-      const float2 e = *reinterpret_cast<const float2*>(cs);
-      c[0] = e.x;
-      s[0] = e.y;
-    } else {
+    if (rotates) {
+      const float* cs = a.rope_cs + (static_cast<int64_t>(pos) * half + kP * item) * 2;
+      if constexpr (kP == 1) {
+        const float2 e = *reinterpret_cast<const float2*>(cs);
+        c[0] = e.x;
+        s[0] = e.y;
+      } else {
 #pragma unroll
-      for (int i = 0; i < kP; i += 2) {
-        const float4 e = *reinterpret_cast<const float4*>(cs + 2 * i);
-        c[i] = e.x;
-        s[i] = e.y;
-        c[i + 1] = e.z;
-        s[i + 1] = e.w;
+        for (int i = 0; i < kP; i += 2) {
+          const float4 e = *reinterpret_cast<const float4*>(cs + 2 * i);
+          c[i] = e.x;
+          s[i] = e.y;
+          c[i + 1] = e.z;
+          s[i + 1] = e.w;
+        }
       }
-    }
-    if (a.inverse) {
+      if (a.inverse) {
 #pragma unroll
-      for (int i = 0; i < kP; ++i) s[i] = -s[i];
+        for (int i = 0; i < kP; ++i) s[i] = -s[i];
+      }
     }
     pass();
+    // rotated and copied items share the accesses, so that a warp that holds
+    // both runs them once
     for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
       V v0[kUn], v1[kUn];
 #pragma unroll
@@ -149,7 +145,7 @@ __global__ void __launch_bounds__(VB == 16 ? 256 : 1024)
         if (k0 + k < p.sweeps && h < a.num_heads) {
           const T* from = x + h * a.x_head;
           v0[k] = *reinterpret_cast<const V*>(from + d0);
-          if constexpr (kTwo) v1[k] = *reinterpret_cast<const V*>(from + d1);
+          if (kTwo && rotates) v1[k] = *reinterpret_cast<const V*>(from + d1);
         }
       }
 #pragma unroll
@@ -157,17 +153,19 @@ __global__ void __launch_bounds__(VB == 16 ? 256 : 1024)
         const int h = h0 + (k0 + k) * p.lanes;
         if (k0 + k < p.sweeps && h < a.num_heads) {
           T* to = y + h * a.y_head;
+          if (rotates) {
 #pragma unroll
-          for (int i = 0; i < kP; ++i) {
-            T& e0 = kTwo ? v0[k].v[i] : v0[k].v[(2 * i) % kE];
-            T& e1 = kTwo ? v1[k].v[i] : v0[k].v[(2 * i + 1) % kE];
-            float x0 = E::get(e0), x1 = E::get(e1);
-            rotate(x0, x1, c[i], s[i]);
-            e0 = E::put(x0);
-            e1 = E::put(x1);
+            for (int i = 0; i < kP; ++i) {
+              T& e0 = kTwo ? v0[k].v[i] : v0[k].v[(2 * i) % kE];
+              T& e1 = kTwo ? v1[k].v[i] : v0[k].v[(2 * i + 1) % kE];
+              float x0 = E::get(e0), x1 = E::get(e1);
+              rotate(x0, x1, c[i], s[i]);
+              e0 = E::put(x0);
+              e1 = E::put(x1);
+            }
+            if (kTwo) *reinterpret_cast<V*>(to + d1) = v1[k];
           }
           *reinterpret_cast<V*>(to + d0) = v0[k];
-          if constexpr (kTwo) *reinterpret_cast<V*>(to + d1) = v1[k];
         }
       }
     }
@@ -184,9 +182,9 @@ cudaError_t launch_rows_vb(const RopeRowsArgs& a, cudaStream_t st) {
   p.per_head = p.rot_items + (a.inplace ? 0 : (a.head_dim - a.rot_dim) / kE);
   const int block = p.per_head <= 256 ? 256 : (p.per_head + 31) / 32 * 32;
   p.lanes = block / p.per_head < a.num_heads ? block / p.per_head : a.num_heads;
-  // Up to four sweeps a block (their loads in flight together), fewer while
-  // that leaves SMs without a block.
-  p.sweeps = 4;
+  // Up to eight sweeps a block (one read of pos and of the table entries for
+  // all), fewer while that leaves SMs without a block.
+  p.sweeps = 8;
   const int64_t want = 4 * static_cast<int64_t>(grid_ctas());
   auto tasks_of = [&](int sweeps) {
     return static_cast<int64_t>(a.num_rows) * ((a.num_heads + p.lanes * sweeps - 1) / (p.lanes * sweeps));
@@ -223,9 +221,10 @@ cudaError_t launch_rows(const RopeRowsArgs& a, cudaStream_t st) {
 // p0, and gets the rest by complex products, e^(i (p+k) f) = e^(i p f) e^(i k f),
 // in pairs of floats (value = hi + lo, about 48 bits; products split exactly by
 // a fused multiply-add, sums by the two-sum).  A product adds an error of about
-// 2^-46 and squaring doubles what is there, so over a block's at most 1024
-// positions the values stay good to 2^-37, and each is rounded once to float32.
-// Writes are the floor: 262144 x 64 entries, 134 MB.
+// 2^-46 and squaring doubles what is there, so over a block's at most 512
+// positions the values stay good to 2^-38, and each is rounded once to float32.
+// 262144 x 64 entries take 35 us (134 MB, the floor 20 us): about forty FP32
+// operations an entry bound it, after a start of float64 sines.
 struct Ff {
   float h, l;
 };
@@ -259,33 +258,34 @@ __device__ __forceinline__ Cplx mul(const Cplx& a, const Cplx& b) {
   return Cplx{dot2<-1>(a.re, b.re, a.im, b.im), dot2<1>(a.re, b.im, a.im, b.re)};
 }
 
-constexpr int kTableThreads = 512;
+constexpr int kTableThreads = 256;
 constexpr int kMaxRuns = 8;
 
 // Thread (pair i, run r) writes the `run` positions from p0 + r * run on, four
 // chains of every fourth position at a time.
-__global__ void __launch_bounds__(kTableThreads) rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, double amplitude,
-                                                                       int half, int run, int runs, int max_pos) {
+__global__ void __launch_bounds__(kTableThreads, 4)
+    rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, double amplitude, int half, int run, int runs, int max_pos) {
   __shared__ Cplx s_base[kMaxRopePairs], s_w[kMaxRopePairs], s_w4[kMaxRopePairs], s_run[kMaxRopePairs];
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x;
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * run * runs;
-  if (t < half) {
+  for (int job = t; job < 2 * half; job += kTableThreads) {
     double s, c;
-    sincos(fr.f[t], &s, &c);
-    Cplx w{split(c), split(s)};
-    s_w[t] = w;
-    for (int k = 1; k < run; k *= 2) {
-      w = mul(w, w);
-      if (k == 2) s_w4[t] = w;
+    if (job < half) {
+      sincos(fr.f[job], &s, &c);
+      Cplx w{split(c), split(s)};
+      s_w[job] = w;
+      for (int k = 1; k < run; k *= 2) {
+        w = mul(w, w);
+        if (k == 2) s_w4[job] = w;
+      }
+      s_run[job] = w;
+    } else {
+      const int i = job - half;
+      sincos(static_cast<double>(p0) * fr.f[i], &s, &c);
+      s_base[i] = Cplx{split(c * amplitude), split(s * amplitude)};
     }
-    s_run[t] = w;
-  } else if (t >= kTableThreads / 2 && t - kTableThreads / 2 < half) {
-    const int i = t - kTableThreads / 2;
-    double s, c;
-    sincos(static_cast<double>(p0) * fr.f[i], &s, &c);
-    s_base[i] = Cplx{split(c * amplitude), split(s * amplitude)};
   }
   __syncthreads();
   const int r = t / half, i = t - r * half;
@@ -321,7 +321,7 @@ cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amp
                                   cudaStream_t st) {
   // Long runs need fewer float64 sines, short ones keep every SM busy.
   const int runs = kTableThreads / half < kMaxRuns ? kTableThreads / half : kMaxRuns;
-  int run = 128;
+  int run = 64;
   while (run > 16 && max_pos < static_cast<int64_t>(run) * runs * 2 * grid_ctas()) run /= 2;
   const unsigned blocks = (max_pos + run * runs - 1) / (run * runs);
   return launch_pdl(rope_cs_scaled_kernel, dim3(blocks), dim3(kTableThreads), 0, st, reinterpret_cast<float2*>(out),

@@ -179,7 +179,8 @@ def _dense(fn, name, t, dtype, *shape):
     """`t` has this dtype and shape (None: any length) and is contiguous."""
     if t is None:
         _invalid(fn, "%s is None" % name)
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    want = tuple(m if n is None else n for n, m in zip(shape, t.shape)) if None in shape else shape
+    if t.dtype != dtype or t.shape != want or len(want) != len(shape):
         _invalid(fn, "%s must be %s of shape %s (got %s %s)" % (name, dtype, list(shape), t.dtype, list(t.shape)))
     if not t.is_contiguous():
         _invalid(fn, "%s must be contiguous" % name)
@@ -278,7 +279,7 @@ def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, invers
     if dim > 1 and (x1 != 1 or y1 != 1):
         _invalid(fn, "the last dimension of x and out must have stride 1")
     _vector(fn, "pos", pos, rows)
-    _dense(fn, "rope_cs", rope_cs, torch.float32, None, rot_dim // 2, 2)
+    _dense(fn, "rope_cs", rope_cs, torch.float32, rope_cs.shape[0], rot_dim // 2, 2)
     _check(_lib.gw_rope_rows(x.data_ptr(), xr, xh, out.data_ptr(), yr, yh, elem, rows, heads, dim, rot_dim,
                              PAIRS_INTERLEAVED if interleaved else PAIRS_HALF, 1 if inverse else 0, pos.data_ptr(),
                              rope_cs.data_ptr(), rope_cs.shape[0], _addr(dev_status), handle))
@@ -384,8 +385,10 @@ def decode_attn_global_acc(pool, q, out, lse, acc, cu_q_rows, seq_lens, block_ta
     handle = _on_device(fn, stream, pool.data, q, out, lse, acc, cu_q_rows, seq_lens, block_table, workspace,
                         dev_status)
     batch = seq_lens.shape[0]
-    _dense(fn, "q", q, torch.bfloat16, None, None, 512)
+    if q.dim() != 3:
+        _invalid(fn, "q must be [rows, heads, 512] (got %s)" % list(q.shape))
     rows, hq = q.shape[0], q.shape[1]
+    _dense(fn, "q", q, torch.bfloat16, rows, hq, 512)
     _dense(fn, "out", out, torch.bfloat16, rows, hq, 512)
     if lse is not None:
         _dense(fn, "lse", lse, torch.float32, rows, hq)

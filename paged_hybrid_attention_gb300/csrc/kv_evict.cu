@@ -15,108 +15,195 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// A cluster of 1 to kMaxSelCtas blocks takes a sequence, each block a
+// contiguous slice of its tokens, each warp a contiguous piece of the slice, up
+// to kSelKeys tokens per thread in registers (longer slices are read again in
+// rounds).  The k-th largest key of the middle is found digit by digit from
+// the top, 8 bits at a time: each block counts its keys of the current prefix
+// by digit in shared memory, and after a cluster barrier every block adds up
+// all blocks' counts and finds the same digit.  (Digits of 11 bits save a pass
+// but make each block read eight times as many counts of the others.)  It
+// ends with the first digit all of whose keys are kept.  Then the blocks
+// exchange how many of their tokens are kept or tied, and write their indices
+// in order.
 constexpr int kSelThreads = 1024;
+constexpr int kSelKeys = 16;
+constexpr int kMaxSelCtas = 8;
 
-// Exclusive sum of v over the block's threads in thread order; `total`
-// receives the sum.  `scratch`: 33 values.
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, uint64_t& total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  uint64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // the previous call's reads of scratch are done
-  if (lane == 31) scratch[w] = x;
-  __syncthreads();
-  if (w == 0) {
-    uint64_t s = scratch[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    scratch[lane] = s;
-  }
-  __syncthreads();
-  total = scratch[31];
-  return (w > 0 ? scratch[w - 1] : 0) + x - v;
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The 32-bit word that block `rank` of the cluster has at this shared address.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
-// One block per sequence.  The k-th largest key of the middle is found digit
-// by digit from the top (four passes of 8 bits), then one pass in token order
-// writes the kept indices.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint64_t scratch[32];
-  __shared__ uint32_t found[2];  // digit, keys above it within the prefix
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const SelectArgs a, int ctas) {
+  __shared__ uint32_t hist[4][256];
+  __shared__ uint32_t found[3];  // digit, keys of the prefix above it, keys of it
+  __shared__ uint32_t kept[2];   // this block's tokens: kept for sure, tied
+  __shared__ uint2 warp_kept[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x, tid = threadIdx.x;
   const int L = a.seq_lens[b];
   int32_t* keep = a.keep_idx + b * a.keep_stride;
-  if (L < 0 || L > a.acc_stride) {
-    if (tid == 0) {
+  if (L < 0 || L > a.acc_stride) {  // the same for the whole cluster
+    if (rank == 0 && tid == 0) {
       set_status(a.status, GW_DEV_LEN_RANGE);
       a.keep_lens[b] = 0;
     }
     return;
   }
-  if (tid == 0) a.keep_lens[b] = min(L, a.budget);
+  if (rank == 0 && tid == 0) a.keep_lens[b] = min(L, a.budget);
   if (L <= a.budget) {
-    for (int j = tid; j < L; j += kSelThreads) keep[j] = j;
+    for (int j = rank * kSelThreads + tid; j < L; j += ctas * kSelThreads) keep[j] = j;
     return;
   }
-  const float* acc = a.acc + b * a.acc_stride;
-  const int lo = a.sinks, hi = L - a.recent;
+  // tokens by their place in the block's slice [t0, t0 + n): a slice has fewer
+  // than 2^29, since a long row has kMaxSelCtas of them
+  const int per = (L - 1) / ctas + 1;
+  const int t0 = static_cast<int>(min(static_cast<int64_t>(rank) * per, static_cast<int64_t>(L)));
+  const int n = min(per, L - t0);
+  const int lo = a.sinks - t0, hi = L - a.recent - t0;  // the middle
+  const float* acc = a.acc + b * a.acc_stride + t0;
   uint32_t need = a.budget - a.sinks - a.recent;  // of the middle
-  const bool any = need > 0;
-  uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; any && shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int j = lo + tid; j < hi; j += kSelThreads) {
-      const uint32_t key = order_key(acc[j]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
+  const int rounds = (per - 1) / (kSelThreads * kSelKeys) + 1;
+  const int keys = rounds > 1 ? kSelKeys : (per - 1) / kSelThreads + 1;  // of a thread, per round
+  uint32_t key[kSelKeys];
+  int first = 0;  // the token of r = 0; the next lie 32 apart
+  auto load = [&](int round) {
+    first = (round * 32 + warp) * keys * 32 + lane;
+#pragma unroll
+    for (int r = 0; r < kSelKeys; ++r) {
+      if (r < keys) {
+        const int j = first + r * 32;
+        key[r] = j < n ? __float_as_uint(acc[j]) : 0;
+      }
     }
-    __syncthreads();
-    // thread t < 256: keys of digit 255 - t and above
-    uint64_t total;
-    const uint32_t mine = tid < 256 ? hist[255 - tid] : 0;
-    const uint32_t above = static_cast<uint32_t>(block_scan(mine, scratch, total));
-    if (tid < 256 && above < need && above + mine >= need) {
-      found[0] = 255 - tid;
-      found[1] = above;
+#pragma unroll
+    for (int r = 0; r < kSelKeys; ++r)
+      if (r < keys) key[r] = order_key(__uint_as_float(key[r]));
+  };
+  load(0);
+  (&hist[0][0])[tid] = 0;
+  if (tid < 2) kept[tid] = 0;
+  __syncthreads();
+  uint32_t prefix = 0, mask = 0;
+  const bool middle = need > 0;  // the same for the whole cluster
+#pragma unroll 1
+  for (int shift = 24; middle && shift >= 0; shift -= 8) {
+    uint32_t* h = hist[shift / 8];
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load(round);
+#pragma unroll
+      for (int r = 0; r < kSelKeys; ++r) {
+        const int j = first + r * 32;
+        if (r < keys && j < n && j >= lo && j < hi && (key[r] & mask) == prefix) atomicAdd(&h[(key[r] >> shift) & 255], 1u);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (warp < 8) {  // thread t: digit 255 - t, counted over the cluster
+      uint32_t count = 0;
+      for (int c = 0; c < ctas; ++c) count += ld_cluster(&h[255 - tid], c);
+      uint32_t x = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_kept[warp].x = x;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      uint32_t above = x - count;
+      for (int w = 0; w < warp; ++w) above += warp_kept[w].x;
+      if (above < need && above + count >= need) {
+        found[0] = 255 - tid;
+        found[1] = above;
+        found[2] = count;
+      }
     }
     __syncthreads();
     prefix |= found[0] << shift;
     mask |= 255u << shift;
     need -= found[1];
-    __syncthreads();
+    const bool done = found[2] == need;  // all of the digit's keys are kept, whatever their lower bits
+    __syncthreads();                     // found and warp_kept are written again
+    if (done) break;
   }
-  // keep all above `prefix`, and the first `need` equal to it
-  uint32_t sure = 0, ties = 0;  // so far
-  for (int j0 = 0; j0 < L; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    uint32_t is_sure = 0, is_tie = 0;
-    if (j < L) {
-      if (j < lo || j >= hi) {
-        is_sure = 1;
-      } else if (any) {
-        const uint32_t key = order_key(acc[j]);
-        is_sure = key > prefix;
-        is_tie = key == prefix;
+  // Kept for sure: the ends, and in the middle what lies above `prefix`; of the
+  // keys that match it (none if nothing of the middle is kept) the first `need`.
+  auto ballots = [&](int r, uint32_t& sure, uint32_t& tie) {
+    const int j = first + r * 32;
+    const bool in = j < n, mid = j >= lo && j < hi;
+    const uint32_t k = key[r] & mask;
+    sure = __ballot_sync(0xffffffffu, in && (!mid || (middle && k > prefix)));
+    tie = __ballot_sync(0xffffffffu, in && mid && middle && k == prefix);
+  };
+  auto count_warp = [&]() {  // the round's counts of this warp
+    uint2 w = make_uint2(0, 0);
+#pragma unroll
+    for (int r = 0; r < kSelKeys; ++r) {
+      if (r < keys) {
+        uint32_t s, e;
+        ballots(r, s, e);
+        w.x += __popc(s);
+        w.y += __popc(e);
       }
     }
-    uint64_t total;
-    const uint64_t before = block_scan((static_cast<uint64_t>(is_sure) << 32) | is_tie, scratch, total);
-    const uint32_t ties_before = ties + static_cast<uint32_t>(before);
-    if (is_sure || (is_tie && ties_before < need))
-      keep[sure + static_cast<uint32_t>(before >> 32) + min(ties_before, need)] = j;
-    sure += static_cast<uint32_t>(total >> 32);
-    ties += static_cast<uint32_t>(total);
+    return w;
+  };
+  uint2 mine = make_uint2(0, 0);
+  for (int round = 0; round < rounds; ++round) {
+    if (rounds > 1) load(round);
+    const uint2 w = count_warp();
+    mine.x += w.x;
+    mine.y += w.y;
   }
+  if (lane == 0) {
+    atomicAdd(&kept[0], mine.x);
+    atomicAdd(&kept[1], mine.y);
+    warp_kept[warp] = mine;
+  }
+  cluster_arrive();
+  cluster_wait();
+  // of the blocks before this one: lane c adds up block c
+  uint32_t base_sure = lane < rank ? ld_cluster(&kept[0], lane) : 0, base_ties = lane < rank ? ld_cluster(&kept[1], lane) : 0;
+  base_sure = __reduce_add_sync(0xffffffffu, base_sure);
+  base_ties = __reduce_add_sync(0xffffffffu, base_ties);
+  cluster_arrive();  // waited for at the end: no block leaves while others read its shared memory
+  for (int round = 0; round < rounds; ++round) {
+    if (rounds > 1) {
+      load(round);
+      mine = count_warp();
+      __syncthreads();  // the previous round's reads of warp_kept are done
+      if (lane == 0) warp_kept[warp] = mine;
+      __syncthreads();
+    }
+    const uint2 w = warp_kept[lane];
+    uint32_t sure = base_sure + __reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0);
+    uint32_t ties = base_ties + __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0);
+    base_sure += __reduce_add_sync(0xffffffffu, w.x);
+    base_ties += __reduce_add_sync(0xffffffffu, w.y);
+    const uint32_t low = (1u << lane) - 1;
+#pragma unroll
+    for (int r = 0; r < kSelKeys; ++r) {
+      if (r < keys) {
+        uint32_t s, e;
+        ballots(r, s, e);
+        const uint32_t ties_before = ties + __popc(e & low);
+        if ((s >> lane & 1) || ((e >> lane & 1) && ties_before < need))
+          keep[sure + __popc(s & low) + min(ties_before, need)] = t0 + first + r * 32;
+        sure += __popc(s);
+        ties += __popc(e);
+      }
+    }
+  }
+  cluster_wait();
 }
 
 // ---- compact ------------------------------------------------------------------
@@ -206,7 +293,24 @@ cudaError_t launch_compact_layout(const CompactArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t st) {
-  return launch_pdl(evict_select_kernel, dim3(a.batch), dim3(kSelThreads), 0, st, a);
+  // Lengths are device values: the row stride bounds them.  More blocks per
+  // sequence while each would still have 4096 tokens.
+  int ctas = 1;
+  while (ctas < kMaxSelCtas && a.acc_stride > static_cast<int64_t>(4096) * ctas) ctas *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * ctas);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early_launch() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas);
 }
 
 cudaError_t launch_evict_compact(int layout, const CompactArgs& a, cudaStream_t st) {

@@ -318,16 +318,15 @@ size_t gw_attn_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int3
       .total;
 }
 
-// Layout of a gw_decode_attn_global_acc workspace behind the attention's own:
-// the softmax statistics, then the logits.
+// Layout of a gw_decode_attn_global_acc workspace: the attention's own, then
+// the logits.
 struct AccLayout {
-  size_t stat, score, total;
+  size_t score, total;
 };
 
 static AccLayout acc_layout(const WsLayout& w, int num_q_heads, int batch, int max_pages) {
   AccLayout l{};
-  l.stat = round_up(w.total, 256);
-  l.score = l.stat + round_up(static_cast<size_t>(batch) * num_q_heads * 8, 256);
+  l.score = round_up(w.total, 256);
   l.total = l.score + round_up(static_cast<size_t>(batch) * max_pages * 16 * num_q_heads * 4, 256);
   return l;
 }
@@ -456,7 +455,6 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
   }
   if (acc) {
     a.score = reinterpret_cast<float*>(ws + al.score);
-    a.stat = reinterpret_cast<float2*>(ws + al.stat);
     a.acc = acc->acc;
     a.acc_stride = acc->stride;
     a.decay = acc->decay;
@@ -469,7 +467,6 @@ static gw_status attn_common(const char* fn, bool local, const gw_kv_pool* pool,
   } else {
     e = launch_global_decode(pool->layout, a, st);
     if (e == cudaSuccess && max_q_rows > 1) e = launch_global_prompt(pool->layout, a, max_q_rows, st);
-    if (e == cudaSuccess && acc) e = launch_attn_acc(a, st);
   }
   return cuda_status(e, fn);
 }

@@ -103,7 +103,6 @@ struct LocalArgs {
   int32_t early_inputs;  // gw_set_early_inputs: plan before the wait on the previous kernel
   // Attention weights (gw_decode_attn_global_acc); score null: none.
   float* score;    // [batch][max_pages * 16][num_q_heads], logits in base-2 units
-  float2* stat;    // [batch][num_q_heads]: {max logit, 1 / sum} of the row's softmax
   float* acc;      // [batch][acc_stride]
   int64_t acc_stride;
   float decay;
@@ -149,13 +148,10 @@ gw_status set_error(gw_status code, const char* fn, const char* fmt, ...);
 // Log-sum-exp merge of each decode row's partials into bf16 `out`; units of
 // heads_per_unit q heads, planned as in a.unit_base, at most max_chunks
 // chunks per sequence; with `discard`, the merged partials' L2 lines are
-// dropped unwritten.
+// dropped unwritten.  With a.score, also the weights pass of
+// gw_decode_attn_global_acc.
 cudaError_t launch_combine(const LocalArgs& a, int heads_per_unit, int head_dim, int max_chunks, bool discard,
                            cudaStream_t st);
-
-// acc = decay * acc + each token's softmax weights summed over the heads, from
-// a.score and a.stat (after launch_combine).
-cudaError_t launch_attn_acc(const LocalArgs& a, cudaStream_t st);
 
 cudaError_t launch_append(int layout, int dtype, const AppendArgs& a, cudaStream_t st);
 

@@ -248,7 +248,7 @@ typedef struct gw_rope_scaling {
   double low, high;  /* RAMP: turns below / above which a pair is fully / not
                         at all interpolated; 0 <= low < high                  */
   double orig_max_pos; /* RAMP: the trained context, > 0                      */
-  double amplitude;  /* > 0: multiplies cos and sin (1 for none)              */
+  double amplitude;  /* in [1e-6, 1e6]: multiplies cos and sin (1 for none)   */
 } gw_rope_scaling;
 
 /*
@@ -265,10 +265,12 @@ typedef struct gw_rope_scaling {
  *           context, g_i = clamp((n_i - low) / (high - low), 0, 1),
  *           f_i = inv_f_i * (g_i + (1 - g_i) / factor)
  *
- * with frequencies and angles in float64 and one rounding to float32.
+ * with frequencies and angles in float64, values good to 2^-36 of the
+ * amplitude, and one rounding to float32.
  * Arguments as gw_rope_cs, rot_dim at most 512; `scaling` is host memory.
  * Errors: GW_ERR_INVALID_ARG (those of gw_rope_cs, a scaling NULL or outside
- * the ranges above), GW_ERR_CUDA.  Asynchronous on `stream`.
+ * the ranges above, angles max_pos * f_i of 2^52 or more), GW_ERR_CUDA.
+ * Asynchronous on `stream`.
  */
 gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32_t head_dim, int32_t max_pos,
                             const gw_rope_scaling* scaling, void* stream);
@@ -480,7 +482,7 @@ size_t gw_attn_acc_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, 
  *   keep_idx   int32 [batch][keep_stride], keep_stride >= budget: the kept
  *              tokens' indices, ascending; entries from keep_lens[b] on are
  *              left as they were.
- *   keep_lens  int32 [batch].
+ *   keep_lens  int32 [batch], not the array seq_lens.
  *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget;
  *   batch 0 is a no-op.
  * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
@@ -604,7 +606,8 @@ size_t gw_noalloc_scratch_bytes(void);
  * cannot take the whole GPU.  The decode and prompt-row kernels here are
  * persistent with one CTA per SM (their shared memory allows no second), and
  * deal their work round-robin over the CTAs they have, so a CTA cap is an SM
- * cap: a prefill lane launched with a cap of N and a decode lane with the
+ * cap (gw_rope_rows keeps to the appends' limit; the combine, the eviction
+ * calls and gw_rope_cs_scaled are short and not capped): a prefill lane launched with a cap of N and a decode lane with the
  * SM count minus N run side by side on disjoint SMs.  Results do not depend
  * on the cap (a work unit's arithmetic never depends on which CTA runs it).
  * The setting is per host thread and is read when a call launches (for a
@@ -635,8 +638,8 @@ gw_status gw_set_early_launch(int32_t on);
  * predecessor may write.  With 1, the decode kernels compute their split plan
  * from cu_q_rows and seq_lens and fetch their first units' block-table
  * entries before that wait, which takes two dependent round trips off the
- * call; gw_kv_append likewise reads slot, pos and the RoPE table rows they
- * select before its wait, and a gw_append_decode_attn_local call the length,
+ * call; gw_kv_append and gw_rope_rows likewise read slot, pos and the RoPE
+ * table rows they select before their wait, and a gw_append_decode_attn_local call the length,
  * page and RoPE rows of the first row it appends.  KV pages, q, k, v, the workspace, out and
  * dev_status are still touched only after the wait.  The caller promises
  * that the kernel just before each call in its stream does not write that

@@ -279,7 +279,8 @@ gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32
   if (sc.kind < GW_ROPE_NONE || sc.kind > GW_ROPE_RAMP || sc.reserved != 0)
     return fail(GW_ERR_INVALID_ARG, fn, "unknown scaling kind %d, or reserved not 0", sc.kind);
   auto positive = [](double v) { return v > 0.0 && std::isfinite(v); };
-  if (!positive(sc.amplitude)) return fail(GW_ERR_INVALID_ARG, fn, "amplitude must be finite and > 0");
+  if (!(sc.amplitude >= 1e-6 && sc.amplitude <= 1e6))
+    return fail(GW_ERR_INVALID_ARG, fn, "amplitude must be in [1e-6, 1e6]");
   if (sc.kind != GW_ROPE_NONE && !positive(sc.factor))
     return fail(GW_ERR_INVALID_ARG, fn, "factor must be finite and > 0");
   if (sc.kind == GW_ROPE_NTK && head_dim <= 2) return fail(GW_ERR_INVALID_ARG, fn, "NTK needs head_dim > 2");
@@ -297,8 +298,15 @@ gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32
       g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
       f *= g + (1.0 - g) / sc.factor;
     }
-    if (!std::isfinite(f)) return fail(GW_ERR_INVALID_ARG, fn, "frequency %d is not finite", i);
-    fr.f[i] = f;
+    // beyond 2^52 a float64 angle has no fraction left
+    if (!(f * max_pos < 4503599627370496.0)) return fail(GW_ERR_INVALID_ARG, fn, "the angles of pair %d exceed 2^52", i);
+    // exact: a double's fraction has at most 53 significant bits, and those
+    // below 2^-96 of a turn do not matter over 2^31 positions
+    const double turn = f / 6.283185307179586;
+    const double hi = std::ldexp(turn - std::floor(turn), 64);
+    const double whole = std::floor(hi);
+    fr.hi[i] = static_cast<uint64_t>(whole);
+    fr.lo[i] = static_cast<uint32_t>(std::ldexp(hi - whole, 32));
   }
   return cuda_status(launch_rope_cs_scaled(rope_cs, fr, sc.amplitude, rot_dim / 2, max_pos,
                                            static_cast<cudaStream_t>(stream)),
@@ -567,6 +575,7 @@ gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch
   if (!acc || !aligned(acc, 4)) return fail(GW_ERR_INVALID_ARG, fn, "acc NULL or misaligned");
   if (!seq_lens || !keep_idx || !keep_lens || !aligned(seq_lens, 4) || !aligned(keep_idx, 4) || !aligned(keep_lens, 4))
     return fail(GW_ERR_INVALID_ARG, fn, "seq_lens/keep_idx/keep_lens NULL or misaligned");
+  if (seq_lens == keep_lens) return fail(GW_ERR_INVALID_ARG, fn, "seq_lens and keep_lens are the same array");
   if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
   SelectArgs a{};
   a.acc = acc;

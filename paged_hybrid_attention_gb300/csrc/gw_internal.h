@@ -182,10 +182,12 @@ struct RopeRowsArgs {
   int32_t early_inputs;  // gw_set_early_inputs: pos and RoPE rows read before the wait
 };
 cudaError_t launch_rope_rows(int elem, const RopeRowsArgs& a, cudaStream_t st);
-// The pairs' frequencies of gw_rope_cs_scaled, computed on the host in float64.
+// The pairs' frequencies of gw_rope_cs_scaled, computed on the host in float64:
+// turns per position modulo 1, as a 96-bit binary fraction.
 constexpr int kMaxRopePairs = 256;
 struct RopeFreqs {
-  double f[kMaxRopePairs];
+  uint64_t hi[kMaxRopePairs];
+  uint32_t lo[kMaxRopePairs];
 };
 cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amplitude, int half, int max_pos,
                                   cudaStream_t st);

@@ -7,13 +7,15 @@ namespace {
 
 // ---- select -------------------------------------------------------------------
 // The weights' order as unsigned integers: larger weight, larger key; -0 and
-// 0 share a key, and every NaN has key 0, below -inf.
+// 0 share a key, and every NaN has key 1, below -inf (0x007fffff).
 __device__ __forceinline__ uint32_t order_key(float w) {
-  uint32_t u = __float_as_uint(w);
-  if (w != w) return 0;
-  if (w == 0.f) u = 0;
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // -0 + 0 = 0
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return w != w ? 1u : k;
 }
+// Keys of no weight: a token behind the slice's end, and one at either end of
+// the sequence that is kept in any case (inf has 0xff800000).
+constexpr uint32_t kNoToken = 0, kProtected = 0xffffffffu;
 
 // A cluster of 1 to kMaxSelCtas blocks takes a sequence, each block a
 // contiguous slice of its tokens, each warp a contiguous piece of the slice, up
@@ -86,8 +88,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
       }
     }
 #pragma unroll
-    for (int r = 0; r < kSelKeys; ++r)
-      if (r < keys) key[r] = order_key(__uint_as_float(key[r]));
+    for (int r = 0; r < kSelKeys; ++r) {
+      if (r < keys) {
+        const int j = first + r * 32;
+        key[r] = j >= n ? kNoToken : j < lo || j >= hi ? kProtected : order_key(__uint_as_float(key[r]));
+      }
+    }
   };
   load(0);
   (&hist[0][0])[tid] = 0;
@@ -102,8 +108,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
       if (rounds > 1) load(round);
 #pragma unroll
       for (int r = 0; r < kSelKeys; ++r) {
-        const int j = first + r * 32;
-        if (r < keys && j < n && j >= lo && j < hi && (key[r] & mask) == prefix) atomicAdd(&h[(key[r] >> shift) & 255], 1u);
+        // key + 1 is 1 and 0 for the keys of no weight
+        if (r < keys && ((key[r] ^ prefix) & mask) == 0 && key[r] + 1 > 1) atomicAdd(&h[(key[r] >> shift) & 255], 1u);
       }
     }
     cluster_arrive();
@@ -136,13 +142,13 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     if (done) break;
   }
   // Kept for sure: the ends, and in the middle what lies above `prefix`; of the
-  // keys that match it (none if nothing of the middle is kept) the first `need`.
+  // keys that match it the first `need`.  If nothing of the middle is kept, no
+  // key but the ends' is above `last`.
+  const uint32_t last = middle ? prefix | ~mask : kProtected;
   auto ballots = [&](int r, uint32_t& sure, uint32_t& tie) {
-    const int j = first + r * 32;
-    const bool in = j < n, mid = j >= lo && j < hi;
-    const uint32_t k = key[r] & mask;
-    sure = __ballot_sync(0xffffffffu, in && (!mid || (middle && k > prefix)));
-    tie = __ballot_sync(0xffffffffu, in && mid && middle && k == prefix);
+    const uint32_t k = key[r];
+    sure = __ballot_sync(0xffffffffu, k > last || k == kProtected);
+    tie = __ballot_sync(0xffffffffu, k >= prefix && k <= last && k + 1 > 1 && middle);
   };
   auto count_warp = [&]() {  // the round's counts of this warp
     uint2 w = make_uint2(0, 0);

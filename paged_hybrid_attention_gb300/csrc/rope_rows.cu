@@ -215,16 +215,18 @@ cudaError_t launch_rows(const RopeRowsArgs& a, cudaStream_t st) {
 }
 
 // ---- table --------------------------------------------------------------------
-// Entry (p, i) is amplitude * e^(i p f_i).  Float64 sine and cosine are slow
-// here (the FP64 pipes of this GPU have about 1/60 of the FP32 rate), so a
-// block computes two per pair, e^(i f) and e^(i p0 f) at its first position
-// p0, and gets the rest by complex products, e^(i (p+k) f) = e^(i p f) e^(i k f),
-// in pairs of floats (value = hi + lo, about 48 bits; products split exactly by
-// a fused multiply-add, sums by the two-sum).  A product adds an error of about
-// 2^-46 and squaring doubles what is there, so over a block's at most 512
-// positions the values stay good to 2^-38, and each is rounded once to float32.
-// 262144 x 64 entries take 35 us (134 MB, the floor 20 us): about forty FP32
-// operations an entry bound it, after a start of float64 sines.
+// Entry (p, i) is amplitude * e^(i p f_i).  The FP64 pipes of this GPU have
+// about 1/60 of the FP32 rate, so nothing here is float64: angles are 64-bit
+// fractions of a turn, whose products wrap as angles do, and values are pairs
+// of floats (hi + lo, about 48 bits; products split exactly by a fused
+// multiply-add, sums by the two-sum).  A thread takes e^(i p f) at the first of
+// its positions by Taylor series and gets the others by complex products with
+// e^(i f) and e^(4 i f).  A series and a product are each good to about 2^-45,
+// and over the up to 32 products of a chain the values stay good to 2^-39; each
+// is rounded once to float32.
+// 262144 x 64 entries take 33 us (134 MB, the floor 20 us), 32768 x 128 15 us:
+// about forty FP32 operations an entry bound it, and at the start of a thread
+// some 700 more.
 struct Ff {
   float h, l;
 };
@@ -232,70 +234,116 @@ struct Cplx {
   Ff re, im;
 };
 
-__device__ __forceinline__ Ff split(double v) {
-  const float h = __double2float_rn(v);
-  return Ff{h, __double2float_rn(v - static_cast<double>(h))};
+__host__ __device__ constexpr Ff split(double v) {
+  const float h = static_cast<float>(v);
+  return Ff{h, static_cast<float>(v - static_cast<double>(h))};
 }
 
-// a b + sign c d in pairs of floats, sign = +-1
+// s = a + b and its rounding error
+__device__ __forceinline__ float two_sum(float a, float b, float& err) {
+  const float s = __fadd_rn(a, b);
+  const float v = __fsub_rn(s, a);
+  err = __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v));
+  return s;
+}
+
+__device__ __forceinline__ Ff renorm(float s, float low) {
+  const float h = __fadd_rn(s, low);
+  return Ff{h, __fsub_rn(low, __fsub_rn(h, s))};
+}
+
+// a b + c in pairs of floats
+__device__ __forceinline__ Ff mul_add(const Ff& a, const Ff& b, const Ff& c) {
+  const float p = __fmul_rn(a.h, b.h);
+  float low = __fmaf_rn(a.h, b.h, -p);
+  low = __fmaf_rn(a.h, b.l, low);
+  low = __fmaf_rn(a.l, b.h, low);
+  float err;
+  const float s = two_sum(p, c.h, err);
+  return renorm(s, __fadd_rn(__fadd_rn(err, low), c.l));
+}
+
+// a b + SIGN c d in pairs of floats, SIGN = +-1
 template <int SIGN>
 __device__ __forceinline__ Ff dot2(const Ff& a, const Ff& b, const Ff& c, const Ff& d) {
   const float ch = SIGN > 0 ? c.h : -c.h, cl = SIGN > 0 ? c.l : -c.l;
   const float p = __fmul_rn(a.h, b.h), q = __fmul_rn(ch, d.h);
-  float low = __fadd_rn(__fmaf_rn(a.h, b.h, -p), __fmaf_rn(ch, d.h, -q));
-  const float s = __fadd_rn(p, q);
-  const float v = __fsub_rn(s, p);
-  low = __fadd_rn(low, __fadd_rn(__fsub_rn(p, __fsub_rn(s, v)), __fsub_rn(q, v)));
+  float err;
+  const float s = two_sum(p, q, err);
+  float low = __fadd_rn(__fadd_rn(__fmaf_rn(a.h, b.h, -p), __fmaf_rn(ch, d.h, -q)), err);
   low = __fmaf_rn(a.h, b.l, low);
   low = __fmaf_rn(a.l, b.h, low);
   low = __fmaf_rn(ch, d.l, low);
   low = __fmaf_rn(cl, d.h, low);
-  const float h = __fadd_rn(s, low);
-  return Ff{h, __fsub_rn(low, __fsub_rn(h, s))};
+  return renorm(s, low);
 }
 
 __device__ __forceinline__ Cplx mul(const Cplx& a, const Cplx& b) {
   return Cplx{dot2<-1>(a.re, b.re, a.im, b.im), dot2<1>(a.re, b.im, a.im, b.re)};
 }
 
+// p * f as a fraction of a turn in units of 2^-64, from f's 96-bit fraction.
+__device__ __forceinline__ uint64_t turns(uint32_t p, const RopeFreqs& fr, int i) {
+  return p * fr.hi[i] + __umulhi(p, fr.lo[i]);
+}
+
+// e^(2 pi i x), x a fraction of a turn in units of 2^-64, good to about 2^-45.
+// With k the nearest quarter turn, y = 2 pi (x - k/4) has |y| < 0.79, and the
+// series of
+//   sin y = y + y z (-1/3! + z (1/5! - ...)),  cos y = 1 + z (-1/2! + z (...)),
+// z = y^2, are cut behind y^15 and y^16 (the next terms are below 2^-54 and
+// 2^-58).  The terms from z^4 on are below 2^-17, where plain floats do.
+__device__ __forceinline__ Cplx unit(uint64_t x) {
+  const int k = static_cast<int>((x + (1ull << 61)) >> 62);
+  const int64_t r = static_cast<int64_t>(x - (static_cast<uint64_t>(k) << 62));  // in [-2^61, 2^61)
+  const float rh = __ll2float_rn(r);
+  const Ff frac{rh, __ll2float_rn(r - __float2ll_rn(rh))};
+  constexpr Ff kUnit = split(6.283185307179586 / 18446744073709551616.0);  // 2 pi 2^-64
+  const Ff y = mul_add(frac, kUnit, Ff{0.f, 0.f});
+  const Ff z = mul_add(y, y, Ff{0.f, 0.f});
+  constexpr Ff kOne{1.f, 0.f};
+  constexpr Ff kS1 = split(-1.0 / 6), kS2 = split(1.0 / 120), kS3 = split(-1.0 / 5040);
+  constexpr Ff kC1 = split(-1.0 / 2), kC2 = split(1.0 / 24), kC3 = split(-1.0 / 720);
+  constexpr float kS4 = 1.0 / 362880, kS5 = -1.0 / 39916800, kS6 = 1.0 / 6227020800.0, kS7 = -1.0 / 1307674368000.0;
+  constexpr float kC4 = 1.0 / 40320, kC5 = -1.0 / 3628800, kC6 = 1.0 / 479001600, kC7 = -1.0 / 87178291200.0,
+                  kC8 = 1.0 / 20922789888000.0;
+  const float ts = fmaf(z.h, fmaf(z.h, fmaf(z.h, kS7, kS6), kS5), kS4);
+  const float tc = fmaf(z.h, fmaf(z.h, fmaf(z.h, fmaf(z.h, kC8, kC7), kC6), kC5), kC4);
+  Ff ps = mul_add(z, Ff{ts, 0.f}, kS3);
+  ps = mul_add(z, ps, kS2);
+  ps = mul_add(z, ps, kS1);
+  const Ff sn = mul_add(mul_add(y, z, Ff{0.f, 0.f}), ps, y);
+  Ff pc = mul_add(z, Ff{tc, 0.f}, kC3);
+  pc = mul_add(z, pc, kC2);
+  pc = mul_add(z, pc, kC1);
+  const Ff cs = mul_add(z, pc, kOne);
+  const Ff a = k & 1 ? sn : cs, b = k & 1 ? cs : sn;
+  const float sa = k == 1 || k == 2 ? -1.f : 1.f, sb = k >= 2 ? -1.f : 1.f;  // k in [0, 3]
+  return Cplx{Ff{sa * a.h, sa * a.l}, Ff{sb * b.h, sb * b.l}};
+}
+
 constexpr int kTableThreads = 256;
-constexpr int kMaxRuns = 8;
+constexpr int kMaxRun = 128;
 
 // Thread (pair i, run r) writes the `run` positions from p0 + r * run on, four
 // chains of every fourth position at a time.
-__global__ void __launch_bounds__(kTableThreads, 4)
-    rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, double amplitude, int half, int run, int runs, int max_pos) {
-  __shared__ Cplx s_base[kMaxRopePairs], s_w[kMaxRopePairs], s_w4[kMaxRopePairs], s_run[kMaxRopePairs];
+__global__ void __launch_bounds__(kTableThreads, 3)
+    rope_cs_scaled_kernel(float2* out, const RopeFreqs fr, float amp_h, float amp_l, int half, int run, int runs, int max_pos) {
+  __shared__ Cplx s_w[2 * kMaxRopePairs];  // e^(i f), then e^(4 i f)
   pdl_wait();
   pdl_trigger();
   const int t = threadIdx.x;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * run * runs;
-  for (int job = t; job < 2 * half; job += kTableThreads) {
-    double s, c;
-    if (job < half) {
-      sincos(fr.f[job], &s, &c);
-      Cplx w{split(c), split(s)};
-      s_w[job] = w;
-      for (int k = 1; k < run; k *= 2) {
-        w = mul(w, w);
-        if (k == 2) s_w4[job] = w;
-      }
-      s_run[job] = w;
-    } else {
-      const int i = job - half;
-      sincos(static_cast<double>(p0) * fr.f[i], &s, &c);
-      s_base[i] = Cplx{split(c * amplitude), split(s * amplitude)};
-    }
-  }
+  for (int job = t; job < 2 * half; job += kTableThreads)
+    s_w[job] = unit(job < half ? turns(1, fr, job) : turns(4, fr, job - half));
   __syncthreads();
   const int r = t / half, i = t - r * half;
-  if (r >= runs) return;
-  const int64_t first = p0 + static_cast<int64_t>(r) * run;
-  if (first >= max_pos) return;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * runs + r) * run;
+  if (r >= runs || first >= max_pos) return;
   Cplx z[4];
-  z[0] = s_base[i];
-  for (int k = 0; k < r; ++k) z[0] = mul(z[0], s_run[i]);
-  const Cplx w = s_w[i], w4 = s_w4[i];
+  z[0] = unit(turns(static_cast<uint32_t>(first), fr, i));
+  const Ff amp{amp_h, amp_l}, zero{0.f, 0.f};
+  z[0] = Cplx{mul_add(z[0].re, amp, zero), mul_add(z[0].im, amp, zero)};
+  const Cplx w = s_w[i], w4 = s_w[half + i];
 #pragma unroll
   for (int k = 1; k < 4; ++k) z[k] = mul(z[k - 1], w);
   float2* o = out + first * half + i;
@@ -319,13 +367,16 @@ cudaError_t launch_rope_rows(int elem, const RopeRowsArgs& a, cudaStream_t st) {
 
 cudaError_t launch_rope_cs_scaled(float* out, const RopeFreqs& freqs, double amplitude, int half, int max_pos,
                                   cudaStream_t st) {
-  // Long runs need fewer float64 sines, short ones keep every SM busy.
-  const int runs = kTableThreads / half < kMaxRuns ? kTableThreads / half : kMaxRuns;
-  int run = 64;
-  while (run > 16 && max_pos < static_cast<int64_t>(run) * runs * 2 * grid_ctas()) run /= 2;
-  const unsigned blocks = (max_pos + run * runs - 1) / (run * runs);
+  // Long runs need fewer series, short ones keep every SM busy.  kMaxRopePairs
+  // is kTableThreads, so a block has at least one run of every pair.
+  static_assert(kMaxRopePairs <= kTableThreads, "a thread per pair");
+  const int runs = kTableThreads / half;
+  int run = kMaxRun;
+  while (run > 32 && max_pos < static_cast<int64_t>(run) * runs * 4 * grid_ctas()) run /= 2;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(max_pos) - 1) / (run * runs) + 1);
+  const Ff amp = split(amplitude);
   return launch_pdl(rope_cs_scaled_kernel, dim3(blocks), dim3(kTableThreads), 0, st, reinterpret_cast<float2*>(out),
-                    freqs, amplitude, half, run, runs, max_pos);
+                    freqs, amp.h, amp.l, half, run, runs, max_pos);
 }
 
 }  // namespace gw

@@ -22,7 +22,7 @@ def _select(acc=1 << 24, stride=1000, batch=4, lens=1 << 24, budget=100, sinks=4
     dict(batch=-1), dict(batch=65536), dict(budget=0), dict(budget=-1), dict(sinks=-1), dict(recent=-1),
     dict(sinks=90, recent=11), dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1), dict(stride=0), dict(stride=(1 << 40) + 1),
     dict(idx_stride=99), dict(idx_stride=(1 << 40) + 1), dict(acc=0), dict(acc=(1 << 24) + 2), dict(lens=0),
-    dict(lens=(1 << 24) + 1), dict(idx=0), dict(idx=(1 << 25) + 2), dict(n=0), dict(n=(1 << 26) + 3),
+    dict(lens=(1 << 24) + 1), dict(idx=0), dict(idx=(1 << 25) + 2), dict(n=0), dict(n=(1 << 26) + 3), dict(n=1 << 24),
     dict(status=(1 << 24) + 2),
 ])
 def test_select_refuses(bad):

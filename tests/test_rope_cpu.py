@@ -51,7 +51,7 @@ def _table(cs=1 << 24, theta=1e4, rot=128, dim=512, max_pos=10, scaling=True, **
 @pytest.mark.parametrize("bad", [
     dict(cs=0), dict(cs=(1 << 24) + 8), dict(theta=0.0), dict(theta=float("inf")), dict(theta=float("nan")),
     dict(rot=0), dict(rot=127), dict(rot=514, dim=1024), dict(rot=256, dim=128), dict(max_pos=0), dict(scaling=False),
-    dict(kind=4), dict(kind=-1), dict(reserved=1), dict(amplitude=0.0), dict(amplitude=float("inf")),
+    dict(kind=4), dict(kind=-1), dict(reserved=1), dict(amplitude=0.0), dict(amplitude=float("inf")), dict(amplitude=1e-7), dict(theta=1e-200, rot=512),
     dict(kind=1, factor=0.0), dict(kind=1, factor=float("nan")), dict(kind=2, factor=-1.0), dict(kind=2, rot=2, dim=2),
     dict(kind=3, low=-1.0), dict(kind=3, low=32.0), dict(kind=3, high=float("inf")), dict(kind=3, orig_max_pos=0.0),
     dict(kind=1, factor=5e-324),                                              # a frequency overflows

@@ -42,6 +42,7 @@ class Cache:
         self.table = torch.full((len(lens), self.width), -7, dtype=torch.int32)
         used = torch.zeros(n_pages, 16, dtype=torch.bool)
         at = 0
+        values = data.float()
         self.tokens = []
         for b, n in enumerate(lens):
             p = perm[at:at + need[b]]
@@ -50,7 +51,7 @@ class Cache:
             self.table[b, :m] = p[:m].int()
             t = torch.arange(max(n, 0))
             used[p[t // 16], t % 16] = True
-            self.tokens.append(data.float()[p].reshape(-1, row)[:max(n, 0)].double())
+            self.tokens.append(values[p].reshape(-1, row)[:max(n, 0)].double())
         raw = data.view(torch.uint8) if kind != torch.bfloat16 else data.view(torch.int16)
         raw[~used] = 0x7f if kind != torch.bfloat16 else 0x7fc0                 # NaN
         raw = raw.view(n_pages, 2, 8, row // blk, blk).permute(0, 1, 3, 2, 4).contiguous()
@@ -231,6 +232,42 @@ def test_wide_workspace_offsets():
     out, lse = c.run(acc)
     assert int(c.status) == 0
     c.check(out, lse, acc, torch.zeros_like(acc))
+
+
+def test_pages_beyond_4_gib():
+    """Page offsets past 32 bits: the same rows at the end of a 6 GB pool."""
+    c = Cache("folded", [900, 64, 1], 8)
+    acc = c.new_acc()
+    out, lse = c.run(acc)
+    small = c.pool
+    big = gw.KVPool("folded", "bf16", 300000)
+    off = big.num_pages - small.num_pages
+    assert off * big.page_bytes > 2 ** 32
+    big.data[off * big.page_bytes:].copy_(small.data)
+    c.pool, c.bt = big, torch.where(c.bt >= 0, c.bt + off, c.bt)
+    acc2 = c.new_acc()
+    out2, lse2 = c.run(acc2)
+    assert torch.equal(out2, out) and torch.equal(lse2, lse) and torch.equal(acc2, acc)
+    keep = torch.arange(0, 900, 3, dtype=torch.int32, device="cuda").view(1, 300).repeat(3, 1)
+    n = G.i32([300, 22, 1])
+    before = big.data[off * big.page_bytes:].clone()
+    for pool, table in ((small, c.bt - off), (big, c.bt)):
+        gw.kv_evict_compact(pool, torch.where(c.bt >= 0, table, c.bt), c.n, keep, n, dev_status=c.status)
+    assert int(c.status) == 0
+    assert torch.equal(big.data[off * big.page_bytes:], small.data) and not torch.equal(before, small.data)
+
+
+def test_largest_batch():
+    """4096 sequences, the most that a call takes."""
+    lens = [1 + b % 23 for b in range(4096)]
+    c = Cache("folded", lens, 8)
+    acc = c.new_acc()
+    out, lse = c.run(acc)
+    assert int(c.status) == 0
+    some = [0, 1, 22, 23, 2047, 4000, 4094, 4095]
+    c.rows = [1 if b in some else 0 for b in range(4096)]
+    c.check(out, lse, acc, torch.zeros_like(acc))
+    assert bool(((acc.double().sum(1) - 8).abs() < 1e-4).all())
 
 
 def test_graph_streams_and_launch_settings():

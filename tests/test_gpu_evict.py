@@ -242,6 +242,35 @@ def test_compact_refuses_bad_values():
     assert int(c.status) == gw.GW_DEV_KEEP_RANGE and torch.equal(c.pool.data.cpu(), mid)
 
 
+def test_largest_batches():
+    """65535 sequences, the most that a call takes."""
+    batch = 65535
+    acc = _weights("tail", batch, 9)
+    lens = torch.arange(batch, dtype=torch.int32, device="cuda") % 10
+    keep = torch.full((batch, 4), -9, dtype=torch.int32, device="cuda")
+    n = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    gw.kv_evict_select(acc, lens, 4, keep, n, 1, 1)
+    assert torch.equal(n, lens.clamp(max=4))
+    w, k = acc.cpu().double().numpy(), keep.cpu().numpy()
+    for b in [*range(0, 40), *range(batch - 40, batch)]:
+        L = b % 10
+        assert k[b, :min(L, 4)].tolist() == _choose(w[b].tolist(), L, 4, 1, 1)
+    pool = gw.KVPool("folded_e4m3", "e4m3", batch)
+    rows = pool.data.view(batch, 2, 40, 8, 16)
+    rows.copy_(torch.arange(16, dtype=torch.uint8, device="cuda").view(2, 1, 8, 1).expand(2, 40, 8, 16))
+    table = torch.arange(batch, dtype=torch.int32, device="cuda").flip(0).view(batch, 1).contiguous()
+    wide = torch.zeros(batch, 16, device="cuda")
+    wide[:, :9] = acc
+    gw.kv_evict_compact(pool, table, lens, keep, n, wide)
+    got = rows[table[:, 0].long()][:, 0, 7, :4, 3].int()        # the token that lies in each of the first four places
+    place = torch.arange(4, device="cuda")
+    assert torch.equal(got, torch.where(place < n[:, None], keep, place.int()))
+    want, every = torch.zeros(batch, 16, device="cuda"), torch.arange(16, device="cuda")
+    want[:, :9] = torch.where(every[:9] < lens[:, None], want[:, :9], acc)         # behind the end: as it was
+    want[:, :4] = torch.where(place < n[:, None], acc.gather(1, keep.clamp(min=0).long()), want[:, :4])
+    assert torch.equal(wide, want)
+
+
 def test_binding_refuses():
     c = Cache("folded", [20], 8)
     keep, n = _keep_tensor([[1, 2]], 4), G.i32([2])

@@ -138,6 +138,24 @@ def test_half_pairs_are_the_appends_bits():
         assert torch.equal(stored(), z)
 
 
+def test_rows_and_tables_beyond_2_31_elements():
+    rows, heads, dim = 70001, 64, 512
+    assert rows * heads * dim > 2 ** 31
+    x = torch.ones(1, heads, dim, dtype=torch.bfloat16, device="cuda").expand(rows, heads, dim)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") % 1000
+    cs = gw.rope_cs_scaled(1e6, 128, dim, 1000)
+    y = gw.rope_rows(x, pos, cs, rot_dim=128)
+    last = slice(rows - 3, rows)
+    _check(y[last], x[last], pos[last], cs, 128, False, False)
+    del y
+    max_pos, half = 9000001, 128
+    assert max_pos * half * 2 > 2 ** 31
+    got = gw.rope_cs_scaled(1e4, 2 * half, 256, max_pos)[-2:].double().cpu().numpy()
+    ang = np.arange(max_pos - 2, max_pos, dtype=np.float64)[:, None] * _freq(1e4, 2 * half, 256, "none", 1, 0, 0, 0)
+    want = np.stack([np.cos(ang), np.sin(ang)], -1)
+    assert np.all(np.abs(got - want) <= 2.0 ** -24 * np.abs(want) * (1 + 2.0 ** -20) + 2.0 ** -51 * ang[..., None] + 2.0 ** -36)
+
+
 def test_bad_positions_leave_their_rows():
     x, _, cs = _inputs(6, 2, 64, 64, "bf16", 10)
     pos = G.i32([0, -1, 9, 10, 2 ** 31 - 1, 3])

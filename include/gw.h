@@ -11,6 +11,11 @@
  *                            the compressed V + k_rot pool (K rebuilt on chip)
  *                            or over a full K + V control pool.
  *
+ * and, beside the step, the rotation of q rows and tables for scaled contexts
+ * (gw_rope_rows, gw_rope_cs_scaled), and the eviction of a global cache by the
+ * attention its tokens draw (gw_decode_attn_global_acc, gw_kv_evict_select,
+ * gw_kv_evict_compact), which the pages do not have.
+ *
  * Sources of the operations (page title, section):
  *   [pegainfer] "Gemma 4" (pegainfer model page): intro, "Scheduling",
  *               "Architecture notes".  Five of six layers are sliding-window

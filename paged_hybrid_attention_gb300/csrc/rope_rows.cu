@@ -40,16 +40,54 @@ __device__ __forceinline__ void rotate(float& x0, float& x1, float c, float s) {
   x1 = y1;
 }
 
-// N elements in one access.
-template <class T, int N>
-struct alignas(sizeof(T) * N) Pack {
-  T v[N];
+// VB bytes of elements in one access, and as floats: two 16-bit elements are
+// packed by one conversion.
+template <int ELEM, int VB>
+struct alignas(VB) Chunk {
+  using E = Elem<ELEM>;
+  using T = typename E::T;
+  static constexpr int kE = VB / static_cast<int>(sizeof(T));
+  T v[kE];
+  __device__ __forceinline__ void get(float (&f)[kE]) const {
+    if constexpr (ELEM == GW_ELEM_F32 || kE == 1) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) f[i] = E::get(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; i += 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&v[i]);
+        if constexpr (ELEM == GW_ELEM_BF16) {
+          f[i] = __uint_as_float(w << 16);
+          f[i + 1] = __uint_as_float(w & 0xffff0000u);
+        } else {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+          f[i] = x.x;
+          f[i + 1] = x.y;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[kE]) {
+    if constexpr (ELEM == GW_ELEM_F32 || kE == 1) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] = E::put(f[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; i += 2) {
+        if constexpr (ELEM == GW_ELEM_BF16)
+          *reinterpret_cast<__nv_bfloat162*>(&v[i]) = __floats2bfloat162_rn(f[i], f[i + 1]);
+        else
+          *reinterpret_cast<__half2*>(&v[i]) = __floats2half2_rn(f[i], f[i + 1]);
+      }
+    }
+  }
 };
 
-// How a call's rows are dealt to threads.
+// How a call's rows are dealt to threads.  A thread keeps its item and so its
+// (cos, sin) entries for all heads of its row that it takes, which leaves the
+// rows themselves as the only traffic beyond L1.
 struct RowsPlan {
-  int per_head;  // items of a (row, head): rot_items rotations, then copies
-  int rot_items;
+  int per_head;  // items of a (row, head)
   int lanes;     // heads that a block takes at a time: thread t has item t % per_head of head t / per_head
   int sweeps;    // times it takes `lanes` heads
   int groups;    // blocks' tasks per row
@@ -60,28 +98,22 @@ struct RowsPlan {
 template <int ELEM, int VB>
 constexpr int kRowThreads = (ELEM == GW_ELEM_F32 ? 4096 : 2048) / VB > 256 ? (ELEM == GW_ELEM_F32 ? 4096 : 2048) / VB : 256;
 
-// An item is the pairs of one VB-byte access (half pairs: of two, one in each
-// half of the rotated dims), or as many copied elements.  A thread keeps its
-// item and so its (cos, sin) entries for all heads of its row that it takes,
-// which leaves the rows themselves as the only traffic beyond L1.  VB is the
-// widest access that pointers, strides and the widths of the two parts allow:
-// 16 bytes where the model's dims are multiples of 8.
-// Bound by memory: 8192 x 32 x 512 bf16 rows with 128 interleaved dims rotated
-// take 91 us for 541 MB (5.9 TB/s, 0.87 of a copy), 4093 x 16 x 256 fp32 rows
-// 25 us for 138 MB.  Two accesses in flight per thread and 32 warps per SM are
-// the best of the mixes: 4 in flight with 24 or fewer warps 102 us, 1 with 48
-// warps 104 us; separate loops for rotated and copied items 121 us, since a
-// head's 16 + 48 items share warps.
+// In place, and out of place where all of a head rotates: an item is the pairs
+// of one VB-byte access (half pairs: of two, one in each half of the rotated
+// dims).  Bound by memory: 8192 x 32 x 512 bf16 rows, all dims rotated, take 82
+// to 85 us for 541 MB (0.94 to 0.97 of a copy), 4093 x 16 x 256 fp32 rows 24.6 us
+// for 138 MB.  Interleaved pairs have one access an item and keep four in
+// flight (two: 94 us), half pairs two of two (three: 87 us).
 template <int ELEM, bool INTER, int VB>
 __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<ELEM, VB>)
-    rope_rows_kernel(const RopeRowsArgs a, const RowsPlan p) {
+    rope_pairs_kernel(const RopeRowsArgs a, const RowsPlan p) {
   using E = Elem<ELEM>;
   using T = typename E::T;
   constexpr int kE = VB / static_cast<int>(sizeof(T));        // elements per access
   constexpr bool kTwo = !INTER || kE == 1;                    // the pairs' elements come from two accesses
   constexpr int kP = kTwo ? kE : kE / 2;                      // pairs per item
-  constexpr int kUn = 2;
-  using V = Pack<T, kE>;
+  constexpr int kUn = kTwo ? 2 : 4;
+  using V = Chunk<ELEM, VB>;
   bool waited = a.early_inputs == 0;  // pos and the table rows may be read before the wait
   auto pass = [&]() {
     if (!waited) {
@@ -96,9 +128,8 @@ __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<E
   }
   const int half = a.rot_dim / 2;
   const int t = threadIdx.x, item = t % p.per_head, lane = t / p.per_head;
-  const bool rotates = item < p.rot_items;
   // offsets of the item's accesses within a head
-  const int d0 = !rotates ? a.rot_dim + (item - p.rot_items) * kE : INTER ? 2 * kP * item : kP * item;
+  const int d0 = INTER ? 2 * kP * item : kP * item;
   const int d1 = INTER ? d0 + 1 : d0 + half;
   for (int64_t task = blockIdx.x; task < p.tasks; task += gridDim.x) {
     const int64_t row = task / p.groups;
@@ -113,30 +144,26 @@ __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<E
     const T* x = static_cast<const T*>(a.x) + row * a.x_row;
     T* y = static_cast<T*>(a.y) + row * a.y_row;
     float c[kP], s[kP];
-    if (rotates) {
-      const float* cs = a.rope_cs + (static_cast<int64_t>(pos) * half + kP * item) * 2;
-      if constexpr (kP == 1) {
-        const float2 e = *reinterpret_cast<const float2*>(cs);
-        c[0] = e.x;
-        s[0] = e.y;
-      } else {
+    const float* cs = a.rope_cs + (static_cast<int64_t>(pos) * half + kP * item) * 2;
+    if constexpr (kP == 1) {
+      const float2 e = *reinterpret_cast<const float2*>(cs);
+      c[0] = e.x;
+      s[0] = e.y;
+    } else {
 #pragma unroll
-        for (int i = 0; i < kP; i += 2) {
-          const float4 e = *reinterpret_cast<const float4*>(cs + 2 * i);
-          c[i] = e.x;
-          s[i] = e.y;
-          c[i + 1] = e.z;
-          s[i + 1] = e.w;
-        }
-      }
-      if (a.inverse) {
-#pragma unroll
-        for (int i = 0; i < kP; ++i) s[i] = -s[i];
+      for (int i = 0; i < kP; i += 2) {
+        const float4 e = *reinterpret_cast<const float4*>(cs + 2 * i);
+        c[i] = e.x;
+        s[i] = e.y;
+        c[i + 1] = e.z;
+        s[i + 1] = e.w;
       }
     }
+    if (a.inverse) {
+#pragma unroll
+      for (int i = 0; i < kP; ++i) s[i] = -s[i];
+    }
     pass();
-    // rotated and copied items share the accesses, so that a warp that holds
-    // both runs them once
     for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
       V v0[kUn], v1[kUn];
 #pragma unroll
@@ -145,7 +172,7 @@ __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<E
         if (k0 + k < p.sweeps && h < a.num_heads) {
           const T* from = x + h * a.x_head;
           v0[k] = *reinterpret_cast<const V*>(from + d0);
-          if (kTwo && rotates) v1[k] = *reinterpret_cast<const V*>(from + d1);
+          if constexpr (kTwo) v1[k] = *reinterpret_cast<const V*>(from + d1);
         }
       }
 #pragma unroll
@@ -153,18 +180,19 @@ __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<E
         const int h = h0 + (k0 + k) * p.lanes;
         if (k0 + k < p.sweeps && h < a.num_heads) {
           T* to = y + h * a.y_head;
-          if (rotates) {
+          float f[kE], g[kE];
+          v0[k].get(f);
+          if constexpr (kTwo) {
+            v1[k].get(g);
 #pragma unroll
-            for (int i = 0; i < kP; ++i) {
-              T& e0 = kTwo ? v0[k].v[i] : v0[k].v[(2 * i) % kE];
-              T& e1 = kTwo ? v1[k].v[i] : v0[k].v[(2 * i + 1) % kE];
-              float x0 = E::get(e0), x1 = E::get(e1);
-              rotate(x0, x1, c[i], s[i]);
-              e0 = E::put(x0);
-              e1 = E::put(x1);
-            }
-            if (kTwo) *reinterpret_cast<V*>(to + d1) = v1[k];
+            for (int i = 0; i < kP; ++i) rotate(f[i], g[i], c[i], s[i]);
+            v1[k].put(g);
+            *reinterpret_cast<V*>(to + d1) = v1[k];
+          } else {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) rotate(f[(2 * i) % kE], f[(2 * i + 1) % kE], c[i], s[i]);
           }
+          v0[k].put(f);
           *reinterpret_cast<V*>(to + d0) = v0[k];
         }
       }
@@ -173,44 +201,202 @@ __global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<E
   pass();
 }
 
-template <int ELEM, int VB>
-cudaError_t launch_rows_vb(const RopeRowsArgs& a, cudaStream_t st) {
-  constexpr int kE = VB / (ELEM == GW_ELEM_F32 ? 4 : 2);
-  const bool inter = a.pairs == GW_PAIRS_INTERLEAVED;
-  RowsPlan p{};
-  p.rot_items = inter && kE > 1 ? a.rot_dim / kE : a.rot_dim / 2 / kE;
-  p.per_head = p.rot_items + (a.inplace ? 0 : (a.head_dim - a.rot_dim) / kE);
+// Out of place, an item can be any aligned chunk of a head: it loads the
+// partners of its elements beside them and writes only itself, so that heads
+// fall into equal items however their parts are cut.  An element turns by
+// y = x c + x' s', with s' = -s for the first of a pair and s for the second,
+// which is the pair's arithmetic bit for bit.  Half pairs whose distance is no
+// whole number of chunks take their partners one by one (from L1: they are some
+// other thread's chunk).
+enum { kInterleaved, kHalfChunks, kHalfScattered };
+
+template <int ELEM, int KIND, int VB>
+__global__ void __launch_bounds__(kRowThreads<ELEM, VB>, 4 * 256 / kRowThreads<ELEM, VB>)
+    rope_chunks_kernel(const RopeRowsArgs a, const RowsPlan p) {
+  using E = Elem<ELEM>;
+  using T = typename E::T;
+  constexpr int kE = VB / static_cast<int>(sizeof(T));
+  constexpr bool INTER = KIND == kInterleaved;
+  constexpr bool kInside = INTER && kE > 1;     // partners lie in the same chunk
+  constexpr bool kWhole = KIND == kHalfChunks;  // the partners are a chunk themselves
+  constexpr int kUn = KIND == kHalfScattered ? 1 : KIND == kHalfChunks ? 2 : 4;
+  using V = Chunk<ELEM, VB>;
+  bool waited = a.early_inputs == 0;  // pos and the table rows may be read before the wait
+  auto pass = [&]() {
+    if (!waited) {
+      pdl_wait();
+      pdl_trigger();
+      waited = true;
+    }
+  };
+  if (waited) {
+    pdl_wait();
+    pdl_trigger();
+  }
+  const int half = a.rot_dim / 2;
+  const int t = threadIdx.x, item = t % p.per_head, lane = t / p.per_head;
+  const int d0 = item * kE;
+  const bool rotates = d0 < a.rot_dim;
+  // element d's pair and partner
+  auto pair_of = [&](int d) { return INTER ? d / 2 : d < half ? d : d - half; };
+  auto partner_of = [&](int d) { return INTER ? d ^ 1 : d < half ? d + half : d - half; };
+  for (int64_t task = blockIdx.x; task < p.tasks; task += gridDim.x) {
+    const int64_t row = task / p.groups;
+    const int h0 = static_cast<int>(task - row * p.groups) * p.lanes * p.sweeps + lane;
+    const int32_t pos = a.pos[row];
+    if (pos < 0 || pos >= a.max_pos) {
+      pass();
+      if (t == 0 && task == row * p.groups) set_status(a.status, GW_DEV_POS_RANGE);
+      continue;
+    }
+    if (lane >= p.lanes) continue;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+    T* y = static_cast<T*>(a.y) + row * a.y_row;
+    float c[kE], s[kE];
+    if (rotates) {
+      const float* cs = a.rope_cs + static_cast<int64_t>(pos) * a.rot_dim;
+      if constexpr (kE > 1 && kWhole) {
+        const int i0 = pair_of(d0);
+#pragma unroll
+        for (int i = 0; i + 1 < kE; i += 2) {
+          const float4 e = *reinterpret_cast<const float4*>(cs + 2 * (i0 + i));
+          c[i] = e.x;
+          s[i] = e.y;
+          c[i + 1] = e.z;
+          s[i + 1] = e.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kE; i += kInside ? 2 : 1) {
+          if (d0 + i < a.rot_dim) {
+            const float2 e = *reinterpret_cast<const float2*>(cs + 2 * pair_of(d0 + i));
+            c[i] = e.x;
+            s[i] = e.y;
+            if (kInside) {
+              c[(i + 1) % kE] = e.x;
+              s[(i + 1) % kE] = e.y;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kE; ++i) {
+        const bool first = INTER ? (d0 + i) % 2 == 0 : d0 + i < half;
+        if (first != (a.inverse != 0)) s[i] = -s[i];
+      }
+    }
+    pass();
+    for (int k0 = 0; k0 < p.sweeps; k0 += kUn) {
+      V v[kUn], w[kUn];
+#pragma unroll
+      for (int k = 0; k < kUn; ++k) {
+        const int h = h0 + (k0 + k) * p.lanes;
+        if (k0 + k < p.sweeps && h < a.num_heads) {
+          const T* from = x + h * a.x_head;
+          v[k] = *reinterpret_cast<const V*>(from + d0);
+          if (!kInside && rotates) {
+            if constexpr (kWhole) {
+              w[k] = *reinterpret_cast<const V*>(from + partner_of(d0));
+            } else {
+#pragma unroll
+              for (int i = 0; i < kE; ++i)
+                if (d0 + i < a.rot_dim) w[k].v[i] = from[partner_of(d0 + i)];
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUn; ++k) {
+        const int h = h0 + (k0 + k) * p.lanes;
+        if (k0 + k < p.sweeps && h < a.num_heads) {
+          V out = v[k];
+          if (rotates) {
+            float f[kE], g[kE], r[kE];
+            v[k].get(f);
+            if constexpr (!kInside) w[k].get(g);
+#pragma unroll
+            for (int i = 0; i < kE; ++i)
+              r[i] = __fadd_rn(__fmul_rn(f[i], c[i]), __fmul_rn(kInside ? f[i ^ 1] : g[i], s[i]));
+            out.put(r);
+            if (d0 + kE > a.rot_dim) {  // the chunk in which the rotated part ends
+#pragma unroll
+              for (int i = 0; i < kE; ++i)
+                if (d0 + i >= a.rot_dim) out.v[i] = v[k].v[i];
+            }
+          }
+          *reinterpret_cast<V*>(y + h * a.y_head + d0) = out;
+        }
+      }
+    }
+  }
+  pass();
+}
+
+// Deals a call's rows to blocks, per_head given; returns a block's threads.
+int plan_rows(const RopeRowsArgs& a, int sweeps, RowsPlan& p) {
   const int block = p.per_head <= 256 ? 256 : (p.per_head + 31) / 32 * 32;
   p.lanes = block / p.per_head < a.num_heads ? block / p.per_head : a.num_heads;
-  // Up to eight sweeps a block (one read of pos and of the table entries for
-  // all), fewer while that leaves SMs without a block.
-  p.sweeps = 8;
+  // Up to `sweeps` times the lanes' heads a block (one read of pos and of the
+  // table entries for all), fewer while that leaves SMs without a block.
+  p.sweeps = sweeps;
   const int64_t want = 4 * static_cast<int64_t>(grid_ctas());
-  auto tasks_of = [&](int sweeps) {
-    return static_cast<int64_t>(a.num_rows) * ((a.num_heads + p.lanes * sweeps - 1) / (p.lanes * sweeps));
+  auto tasks_of = [&](int n) {
+    return static_cast<int64_t>(a.num_rows) * ((a.num_heads + p.lanes * n - 1) / (p.lanes * n));
   };
   while (p.sweeps > 1 && tasks_of(p.sweeps) < want) p.sweeps /= 2;
   p.groups = (a.num_heads + p.lanes * p.sweeps - 1) / (p.lanes * p.sweeps);
   p.tasks = tasks_of(p.sweeps);
+  return block;
+}
+
+dim3 rows_grid(const RowsPlan& p) {
   const int64_t cap = static_cast<int64_t>(grid_ctas()) * 16;
-  const dim3 grid(static_cast<unsigned>(p.tasks < cap ? p.tasks : cap));
-  if (inter) return launch_pdl(rope_rows_kernel<ELEM, true, VB>, grid, dim3(block), 0, st, a, p);
-  return launch_pdl(rope_rows_kernel<ELEM, false, VB>, grid, dim3(block), 0, st, a, p);
+  return dim3(static_cast<unsigned>(p.tasks < cap ? p.tasks : cap));
+}
+
+template <int ELEM, int VB>
+cudaError_t launch_pairs(const RopeRowsArgs& a, cudaStream_t st) {
+  constexpr int kE = VB / (ELEM == GW_ELEM_F32 ? 4 : 2);
+  const bool inter = a.pairs == GW_PAIRS_INTERLEAVED;
+  RowsPlan p{};
+  p.per_head = inter && kE > 1 ? a.rot_dim / kE : a.rot_dim / 2 / kE;
+  const int block = plan_rows(a, 4, p);
+  if (inter) return launch_pdl(rope_pairs_kernel<ELEM, true, VB>, rows_grid(p), dim3(block), 0, st, a, p);
+  return launch_pdl(rope_pairs_kernel<ELEM, false, VB>, rows_grid(p), dim3(block), 0, st, a, p);
+}
+
+template <int ELEM, int VB>
+cudaError_t launch_chunks(const RopeRowsArgs& a, cudaStream_t st) {
+  RowsPlan p{};
+  p.per_head = a.head_dim / (VB / (ELEM == GW_ELEM_F32 ? 4 : 2));
+  const int block = plan_rows(a, 8, p);
+  constexpr int kE = VB / (ELEM == GW_ELEM_F32 ? 4 : 2);
+  auto kern = a.pairs == GW_PAIRS_INTERLEAVED ? rope_chunks_kernel<ELEM, kInterleaved, VB>
+              : a.rot_dim / 2 % kE == 0       ? rope_chunks_kernel<ELEM, kHalfChunks, VB>
+                                              : rope_chunks_kernel<ELEM, kHalfScattered, VB>;
+  return launch_pdl(kern, rows_grid(p), dim3(block), 0, st, a, p);
 }
 
 template <int ELEM>
 cudaError_t launch_rows(const RopeRowsArgs& a, cudaStream_t st) {
   constexpr int kSize = ELEM == GW_ELEM_F32 ? 4 : 2;
-  // every offset that an access can have, in bytes
-  uint64_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
-  if (a.num_rows > 1) all |= static_cast<uint64_t>(a.x_row | a.y_row) * kSize;
-  if (a.num_heads > 1) all |= static_cast<uint64_t>(a.x_head | a.y_head) * kSize;
-  all |= static_cast<uint64_t>(a.pairs == GW_PAIRS_HALF ? a.rot_dim / 2 : a.rot_dim) * kSize;
-  if (!a.inplace) all |= static_cast<uint64_t>(a.head_dim - a.rot_dim) * kSize;
-  if (all % 16 == 0) return launch_rows_vb<ELEM, 16>(a, st);
-  if (all % 8 == 0) return launch_rows_vb<ELEM, 8>(a, st);
-  if (all % 4 == 0) return launch_rows_vb<ELEM, 4>(a, st);
-  if constexpr (kSize == 2) return launch_rows_vb<ELEM, 2>(a, st);
+  // every offset of a head, in bytes
+  uint64_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y);
+  if (a.num_rows > 1) at |= static_cast<uint64_t>(a.x_row | a.y_row) * kSize;
+  if (a.num_heads > 1) at |= static_cast<uint64_t>(a.x_head | a.y_head) * kSize;
+  const uint64_t pairs = at | static_cast<uint64_t>(a.pairs == GW_PAIRS_HALF ? a.rot_dim / 2 : a.rot_dim) * kSize;
+  const uint64_t chunks = at | static_cast<uint64_t>(a.head_dim) * kSize;
+  if (a.inplace || (a.rot_dim == a.head_dim && pairs % 16 == 0)) {
+    if (pairs % 16 == 0) return launch_pairs<ELEM, 16>(a, st);
+    if (pairs % 8 == 0) return launch_pairs<ELEM, 8>(a, st);
+    if (pairs % 4 == 0) return launch_pairs<ELEM, 4>(a, st);
+    if constexpr (kSize == 2) return launch_pairs<ELEM, 2>(a, st);
+  } else {
+    if (chunks % 16 == 0) return launch_chunks<ELEM, 16>(a, st);
+    if (chunks % 8 == 0) return launch_chunks<ELEM, 8>(a, st);
+    if (chunks % 4 == 0) return launch_chunks<ELEM, 4>(a, st);
+    if constexpr (kSize == 2) return launch_chunks<ELEM, 2>(a, st);
+  }
   return cudaErrorInvalidValue;  // not reached: the entry point checks the alignment to an element
 }
 

@@ -524,7 +524,7 @@ gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch
  *              more than dst_max_pages pages (GW_DEV_KEEP_RANGE), is left as
  *              it was.
  *   A row whose source or destination page is outside [0, num_pages) is not
- *   moved (GW_DEV_PAGE_RANGE).
+ *   moved (GW_DEV_PAGE_RANGE); its acc is.
  *   batch in [0, 65535]; 0 is a no-op.  seq_lens and keep_lens must not be
  *   the same array.
  * Errors: GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED (a LOCAL pool: its window

@@ -117,8 +117,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     cluster_arrive();
     cluster_wait();
     if (warp < 8) {  // thread t: digit 255 - t, counted over the cluster
-      uint32_t count = 0;
-      for (int c = 0; c < ctas; ++c) count += ld_cluster(&h[255 - tid], c);
+      uint32_t from[kMaxSelCtas], count = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxSelCtas; ++c) from[c] = c < ctas ? ld_cluster(&h[255 - tid], c) : 0;
+#pragma unroll
+      for (int c = 0; c < kMaxSelCtas; ++c) count += from[c];
       uint32_t x = count;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -198,6 +201,19 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
     base_sure += __reduce_add_sync(0xffffffffu, w.x);
     base_ties += __reduce_add_sync(0xffffffffu, w.y);
     const uint32_t low = (1u << lane) - 1;
+    if (mine.y == 0) {  // no ties in this warp, as in nearly all
+      sure += min(ties, need);
+#pragma unroll
+      for (int r = 0; r < kSelKeys; ++r) {
+        if (r < keys) {
+          const bool is_sure = key[r] > last || key[r] == kProtected;
+          const uint32_t s = __ballot_sync(0xffffffffu, is_sure);
+          if (is_sure) keep[sure + __popc(s & low)] = t0 + first + r * 32;
+          sure += __popc(s);
+        }
+      }
+      continue;
+    }
 #pragma unroll
     for (int r = 0; r < kSelKeys; ++r) {
       if (r < keys) {

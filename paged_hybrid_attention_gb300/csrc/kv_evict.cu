@@ -150,23 +150,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   // keys that match it the first `need`.  If nothing of the middle is kept, no
   // key but the ends' is above `last`.
   const uint32_t last = middle ? prefix | ~mask : kProtected;
-  auto ballots = [&](int r, uint32_t& sure, uint32_t& tie) {
-    const uint32_t k = key[r];
-    sure = __ballot_sync(0xffffffffu, k > last || k == kProtected);
-    tie = __ballot_sync(0xffffffffu, k >= prefix && k <= last && k + 1 > 1 && middle);
-  };
+  auto is_sure = [&](int r) { return key[r] > last || key[r] == kProtected; };
+  auto is_tie = [&](int r) { return middle && key[r] >= prefix && key[r] <= last && key[r] + 1 > 1; };
   auto count_warp = [&]() {  // the round's counts of this warp
-    uint2 w = make_uint2(0, 0);
+    uint2 n = make_uint2(0, 0);
 #pragma unroll
     for (int r = 0; r < kSelKeys; ++r) {
       if (r < keys) {
-        uint32_t s, e;
-        ballots(r, s, e);
-        w.x += __popc(s);
-        w.y += __popc(e);
+        n.x += is_sure(r);
+        n.y += is_tie(r);
       }
     }
-    return w;
+    return make_uint2(__reduce_add_sync(0xffffffffu, n.x), __reduce_add_sync(0xffffffffu, n.y));
   };
   uint2 mine = make_uint2(0, 0);
   for (int round = 0; round < rounds; ++round) {
@@ -206,9 +201,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 #pragma unroll
       for (int r = 0; r < kSelKeys; ++r) {
         if (r < keys) {
-          const bool is_sure = key[r] > last || key[r] == kProtected;
-          const uint32_t s = __ballot_sync(0xffffffffu, is_sure);
-          if (is_sure) keep[sure + __popc(s & low)] = t0 + first + r * 32;
+          const uint32_t s = __ballot_sync(0xffffffffu, is_sure(r));
+          if (is_sure(r)) keep[sure + __popc(s & low)] = t0 + first + r * 32;
           sure += __popc(s);
         }
       }
@@ -217,8 +211,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 #pragma unroll
     for (int r = 0; r < kSelKeys; ++r) {
       if (r < keys) {
-        uint32_t s, e;
-        ballots(r, s, e);
+        const uint32_t s = __ballot_sync(0xffffffffu, is_sure(r)), e = __ballot_sync(0xffffffffu, is_tie(r));
         const uint32_t ties_before = ties + __popc(e & low);
         if ((s >> lane & 1) || ((e >> lane & 1) && ties_before < need))
           keep[sure + __popc(s & low) + min(ties_before, need)] = t0 + first + r * 32;

@@ -489,7 +489,7 @@ size_t gw_attn_acc_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, 
  *              left as they were.
  *   keep_lens  int32 [batch], not the array seq_lens.
  *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget;
- *   batch 0 is a no-op.
+ *   batch in [0, 65535], 0 is a no-op.
  * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
  */
 gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch, const int32_t* seq_lens,

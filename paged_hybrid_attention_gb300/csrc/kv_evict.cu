@@ -27,9 +27,9 @@ constexpr uint32_t kNoToken = 0, kProtected = 0xffffffffu;
 // but make each block read eight times as many counts of the others.)  It
 // ends with the first digit all of whose keys are kept.  Then the blocks
 // exchange how many of their tokens are kept or tied, and write their indices
-// in order.  8 x 131072 tokens take 17 us, 4.2 MB of weights read once: short
-// passes between barriers bound it (a pass over 16 keys a thread is 1.6 us, its
-// barrier and sums as much again).
+// in order.  8 x 131072 tokens take 15.6 us, 4.2 MB of weights read once: short
+// passes between barriers bound it (a pass over 16 keys a thread is 1.2 us, its
+// barrier and sums 1.5 us).
 constexpr int kSelThreads = 1024;
 constexpr int kSelKeys = 16;
 constexpr int kMaxSelCtas = 8;
@@ -371,7 +371,7 @@ cudaError_t launch_compact_layout(const CompactArgs& a, cudaStream_t st) {
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t st) {
   // Lengths are device values: the row stride bounds them.  More blocks per
   // sequence while each would still have 4096 tokens (8192 x 16 tokens: two
-  // blocks each 10.8 us, one 11.7, eight 11.6).
+  // blocks each 10.8 us, one 11.7, eight 11.6 before later steps).
   int ctas = 1;
   while (ctas < kMaxSelCtas && a.acc_stride > static_cast<int64_t>(4096) * ctas) ctas *= 2;
   cudaLaunchConfig_t cfg{};

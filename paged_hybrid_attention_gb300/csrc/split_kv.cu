@@ -194,8 +194,9 @@ __device__ __forceinline__ void acc_block(const LocalArgs& a, AccSmem<HQ>& sm, i
   const int L = a.seq_lens[s];
   const int row0 = a.cu_q_rows[s], row1 = a.cu_q_rows[s + 1];
   const int ub = a.unit_base[s], ub1 = a.unit_base[s + 1], ub_total = a.unit_base[a.batch];
+  if (row1 - row0 != 1 || L < 1 || L > a.max_pages * kPage || ub_total > a.max_units) return;
   const int tiles = (L - 1) / kAccTile + 1;
-  if (row1 - row0 != 1 || L < 1 || L > a.max_pages * kPage || ub_total > a.max_units || blk >= tiles) return;
+  if (blk >= tiles) return;
   const float4* score = reinterpret_cast<const float4*>(a.score + static_cast<int64_t>(s) * a.max_pages * kPage * HQ);
   float* acc = a.acc + s * a.acc_stride;
   if (tid == 0) {

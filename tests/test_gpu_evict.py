@@ -290,6 +290,42 @@ def test_binding_refuses():
         gw.kv_evict_compact(local, c.bt, c.n, keep, n)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own cache, weights and workspace,
+    overlap without changing either's results."""
+    lens = [5000, 300, 2100]
+    jobs = []
+    for k in range(2):
+        c = Cache(LAYOUTS[k], lens, 8, seed=20 + k)
+        jobs.append(dict(c=c, start=c.pool.data.clone(), acc=c.new_acc(), q=c.q.cuda(), stream=torch.cuda.Stream(),
+                         keep=torch.full((3, 512), -1, dtype=torch.int32, device="cuda"),
+                         n=torch.zeros(3, dtype=torch.int32, device="cuda"), got=[]))
+        jobs[-1]["out"] = torch.empty_like(jobs[-1]["q"])
+
+    def go(j, stream):
+        c = j["c"]
+        c.run(j["acc"], q=j["q"], out=j["out"], lse=None, stream=stream)
+        gw.kv_evict_select(j["acc"], c.n, 512, j["keep"], j["n"], 3, 64, c.status, stream)
+        gw.kv_evict_compact(c.pool, c.bt, c.n, j["keep"], j["n"], j["acc"], dev_status=c.status, stream=stream)
+
+    for turn in range(3):
+        for j in jobs:
+            j["c"].pool.data.copy_(j["start"])
+            j["acc"].zero_()
+        torch.cuda.synchronize()
+        for j in jobs:
+            go(j, j["stream"] if turn else None)
+            if not turn:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        for j in jobs:
+            assert int(j["c"].status) == 0
+            j["got"].append([t.clone() for t in (j["out"], j["acc"], j["keep"], j["n"], j["c"].pool.data)])
+    for j in jobs:
+        for turn in (1, 2):
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(j["got"][turn], j["got"][0]))
+
+
 # ------------------------------------------------------- a decode loop with both
 @pytest.mark.parametrize("layout", LAYOUTS)
 def test_decode_loop_with_eviction(layout):

@@ -244,8 +244,9 @@ template <int HQ>
 __device__ __forceinline__ void store_logits(float* dst, const float (&s)[HQ]) {
 #pragma unroll
   for (int h = 0; h < HQ; h += 8)
-    asm volatile("st.global.L1::no_allocate.L2::evict_last.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + h), "f"(s[h]), "f"(s[h + 1]),
-                 "f"(s[h + 2]), "f"(s[h + 3]), "f"(s[h + 4]), "f"(s[h + 5]), "f"(s[h + 6]), "f"(s[h + 7])
+    asm volatile("st.global.L1::no_allocate.L2::evict_last.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + h),
+                 "f"(s[h]), "f"(s[h + 1]), "f"(s[h + 2]), "f"(s[h + 3]), "f"(s[h + 4]), "f"(s[h + 5]), "f"(s[h + 6]),
+                 "f"(s[h + 7])
                  : "memory");
 }
 
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
   // The reference that exponents are taken against lies this far (base-2) below
   // a new maximum.  e4m3 weights have an absolute step (2^-9), so the variant
   // that sums weights lets them grow to 2^6 and more of the 2^8 that the lazy
-  // maximum allows: rows of random data are 0.0018 from float64 (rel-L2)
-  // instead of 0.0034, near the 0.0017 of their bf16 rounding.
+  // maximum allows: rows of random data are 0.0017 from float64 (rel-L2),
+  // which is their bf16 rounding, instead of 0.0034.
   constexpr float kBelowMax = kAcc && kE4 ? 6.f : 0.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);

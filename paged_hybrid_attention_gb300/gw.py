@@ -196,6 +196,8 @@ def _row_stride(fn, name, t, dtype, rows):
     """The row stride of `t`, [rows, columns] of this dtype whose columns are
     adjacent and whose rows do not overlap; each row, the last one too, has
     the stride's length of memory behind it."""
+    if t is None:
+        _invalid(fn, "%s is None" % name)
     if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows:
         _invalid(fn, "%s must be %s [%d, columns] (got %s %s)" % (name, dtype, rows, t.dtype, list(t.shape)))
     cols = int(t.shape[1])
@@ -279,10 +281,11 @@ def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, invers
     if dim > 1 and (x1 != 1 or y1 != 1):
         _invalid(fn, "the last dimension of x and out must have stride 1")
     _vector(fn, "pos", pos, rows)
-    _dense(fn, "rope_cs", rope_cs, torch.float32, rope_cs.shape[0], rot_dim // 2, 2)
+    max_pos = 0 if rope_cs is None else rope_cs.shape[0]
+    _dense(fn, "rope_cs", rope_cs, torch.float32, max_pos, rot_dim // 2, 2)
     _check(_lib.gw_rope_rows(x.data_ptr(), xr, xh, out.data_ptr(), yr, yh, elem, rows, heads, dim, rot_dim,
                              PAIRS_INTERLEAVED if interleaved else PAIRS_HALF, 1 if inverse else 0, pos.data_ptr(),
-                             rope_cs.data_ptr(), rope_cs.shape[0], _addr(dev_status), handle))
+                             rope_cs.data_ptr(), max_pos, _addr(dev_status), handle))
     return out
 
 

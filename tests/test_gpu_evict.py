@@ -290,6 +290,35 @@ def test_binding_refuses():
         gw.kv_evict_compact(local, c.bt, c.n, keep, n)
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_early_inputs_behind_a_cut(layout):
+    """Choice, move and the next attention over the new lengths without a
+    kernel between them, with the index inputs read early: the same bits."""
+    lens = [3000, 40, 700, 1, 260]
+    c = Cache(layout, lens, 16)
+    start, q = c.pool.data.clone(), c.q.cuda()
+    got = []
+    try:
+        for early in (False, True, True):
+            c.pool.data.copy_(start)
+            acc, keep = c.new_acc(), torch.full((5, 256), -1, dtype=torch.int32, device="cuda")
+            n, out = torch.zeros(5, dtype=torch.int32, device="cuda"), [torch.empty_like(q) for _ in range(3)]
+            torch.cuda.synchronize()
+            gw.set_early_inputs(early)
+            c.run(acc, q=q, out=out[0], lse=None)
+            gw.kv_evict_select(acc, c.n, 256, keep, n, 2, 30, c.status)
+            gw.kv_evict_compact(c.pool, c.bt, c.n, keep, n, acc, dev_status=c.status)
+            gw.decode_attn_global_acc(c.pool, q, out[1], None, acc, c.cu, n, c.bt, c.ws, dev_status=c.status)
+            gw.decode_attn_global(c.pool, q, out[2], c.cu, n, c.bt, c.ws, dev_status=c.status)
+            torch.cuda.synchronize()
+            got.append([t.view(torch.uint8).clone() for t in (*out, acc, keep, n, c.pool.data)])
+    finally:
+        gw.set_early_inputs(False)
+    assert int(c.status) == 0
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with its own cache, weights and workspace,
     overlap without changing either's results."""

@@ -275,3 +275,15 @@ def test_unscaled_table_is_rope_cs():
     a, b = gw.rope_cs(1e6, 128, 512, 70000), gw.rope_cs_scaled(1e6, 128, 512, 70000)
     ang = 70000.0
     assert float((a.double() - b.double()).abs().max()) <= 2.0 ** -23 + 2.0 ** -50 * ang
+
+
+def test_binding_refuses():
+    x, pos, cs = _inputs(4, 2, 64, 64, "bf16", 10)
+    for call in (lambda: gw.rope_rows(x, pos, None), lambda: gw.rope_rows(x, pos.long(), cs), lambda: gw.rope_rows(x[0], pos, cs),
+                 lambda: gw.rope_rows(x, pos[:3], cs), lambda: gw.rope_rows(x, pos, cs, rot_dim=32),
+                 lambda: gw.rope_rows(x.double(), pos, cs), lambda: gw.rope_rows(x, pos, cs, out=x.float()),
+                 lambda: gw.rope_rows(x[..., ::2], pos, cs[:, :16].contiguous()), lambda: gw.rope_rows(x, pos, cs.cpu()),
+                 lambda: gw.rope_rows(x, pos, cs, out=x[:, :1].expand(4, 2, 64)),
+                 lambda: gw.rope_rows(x[:3], pos[:3], cs, out=x[1:]), lambda: gw.rope_cs_scaled(1e4, 64, 128, 10, out=cs[:9])):
+        with pytest.raises(gw.GwError):
+            call()

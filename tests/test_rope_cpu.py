@@ -69,3 +69,6 @@ def test_binding_refuses():
         gw.rope_cs_scaled(1e4, 128, 512, 16, kind="cubic")
     with pytest.raises(gw.GwError, match="not on a CUDA device"):
         gw.rope_cs_scaled(1e4, 128, 512, 16, out=torch.zeros(16, 64, 2))
+    with pytest.raises(gw.GwError, match="budget|CUDA"):
+        gw.kv_evict_select(torch.zeros(1, 4), torch.zeros(1, dtype=torch.int32), 2, torch.zeros(1, 4, dtype=torch.int32),
+                           torch.zeros(1, dtype=torch.int32))

@@ -5,6 +5,29 @@
 namespace gw {
 namespace {
 
+// A launch in clusters of `ctas` blocks along x, early under the same terms as
+// launch_pdl's.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, int ctas, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = early_launch() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // ---- select -------------------------------------------------------------------
 // The weights' order as unsigned integers: larger weight, larger key; -0 and
 // 0 share a key, and every NaN has key 1, below -inf (0x007fffff).
@@ -33,9 +56,6 @@ constexpr uint32_t kNoToken = 0, kProtected = 0xffffffffu;
 constexpr int kSelThreads = 1024;
 constexpr int kSelKeys = 16;
 constexpr int kMaxSelCtas = 8;
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The 32-bit word that block `rank` of the cluster has at this shared address.
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
@@ -224,17 +244,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 }
 
 // ---- compact ------------------------------------------------------------------
-// Token i's row takes token keep[i]'s place, keep[i] >= i.  A block walks W
-// adjacent 16-byte column blocks of the sequence's rows in token order, a step
-// of kMoveThreads rows at a time: all of a step's rows are read before any is
-// written (the barrier), and no later step reads what it writes, since later
-// steps' sources lie at or behind their own first token.  So the move is exact
-// in place, column blocks need no order among themselves, and the next step's
-// rows may be on their way while this one's are written.
-// 8 x 131072 folded rows to 32768 take 198 us: 924 MB read (the 64-byte pieces
-// that hold a kept row) and 316 MB written, 0.95 of a copy's rate.  512 rows a
-// step are the best: 256 take 284 us, 1024 278 us.
+// Token i's row takes token keep[i]'s place, keep[i] >= i.  A walk takes
+// kWalkCols adjacent 16-byte column blocks of the sequence's rows in token
+// order, a step of kMoveThreads rows per block at a time: all of a step's rows
+// are read before any is written (the barrier, of the block or of the walk's
+// cluster), and no later step reads what it writes, since later steps' sources
+// lie at or behind their own first token.  So the move is exact in place, walks
+// need no order among themselves, and the next step's rows may be on their way
+// while this one's are written.
+// 8 x 131072 folded rows to 32768 take 190 to 200 us: 924 MB read (the 64-byte
+// pieces that hold a kept row) and 316 MB written, 0.95 of a copy's rate; to
+// 122880, 470 us (384 at a copy's rate).  Few sequences are bound by a step's
+// round trip, about 1.4 us: their walks get more blocks.  512 rows per block and
+// step are the best: 256 took 284 us, 1024 278 us; four column blocks a walk are
+// no faster, one takes 264 us.
 constexpr int kMoveThreads = 512;
+constexpr int kWalkCols = 2;     // column blocks of a walk
+constexpr int kMaxMoveCtas = 8;  // blocks of a walk
 
 template <int LAYOUT>
 struct RowShape {
@@ -259,49 +285,63 @@ __device__ __forceinline__ uint4 ld_piece(const uint8_t* p) {
   return v;
 }
 
+// All of a walk's threads have read a step: the block's, or those of the `ctas`
+// blocks of its cluster.
+__device__ __forceinline__ void step_bar(int ctas) {
+  if (ctas == 1) {
+    __syncthreads();
+  } else {
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+
 // The weights of one sequence: the same walk, kAccRows tokens per thread and step.
-__device__ __forceinline__ void move_weights(float* acc, const int32_t* keep, int n, int L) {
+__device__ __forceinline__ void move_weights(float* acc, const int32_t* keep, int n, int L, int rank, int ctas) {
   constexpr int kAccRows = 8;
   const int tid = threadIdx.x;
-  for (int i0 = 0; i0 < n; i0 += kMoveThreads * kAccRows) {
+  const int64_t step = static_cast<int64_t>(ctas) * kMoveThreads * kAccRows;
+  for (int64_t i0 = static_cast<int64_t>(rank) * kMoveThreads * kAccRows, s0 = 0; s0 < n; i0 += step, s0 += step) {
     int j[kAccRows];
     float w[kAccRows];
 #pragma unroll
     for (int r = 0; r < kAccRows; ++r) {
-      const int i = i0 + r * kMoveThreads + tid;
-      j[r] = i < n ? source_of(keep, i, L) : -1;
+      const int64_t i = i0 + r * kMoveThreads + tid;
+      j[r] = i < n ? source_of(keep, static_cast<int>(i), L) : -1;
     }
 #pragma unroll
     for (int r = 0; r < kAccRows; ++r) w[r] = j[r] >= 0 ? acc[j[r]] : 0.f;
-    __syncthreads();
+    step_bar(ctas);
 #pragma unroll
     for (int r = 0; r < kAccRows; ++r)
       if (j[r] >= 0) acc[i0 + r * kMoveThreads + tid] = w[r];
   }
-  __syncthreads();
-  for (int i = n + tid; i < L; i += kMoveThreads) acc[i] = 0.f;
+  step_bar(ctas);
+  for (int64_t i = n + rank * kMoveThreads + tid; i < L; i += ctas * kMoveThreads) acc[i] = 0.f;
 }
 
-template <int LAYOUT, int W>
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactArgs a) {
+template <int LAYOUT>
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactArgs a, int ctas) {
   using R = RowShape<LAYOUT>;
+  constexpr int W = kWalkCols;
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int col = static_cast<int>(blockIdx.x) - (a.acc ? 1 : 0);  // -1: the weights
+  const int rank = static_cast<int>(blockIdx.x) % ctas;
+  const int col = static_cast<int>(blockIdx.x) / ctas - (a.acc ? 1 : 0);  // -1: the weights
   const int L = a.seq_lens[b], n = a.keep_lens[b];
   const bool reports = col == 0;
-  if (L < 0 || L > a.max_pages * kPage) {
-    if (reports && tid == 0) set_status(a.status, GW_DEV_LEN_RANGE);
+  if (L < 0 || L > a.max_pages * kPage) {  // as below, the same for all of a cluster
+    if (reports && rank == 0 && tid == 0) set_status(a.status, GW_DEV_LEN_RANGE);
     return;
   }
   if (n < 0 || n > L || n > a.keep_stride || n > static_cast<int64_t>(a.dst_max_pages) * kPage) {
-    if (reports && tid == 0) set_status(a.status, GW_DEV_KEEP_RANGE);
+    if (reports && rank == 0 && tid == 0) set_status(a.status, GW_DEV_KEEP_RANGE);
     return;
   }
   const int32_t* keep = a.keep_idx + b * a.keep_stride;
   if (col < 0) {
-    move_weights(a.acc + b * a.acc_stride, keep, n, L);
+    move_weights(a.acc + b * a.acc_stride, keep, n, L, rank, ctas);
     return;
   }
   const int32_t* src_table = a.block_table + static_cast<int64_t>(b) * a.max_pages;
@@ -311,9 +351,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     uint4 v[W];
     uint8_t* to;  // null: nothing to move
   };
-  // the source token of the row that this thread has in the step at i0; -1: none
+  const int64_t step = static_cast<int64_t>(ctas) * kMoveThreads;
+  const int mine = rank * kMoveThreads + tid;  // this thread's row of a step
+  // the source token of the thread's row of the step at i0; -1: none
   auto index = [&](int64_t i0) {
-    const int64_t i = i0 + tid;
+    const int64_t i = i0 + mine;
     if (i >= n) return -1;
     const int j = source_of(keep, static_cast<int>(i), L);
     if (j < 0 && reports) set_status(a.status, GW_DEV_KEEP_RANGE);
@@ -322,7 +364,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
   auto fetch = [&](int64_t i0, int j, Rows& x) {
     x.to = nullptr;
     if (j < 0) return;
-    const int i = static_cast<int>(i0) + tid;
+    const int i = static_cast<int>(i0) + mine;
     const int32_t sp = src_table[j / kPage], dp = dst_table[i / kPage];
     if (sp < 0 || sp >= a.num_pages || dp < 0 || dp >= a.num_pages) {
       if (reports) set_status(a.status, GW_DEV_PAGE_RANGE);
@@ -335,12 +377,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     for (int k = 0; k < W; ++k) x.v[k] = ld_piece(from + k * 128);
   };
   Rows now, next;
-  int j = index(0), j1 = index(kMoveThreads);
+  int j = index(0), j1 = index(step);
   fetch(0, j, now);
-  for (int64_t i0 = 0; i0 < n; i0 += kMoveThreads) {
-    const int j2 = index(i0 + 2 * kMoveThreads);
-    fetch(i0 + kMoveThreads, j1, next);
-    __syncthreads();
+  for (int64_t i0 = 0; i0 < n; i0 += step) {
+    const int j2 = index(i0 + 2 * step);
+    fetch(i0 + step, j1, next);
+    step_bar(ctas);
     if (now.to) {
 #pragma unroll
       for (int k = 0; k < W; ++k) *reinterpret_cast<uint4*>(now.to + k * 128) = now.v[k];
@@ -350,20 +392,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
   }
 }
 
-template <int LAYOUT, int W>
-cudaError_t launch_compact_w(const CompactArgs& a, cudaStream_t st) {
-  const dim3 grid(RowShape<LAYOUT>::kBlk / W + (a.acc ? 1 : 0), a.batch);
-  return launch_pdl(evict_compact_kernel<LAYOUT, W>, grid, dim3(kMoveThreads), 0, st, a);
-}
-
 template <int LAYOUT>
 cudaError_t launch_compact_layout(const CompactArgs& a, cudaStream_t st) {
-  // Two column blocks share one walk over the indices where that leaves every
-  // SM two blocks: 8 x 65536 folded rows to a quarter 98 us, one a walk 135;
-  // 1 x 131072 rows 93 and 88 us the other way round.  (Four a walk: 101 and
-  // 105 us; two or four rows a thread and step at 8 x 65536: 152 and 204 us.)
-  const int64_t blocks = static_cast<int64_t>(RowShape<LAYOUT>::kBlk) * a.batch;
-  return blocks >= 4 * static_cast<int64_t>(grid_ctas()) ? launch_compact_w<LAYOUT, 2>(a, st) : launch_compact_w<LAYOUT, 1>(a, st);
+  // As many blocks to a walk as leave the blocks of all walks on the GPU at
+  // once, three per SM less a twelfth that clusters leave unused.  1 x 131072
+  // folded rows to a quarter: eight 34 us, four 50, one 91; 3 x 131072: three
+  // 85, two 102, one 115; 8 x 131072: one 191, two 233.
+  const int64_t walks = static_cast<int64_t>(RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0)) * a.batch;
+  const int64_t room = 11 * static_cast<int64_t>(grid_ctas()) / (4 * walks);
+  const int ctas = static_cast<int>(room < 1 ? 1 : room > kMaxMoveCtas ? kMaxMoveCtas : room);
+  const dim3 grid((RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0)) * ctas, a.batch);
+  return launch_cluster(evict_compact_kernel<LAYOUT>, grid, dim3(kMoveThreads), ctas, st, a, ctas);
 }
 
 }  // namespace
@@ -374,20 +413,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t st) {
   // blocks each 10.8 us, one 11.7, eight 11.6 before later steps).
   int ctas = 1;
   while (ctas < kMaxSelCtas && a.acc_stride > static_cast<int64_t>(4096) * ctas) ctas *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * ctas);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = early_launch() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas);
+  return launch_cluster(evict_select_kernel, dim3(static_cast<unsigned>(a.batch) * ctas), dim3(kSelThreads), ctas, st, a, ctas);
 }
 
 cudaError_t launch_evict_compact(int layout, const CompactArgs& a, cudaStream_t st) {

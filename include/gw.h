@@ -427,7 +427,10 @@ gw_status gw_decode_attn_global_lse(const gw_kv_pool* pool, const void* q, void*
  * The sum over steps (and, with decay < 1, its fading form) is what
  * gw_kv_evict_select ranks tokens by.  Weights, their normaliser and acc are
  * float32 and the heads are added in a fixed order, so results do not depend
- * on the batch.  Sequences without exactly one row, or of invalid length,
+ * on the batch.  The rows are those of float32 weights, rounded once to bf16
+ * (gw_decode_attn_global contracts weights in bf16 or two e4m3 terms): weights
+ * enter P.V to 2^-15, on an e4m3 pool to 2^-11 and 2^-23 of a chunk's largest.
+ * Sequences without exactly one row, or of invalid length,
  * keep their acc row; so does every acc[b][j] with j >= seq_lens[b].  With
  * decay 0 the old values are not read (they may be anything).
  *

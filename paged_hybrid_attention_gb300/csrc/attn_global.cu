@@ -115,7 +115,8 @@ struct TileDesc {
 };
 constexpr int kFirst = 1, kLast = 2, kEnd = 4;
 
-template <int LAYOUT, int HQ>
+// kAcc: of gw_decode_attn_global_acc's variant (global_decode_kernel).
+template <int LAYOUT, int HQ, bool kAcc>
 struct GSmem {
   using T = GTraits<LAYOUT>;
   static constexpr int kNP = HQ < 16 ? 16 : HQ;  // P.V N (M=128 needs N % 16 == 0)
@@ -127,9 +128,12 @@ struct GSmem {
   // bf16: K-major Q [hb][cb 64][8 heads][8 dims].  e4m3: the hi term then
   // the lo term, each K-major [hb][cb 32][8 heads][16 dims].
   static constexpr int kQBytes = HQ * 512 * 2;
-  // bf16: MN-major P^T [tb 8][hb 8-head blocks][8 tokens][8 heads].  e4m3:
-  // the hi term then the lo term, each [tb 8][16-head blocks][8 tokens][16 heads].
-  static constexpr int kPBytes = 64 * kNP * 2;
+  // The terms of P^T, one after the other.  bf16: one, MN-major [tb 8][hb 8-head
+  // blocks][8 tokens][8 heads]; with weights two.  e4m3: two (hi and lo), each
+  // [tb 8][16-head blocks][8 tokens][16 heads]; with weights four, in e5m2.
+  static constexpr int kPTerms = (T::kE4 ? 2 : 1) * (kAcc ? 2 : 1);
+  static constexpr int kPTermBytes = 64 * kNP * (T::kE4 ? 1 : 2);
+  static constexpr int kPBytes = kPTerms * kPTermBytes;
   uint8_t tiles[T::kNumBuf][kTilePages][T::kPageBytes];
   uint8_t q[kQBuf][kQBytes];
   uint8_t p[2][kPBytes];
@@ -148,9 +152,9 @@ struct GSmem {
   int32_t app_done;  // fused append: units of this CTA (in order) whose rows are written
   int32_t ub[kMaxBatch + 1 + 32];  // split plan (+ scan scratch)
 };
-static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FOLDED, 32>) <= 232448, "shared memory of one CTA");
-static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FULL, 32>) <= 232448, "shared memory of one CTA");
-static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3, 32>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FOLDED, 32, true>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FULL, 32, true>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(GSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3, 32, true>) <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -238,8 +242,8 @@ __device__ __noinline__ void append_unit_row(const LocalArgs& a, const int32_t* 
 // Stores the HQ logits of one token, 32 bytes at a time: the softmax's lanes
 // hold a token each, so a wider store fills whole sectors.  The lines ask to
 // stay in L2 until the weights pass reads them (those of short contexts do; at
-// 8 x 131072 tokens the 134 MB of logits pass through memory: 280 us against
-// 239 without weights, at the same 5.7 TB/s).
+// 8 x 131072 tokens the 134 MB of logits pass through memory: 291 us against
+// 240 without weights, 12 of them for P's second term).
 template <int HQ>
 __device__ __forceinline__ void store_logits(float* dst, const float (&s)[HQ]) {
 #pragma unroll
@@ -254,23 +258,36 @@ __device__ __forceinline__ void store_logits(float* dst, const float (&s)[HQ]) {
 // gw_decode_attn_global_acc, which stores every token's logits for the pass
 // that turns them into weights and sums the softmax's unrounded weights, since
 // that pass is held to float32 (the plain call sums the weights as rounded for
-// P.V, so that numerator and denominator round alike).  Each is a kernel of
-// its own, so that the plain call's code is unchanged.
+// P.V, so that numerator and denominator round alike).  So that its rows are
+// still a numerator over its own denominator, P enters P.V in one term more,
+// what the plain call's terms leave:
+//   bf16 pools   p = hi + lo, both bf16, hi cut off: 2^-15 of p.
+//   e4m3 pool    p rounded to fp16, 2^-11 of p, = four e5m2 terms of three bits
+//                each: an e5m2 number is the upper byte of an fp16 one, so the
+//                terms are cut off by masks and exact differences, which costs
+//                the softmax less than e4m3's conversions there and back (253 us
+//                at 8 x 131072 tokens and 32 heads; e4m3 hi and lo and a third
+//                term in e5m2: 314 us; hi and lo alone, 2^-8 and 2^-16 of the
+//                largest at the tail: 261 us).  What lies
+//                below e5m2's smallest number, 2^-16, is lost; the exponents'
+//                reference lies kBelowMax (base-2) below a new maximum, so that
+//                the largest weight of a unit is 2^7 to 2^15 (the lazy maximum
+//                lets it grow by 2^8) and a long tail counts down to 2^-23 of it.
+// Rows are then what float32 weights give, 0.00165 from float64 (rel-L2) as
+// their rounding to bf16 alone (the plain call: 0.0020 on bf16, 0.0024 on e4m3
+// pools).  Each is a kernel of its own, so that the plain call's code is
+// unchanged.
 template <int LAYOUT, int HQ, bool kApp, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalArgs a) {
   using T = GTraits<LAYOUT>;
-  using SM = GSmem<LAYOUT, HQ>;
+  using SM = GSmem<LAYOUT, HQ, kAcc>;
   constexpr int NB = T::kNumBuf;
   constexpr int NP = SM::kNP;
   constexpr bool kE4 = T::kE4;
   constexpr int QB = SM::kQBuf;
   constexpr uint32_t kTileBytes = kTilePages * T::kPageBytes;
-  // The reference that exponents are taken against lies this far (base-2) below
-  // a new maximum.  e4m3 weights have an absolute step (2^-9), so the variant
-  // that sums weights lets them grow to 2^6 and more of the 2^8 that the lazy
-  // maximum allows: rows of random data are 0.0017 from float64 (rel-L2),
-  // which is their bf16 rounding, instead of 0.0034.
-  constexpr float kBelowMax = kAcc && kE4 ? 6.f : 0.f;
+  constexpr float kBelowMax = kAcc && kE4 ? 7.f : 0.f;
+  constexpr float kLazy = kLazyThreshold + kBelowMax;  // a logit this far above the reference asks for a new one
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -475,7 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
   } else if (warp == 7) {
     // ------------------------------------------------------------ P.V issue
     wait_prev();
-    const uint32_t id_pv = kE4 ? tc::idesc_e4m3(128, NP, true, true) : tc::idesc_bf16(128, NP, true, true);
+    const uint32_t id_pv = !kE4   ? tc::idesc_bf16(128, NP, true, true)
+                           : kAcc ? tc::idesc_e4m3_e5m2(128, NP, true, true)
+                                  : tc::idesc_e4m3(128, NP, true, true);
     const uint64_t pv_a0 = tc::smem_desc(smem_u32(sm.tiles[0]), T::kBlk * 128, 128);
     // P^T: 8-token block rows (NP / 8 or NP / 16 head blocks of 16 bytes) apart
     const uint64_t pv_b0 = tc::smem_desc(smem_u32(sm.p[0]), (kE4 ? NP / 16 : NP / 8) * 128, 128);
@@ -493,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       const uint64_t a_tile = pv_a0 + ((b * kTileBytes) >> 4);
       const uint64_t b_p = pv_b0 + (((n & 1) * SM::kPBytes) >> 4);
       if constexpr (kE4) {
-        // K = 32 tokens per MMA: pages 2j and 2j + 1; O^T += V^T (P_hi + P_lo)^T
+        // K = 32 tokens per MMA: pages 2j and 2j + 1; O^T += V^T (sum of the terms)^T
 #pragma unroll
         for (int j = 0; j < kTilePages / 2; ++j) {
           const uint64_t bd = b_p + ((4 * j * (NP / 16) * 128) >> 4);
@@ -502,7 +521,16 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
             const uint64_t ad = a_tile + ((2 * j * T::kPageBytes + (T::kVcb + 8 * blk) * 128) >> 4);
             const uint32_t d_o = tmem + kOBase + 128 * ob + 32 * blk;
             tc::mma_e4m3_warp(d_o, ad, bd, id_pv, !((d.flags & kFirst) && j == 0));
-            tc::mma_e4m3_warp(d_o, ad, bd + ((64 * NP) >> 4), id_pv, true);
+            if constexpr (!kAcc) tc::mma_e4m3_warp(d_o, ad, bd + (SM::kPTermBytes >> 4), id_pv, true);
+          }
+          if constexpr (kAcc) {
+#pragma unroll
+            for (int term = 1; term < SM::kPTerms; ++term)
+#pragma unroll
+              for (int blk = 0; blk < 4; ++blk) {
+                const uint64_t ad = a_tile + ((2 * j * T::kPageBytes + (T::kVcb + 8 * blk) * 128) >> 4);
+                tc::mma_e4m3_warp(tmem + kOBase + 128 * ob + 32 * blk, ad, bd + (term * SM::kPTermBytes >> 4), id_pv, true);
+              }
           }
           tc::commit_warp(&sm.slot_empty[b][2 * j]);  // the producer may refill these page slots
           tc::commit_warp(&sm.slot_empty[b][2 * j + 1]);
@@ -514,7 +542,15 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
 #pragma unroll
           for (int blk = 0; blk < 4; ++blk) {
             const uint64_t ad = a_tile + ((j * T::kPageBytes + (T::kVcb + 16 * blk) * 128) >> 4);
-            tc::mma_bf16_warp(tmem + kOBase + 128 * ob + 32 * blk, ad, bd, id_pv, !((d.flags & kFirst) && j == 0));
+            const uint32_t d_o = tmem + kOBase + 128 * ob + 32 * blk;
+            tc::mma_bf16_warp(d_o, ad, bd, id_pv, !((d.flags & kFirst) && j == 0));
+          }
+          if constexpr (kAcc) {
+#pragma unroll
+            for (int blk = 0; blk < 4; ++blk) {
+              const uint64_t ad = a_tile + ((j * T::kPageBytes + (T::kVcb + 16 * blk) * 128) >> 4);
+              tc::mma_bf16_warp(tmem + kOBase + 128 * ob + 32 * blk, ad, bd + (SM::kPTermBytes >> 4), id_pv, true);
+            }
           }
           tc::commit_warp(&sm.slot_empty[b][j]);  // the producer may refill this page slot
         }
@@ -699,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       for (int h = 0; h < HQ; ++h) {
         const float sc = kE4 ? sm.qscale[uidx & 3][h] * a.scale_log2 : a.scale_log2;
         s[h] = valid ? __uint_as_float(r[h]) * sc : -INFINITY;
-        need |= s[h] > m_run[h] + kLazyThreshold;
+        need |= s[h] > m_run[h] + kLazy;
       }
       // A thread asking for a new max tags the flag of this tile's parity
       // with the tile; the other parity's flag may meanwhile be written for
@@ -719,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
         if (tid < HQ) {
           const float mx = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid]));
           const float mo = first ? -INFINITY : sm.mvec[tid];
-          sm.mvec[tid] = (first || mx > mo + kLazyThreshold) ? fmaxf(mo, mx - kBelowMax) : mo;
+          sm.mvec[tid] = (first || mx > mo + kLazy) ? fmaxf(mo, mx - kBelowMax) : mo;
         }
         softmax_bar();
         float alpha[HQ];
@@ -752,11 +788,44 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       }
       // ---- P^T (bf16) for this tile; wait until P.V two tiles back released the buffer
       if (n >= 2 && !mbar_wait(&sm.pfree[n & 1], ((n >> 1) - 1) & 1, st)) break;
-      if (active && kE4) {
+      if (active && kE4 && kAcc) {
+        uint8_t* pdst = sm.p[n & 1] + ((t >> 3) * (NP / 16)) * 128 + (t & 7) * 16;
+#pragma unroll
+        for (int hb = 0; hb < NP / 16; ++hb) {
+          uint32_t w[4][4];  // by term
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            __half2 x[2];
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              const int h0 = hb * 16 + 4 * k4 + 2 * jj;
+              const int i0 = h0 < HQ ? h0 : 0, i1 = h0 + 1 < HQ ? h0 + 1 : 0;
+              const float p0 = (valid && h0 < HQ) ? ex2(s[i0] - m_run[i0]) : 0.f;
+              const float p1 = (valid && h0 + 1 < HQ) ? ex2(s[i1] - m_run[i1]) : 0.f;
+              if (h0 < HQ) l_acc[i0] += p0;
+              if (h0 + 1 < HQ) l_acc[i1] += p1;
+              x[jj] = __floats2half2_rn(p0, p1);
+            }
+#pragma unroll
+            for (int term = 0; term < 4; ++term) {
+              uint32_t a0 = *reinterpret_cast<uint32_t*>(&x[0]), a1 = *reinterpret_cast<uint32_t*>(&x[1]);
+              w[term][k4] = __byte_perm(a0, a1, 0x7531);  // the upper bytes
+              a0 &= 0xff00ff00u;
+              a1 &= 0xff00ff00u;
+              x[0] = __hsub2(x[0], *reinterpret_cast<__half2*>(&a0));
+              x[1] = __hsub2(x[1], *reinterpret_cast<__half2*>(&a1));
+            }
+          }
+#pragma unroll
+          for (int term = 0; term < 4; ++term)
+            *reinterpret_cast<uint4*>(pdst + term * SM::kPTermBytes + hb * 128) =
+                make_uint4(w[term][0], w[term][1], w[term][2], w[term][3]);
+        }
+      } else if (active && kE4) {
         // P = P_hi + P_lo, two e4m3 terms (P <= 2^8 under the lazy max); l
         // sums exactly the weights the contraction uses
         uint8_t* phi = sm.p[n & 1] + ((t >> 3) * (NP / 16)) * 128 + (t & 7) * 16;
-        uint8_t* plo = phi + 64 * NP;
+        uint8_t* plo = phi + SM::kPTermBytes;
 #pragma unroll
         for (int hb = 0; hb < NP / 16; ++hb) {
           uint32_t whi[4], wlo[4];
@@ -774,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
               const __nv_fp8x2_storage_t lo2 =
                   __nv_cvt_float2_to_fp8x2(make_float2(p0 - hf.x, p1 - hf.y), __NV_SATFINITE, __NV_E4M3);
               const float2 lf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(lo2, __NV_E4M3)));
-              if (h0 < HQ) l_acc[i0] += kAcc ? p0 : hf.x + lf.x;
-              if (h0 + 1 < HQ) l_acc[i1] += kAcc ? p1 : hf.y + lf.y;
+              if (h0 < HQ) l_acc[i0] += hf.x + lf.x;
+              if (h0 + 1 < HQ) l_acc[i1] += hf.y + lf.y;
               hw |= static_cast<uint32_t>(hi2) << (16 * jj);
               lw |= static_cast<uint32_t>(lo2) << (16 * jj);
             }
@@ -785,33 +854,41 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
           *reinterpret_cast<uint4*>(phi + hb * 128) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
           *reinterpret_cast<uint4*>(plo + hb * 128) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
         }
-        if (pvalid && tabs >= d.L) {
-          uint8_t* row = sm.tiles[b][j] + (lane >> 3) * T::kBlk * 128 + (lane & 7) * 16;
-          for (int cb = 0; cb < T::kBlk; ++cb) *reinterpret_cast<uint4*>(row + cb * 128) = make_uint4(0, 0, 0, 0);
-        }
       } else if (active) {
         uint8_t* pdst = sm.p[n & 1] + ((t >> 3) * (NP / 8)) * 128 + (t & 7) * 16;
 #pragma unroll
         for (int hb = 0; hb < HQ / 8; ++hb) {
-          uint32_t w[4];
+          uint32_t w[4], wlo[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int h0 = hb * 8 + 2 * k;
             const float p0 = valid ? ex2(s[h0] - m_run[h0]) : 0.f;
             const float p1 = valid ? ex2(s[h0 + 1] - m_run[h0 + 1]) : 0.f;
-            __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
-            l_acc[h0] += kAcc ? p0 : __low2float(pb);
-            l_acc[h0 + 1] += kAcc ? p1 : __high2float(pb);
-            w[k] = *reinterpret_cast<uint32_t*>(&pb);
+            if constexpr (kAcc) {
+              const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+              w[k] = __byte_perm(b0, b1, 0x7632);  // the upper halves
+              __nv_bfloat162 pl = __floats2bfloat162_rn(p0 - __uint_as_float(b0 & 0xffff0000u),
+                                                        p1 - __uint_as_float(b1 & 0xffff0000u));
+              wlo[k] = *reinterpret_cast<uint32_t*>(&pl);
+              l_acc[h0] += p0;
+              l_acc[h0 + 1] += p1;
+            } else {
+              __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+              l_acc[h0] += __low2float(pb);
+              l_acc[h0 + 1] += __high2float(pb);
+              w[k] = *reinterpret_cast<uint32_t*>(&pb);
+            }
           }
           *reinterpret_cast<uint4*>(pdst + hb * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (kAcc)
+            *reinterpret_cast<uint4*>(pdst + SM::kPTermBytes + hb * 128) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
         }
-        if (pvalid && tabs >= d.L) {
-          // token past the end of the sequence in a valid page: clear its row
-          // so whatever the pool holds there cannot reach P.V
-          uint8_t* row = sm.tiles[b][j] + (lane >> 3) * T::kBlk * 128 + (lane & 7) * 16;
-          for (int cb = 0; cb < T::kBlk; ++cb) *reinterpret_cast<uint4*>(row + cb * 128) = make_uint4(0, 0, 0, 0);
-        }
+      }
+      if (active && pvalid && tabs >= d.L) {
+        // token past the end of the sequence in a valid page: clear its row
+        // so whatever the pool holds there cannot reach P.V
+        uint8_t* row = sm.tiles[b][j] + (lane >> 3) * T::kBlk * 128 + (lane & 7) * 16;
+        for (int cb = 0; cb < T::kBlk; ++cb) *reinterpret_cast<uint4*>(row + cb * 128) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       tc::fence_before();
@@ -865,7 +942,7 @@ cudaError_t launch_layout(const LocalArgs& a, cudaStream_t stream) {
   auto kern = a.score   ? global_decode_kernel<LAYOUT, HQ, false, true>
               : a.k_new ? global_decode_kernel<LAYOUT, HQ, true, false>
                         : global_decode_kernel<LAYOUT, HQ, false, false>;
-  const size_t smem = sizeof(GSmem<LAYOUT, HQ>);
+  const size_t smem = a.score ? sizeof(GSmem<LAYOUT, HQ, true>) : sizeof(GSmem<LAYOUT, HQ, false>);
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(grid_ctas()), dim3(kThreads), smem, stream, a);

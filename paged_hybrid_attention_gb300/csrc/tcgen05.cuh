@@ -40,6 +40,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major,
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// As idesc_e4m3 with e5m2 B (format code 1): kind::f8f6f4 takes any two of its types.
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 10);
+}
+
 __device__ __forceinline__ void alloc(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)),
                "r"(ncols)
@@ -76,7 +81,7 @@ __device__ __forceinline__ void mma_bf16_warp(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// As mma_bf16_warp for kind::f8f6f4 (both operands e4m3 in shared memory).
+// As mma_bf16_warp for kind::f8f6f4 (both operands in shared memory, 8-bit types as in `idesc`).
 __device__ __forceinline__ void mma_e4m3_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                               bool accumulate) {
   asm volatile(

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
   }
   if (rank == 0 && tid == 0) a.keep_lens[b] = min(L, a.budget);
   if (L <= a.budget) {
-    for (int j = rank * kSelThreads + tid; j < L; j += ctas * kSelThreads) keep[j] = j;
+    for (int64_t j = rank * kSelThreads + tid; j < L; j += ctas * kSelThreads) keep[j] = static_cast<int32_t>(j);
     return;
   }
   // tokens by their place in the block's slice [t0, t0 + n): a slice has fewer

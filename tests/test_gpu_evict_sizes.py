@@ -1,0 +1,38 @@
+"""gw_kv_evict_select and gw_kv_evict_compact at the longest sequences that they
+accept, where indices reach 2^31, and where their pipelines run for many steps."""
+
+import pytest
+import torch
+
+from paged_hybrid_attention_gb300 import gw
+from tests import gpu_helpers as G
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 1 << 16  # elements before a row
+
+
+def _guarded(n, dtype, fill):
+    flat = torch.empty(GUARD + n + GUARD, dtype=dtype, device="cuda")
+    flat[:GUARD].fill_(fill)
+    flat[GUARD + n:].fill_(fill)
+    return flat, flat[GUARD:GUARD + n].view(1, n)
+
+
+def _guards_hold(flat, fill):
+    return bool((flat[:GUARD] == fill).all()) and bool((flat[-GUARD:] == fill).all())
+
+
+def _pieces(n, step=1 << 28):
+    return [slice(i, min(n, i + step)) for i in range(0, n, step)]
+
+
+def test_select_keeps_all_of_the_longest_row():
+    """2^31 - 1 tokens within the budget."""
+    n = 2 ** 31 - 1
+    flat, keep = _guarded(n, torch.int32, -9)
+    acc, lens = torch.empty(1, n, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    gw.kv_evict_select(acc, G.i32([n]), n, keep, lens)
+    assert int(lens) == n and _guards_hold(flat, -9)
+    for p in _pieces(n):
+        assert torch.equal(keep[0, p], torch.arange(p.start, p.stop, dtype=torch.int32, device="cuda"))

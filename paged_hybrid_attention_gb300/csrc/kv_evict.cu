@@ -317,7 +317,7 @@ __device__ __forceinline__ void move_weights(float* acc, const int32_t* keep, in
       if (j[r] >= 0) acc[i0 + r * kMoveThreads + tid] = w[r];
   }
   step_bar(ctas);
-  for (int64_t i = n + rank * kMoveThreads + tid; i < L; i += ctas * kMoveThreads) acc[i] = 0.f;
+  for (int64_t i = static_cast<int64_t>(n) + rank * kMoveThreads + tid; i < L; i += ctas * kMoveThreads) acc[i] = 0.f;
 }
 
 template <int LAYOUT>

@@ -36,3 +36,23 @@ def test_select_keeps_all_of_the_longest_row():
     assert int(lens) == n and _guards_hold(flat, -9)
     for p in _pieces(n):
         assert torch.equal(keep[0, p], torch.arange(p.start, p.stop, dtype=torch.int32, device="cuda"))
+
+
+def test_compact_weights_of_the_longest_sequence():
+    """The most pages that a sequence has; the weights behind the kept ones
+    become 0.  All rows stay in place (every table entry is the one page)."""
+    pages = 2 ** 27 - 1
+    n = 16 * pages
+    kept = n - 5
+    pool = gw.KVPool("folded_e4m3", "e4m3", 1)
+    before = pool.data.clone()
+    flat, acc = _guarded(n, torch.float32, 7.0)
+    acc.fill_(1.0)
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    keep = torch.arange(kept, dtype=torch.int32, device="cuda").view(1, kept)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gw.kv_evict_compact(pool, table, G.i32([n]), keep, G.i32([kept]), acc, dev_status=status)
+    assert int(status) == 0 and _guards_hold(flat, 7.0) and torch.equal(pool.data, before)
+    for p in _pieces(kept):
+        assert bool((acc[0, p] == 1).all())
+    assert bool((acc[0, kept:] == 0).all())

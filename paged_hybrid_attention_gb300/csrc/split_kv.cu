@@ -238,7 +238,7 @@ __device__ __forceinline__ void acc_block(const LocalArgs& a, AccSmem<HQ>& sm, i
   int stage = 0;
   uint32_t parity = 0;
   for (int tile = blk; tile < tiles; tile += blocks_per_seq) {
-    const int t = tile * kAccTile + tid;  // below 2^31: L is at most max_pages * 16 < 2^31 - kAccTile
+    const int t = tile * kAccTile + tid;  // below 2^31: L is too, and tiles are whole parts of 2^31
     const float old = t < L && a.decay > 0.f ? acc[t] : 0.f;
     if (!mbar_wait(&sm.full[stage], parity, a.status)) return;
     if (t < L) {

@@ -6,6 +6,7 @@ import torch
 
 from paged_hybrid_attention_gb300 import gw
 from tests import gpu_helpers as G
+from tests.test_gpu_acc import Cache
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,75 @@ def test_compact_weights_of_the_longest_sequence():
     for p in _pieces(kept):
         assert bool((acc[0, p] == 1).all())
     assert bool((acc[0, kept:] == 0).all())
+
+
+ROW = {"folded": 80, "full": 128, "folded_e4m3": 40}  # 16-byte column blocks of a row
+
+
+def _cut(L, share, g):
+    """A random choice of L * share tokens (L - 1 for "all but one"), ascending."""
+    n = L - 1 if share == "all but one" else int(L * share)
+    return torch.randperm(L, generator=g, device="cuda")[:n].sort().values.to(torch.int32)
+
+
+@pytest.mark.parametrize("layout", ["folded", "full", "folded_e4m3"])
+@pytest.mark.parametrize("batch", [1, 2, 3, 5, 9])
+@pytest.mark.parametrize("share", [0.25, 15 / 16, "all but one"])
+@pytest.mark.parametrize("other_pages", [False, True])
+def test_long_cuts(layout, batch, share, other_pages):
+    """Walks of many steps, over blocks and over clusters of every size that
+    the batches get, with a partial last step: every byte of the pool, every
+    weight."""
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    lens = [70001 - 7777 * b for b in range(batch)]
+    width = (max(lens) + 15) // 16 + 1
+    need = [(n + 15) // 16 for n in lens]
+    copies = 2 if other_pages else 1
+    perm = torch.randperm(copies * sum(need), generator=g, device="cuda").to(torch.int32)
+    pool = gw.KVPool(layout, "e4m3" if layout == "folded_e4m3" else "bf16", copies * sum(need))
+    pool.data.copy_(torch.randint(0, 256, (pool.nbytes,), generator=g, device="cuda", dtype=torch.uint8))
+    tables = torch.full((copies, batch, width), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for c in range(copies):
+        for b in range(batch):
+            tables[c, b, :need[b]] = perm[at:at + need[b]]
+            at += need[b]
+    keeps = [_cut(n, share, g) for n in lens]
+    keep = torch.full((batch, max(len(k) for k in keeps) + 3), -5, dtype=torch.int32, device="cuda")
+    for b, k in enumerate(keeps):
+        keep[b, :len(k)] = k
+    acc = torch.rand(batch, width * 16 + 1, generator=g, device="cuda")
+    want, before, old = pool.data.clone(), pool.data.clone(), acc.clone()
+    rows = [t.view(-1, 2, ROW[layout], 8, 16) for t in (want, before)]
+    for b, k in enumerate(keeps):
+        j, i = k.long(), torch.arange(len(k), device="cuda")
+        src, dst = tables[0, b].long()[j // 16], tables[-1, b].long()[i // 16]
+        rows[0][dst, i % 16 // 8, :, i % 8] = rows[1][src, j % 16 // 8, :, j % 8]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gw.kv_evict_compact(pool, tables[0], G.i32(lens), keep, G.i32([len(k) for k in keeps]), acc,
+                        tables[1] if other_pages else None, status)
+    assert int(status) == 0 and torch.equal(pool.data, want)
+    for b, k in enumerate(keeps):
+        assert torch.equal(acc[b, :len(k)], old[b, k.long()])
+        assert bool((acc[b, len(k):lens[b]] == 0).all()) and torch.equal(acc[b, lens[b]:], old[b, lens[b]:])
+
+
+@pytest.mark.parametrize("layout", ["folded", "full", "folded_e4m3"])
+@pytest.mark.parametrize("lens,heads,ctas", [([20001, 300, 8192], 8, 2), ([8192 - 37 * b for b in range(16)], 32, 0),
+                                             ([6000], 16, 1)])
+def test_weights_of_many_tiles_a_block(layout, lens, heads, ctas):
+    """Blocks of the weights pass that go through more tiles than they have
+    stages; the bits do not depend on the CTA cap."""
+    c = Cache(layout, lens, heads)
+    acc = c.new_acc(0.25)
+    old = acc.clone()
+    try:
+        gw.set_max_ctas(ctas)
+        out, lse = c.run(acc)
+    finally:
+        gw.set_max_ctas(0)
+    assert int(c.status) == 0
+    c.check(out, lse, acc, old)
+    again = old.clone()
+    out2, lse2 = c.run(again)
+    assert torch.equal(again, acc) and torch.equal(out2, out) and torch.equal(lse2, lse)

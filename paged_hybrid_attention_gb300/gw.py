@@ -155,26 +155,26 @@ def _invalid(fn, what):
     raise GwError(GW_ERR_INVALID_ARG, "%s: %s" % (fn, what))
 
 
-def _on_device(fn, stream, needed, *others):
-    """The tensors `needed`, by name, and the `others` that are not None lie on
-    one CUDA device, which the stream (the current one if None) belongs to and
-    which is the current device, since the library launches there.  Returns the
-    stream's handle."""
-    first = None
-    for name, t in needed.items():
+def _missing(fn, **tensors):
+    """Refuses the first of these that is None, by its name."""
+    for name, t in tensors.items():
         if t is None:
             _invalid(fn, "%s is None" % name)
-        if first is None:
-            first, dev = t, t.get_device()  # -1 on the CPU
-        elif t.get_device() != dev:
-            _invalid(fn, "tensors on %s and %s" % (first.device, t.device))
-    for t in others:
+
+
+def _on_device(fn, stream, *tensors):
+    """Every tensor (None: left out, but not the first) on one CUDA device,
+    which the stream (the current one if None) belongs to and which is the
+    current device, since the library launches there.  Returns the stream's
+    handle."""
+    dev = tensors[0].get_device()  # -1 on the CPU
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            _invalid(fn, "tensors on %s and %s" % (first.device, t.device))
+            _invalid(fn, "tensors on %s and %s" % (tensors[0].device, t.device))
     if dev < 0:
-        _invalid(fn, "tensors on %s, not on a CUDA device" % first.device)
+        _invalid(fn, "tensors on %s, not on a CUDA device" % tensors[0].device)
     if dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
-        _invalid(fn, "tensors on %s, but the current device or the stream is another" % first.device)
+        _invalid(fn, "tensors on %s, but the current device or the stream is another" % tensors[0].device)
     # the raw handle costs 0.1 us, a torch.cuda.Stream object 2.9 us
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -257,7 +257,7 @@ def rope_cs_scaled(theta, rot_dim, head_dim, max_pos, kind="none", factor=1.0, l
         _invalid(fn, "unknown kind %r" % (kind,))
     if out is None:
         out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
-    handle = _on_device(fn, stream, dict(out=out))
+    handle = _on_device(fn, stream, out)
     _dense(fn, "out", out, torch.float32, max_pos, rot_dim // 2, 2)
     sc = RopeScaling(ROPE_KINDS[kind], 0, factor, low, high, orig_max_pos, amplitude)
     _check(_lib.gw_rope_cs_scaled(out.data_ptr(), float(theta), int(rot_dim), int(head_dim), int(max_pos),
@@ -271,9 +271,11 @@ def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, invers
     any strides, the last one 1) rotated by pos int32 [rows] into `out` (x
     itself: in place; a new contiguous tensor if None), which is returned."""
     fn = "gw_rope_rows"
-    if out is None and x is not None:
+    if x is None or pos is None or rope_cs is None:  # a call of _missing costs as much as all checks below
+        _missing(fn, x=x, pos=pos, rope_cs=rope_cs)
+    if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    handle = _on_device(fn, stream, dict(x=x, out=out, pos=pos, rope_cs=rope_cs), dev_status)
+    handle = _on_device(fn, stream, x, out, pos, rope_cs, dev_status)
     elem = ELEMS.get(x.dtype)
     if x.dim() != 3 or elem is None or out.dtype != x.dtype or out.shape != x.shape:
         _invalid(fn, "x and out must be [rows, heads, head_dim] of one of bf16, fp16, fp32 (got %s %s and %s %s)" %
@@ -285,8 +287,8 @@ def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, invers
     if dim > 1 and (x1 != 1 or y1 != 1):
         _invalid(fn, "the last dimension of x and out must have stride 1")
     _vector(fn, "pos", pos, rows)
-    _dense(fn, "rope_cs", rope_cs, torch.float32, None, rot_dim // 2, 2)
     max_pos = rope_cs.shape[0]
+    _dense(fn, "rope_cs", rope_cs, torch.float32, max_pos, rot_dim // 2, 2)
     _check(_lib.gw_rope_rows(x.data_ptr(), xr, xh, out.data_ptr(), yr, yh, elem, rows, heads, dim, rot_dim,
                              PAIRS_INTERLEAVED if interleaved else PAIRS_HALF, 1 if inverse else 0, pos.data_ptr(),
                              rope_cs.data_ptr(), max_pos, _addr(dev_status), handle))
@@ -389,8 +391,12 @@ def decode_attn_global_acc(pool, q, out, lse, acc, cu_q_rows, seq_lens, block_ta
     float32 [rows, heads] or None), and acc [batch, stride] = decay * acc +
     each cached token's softmax weights summed over the heads."""
     fn = "gw_decode_attn_global_acc"
-    handle = _on_device(fn, stream, dict(q=q, out=out, acc=acc, cu_q_rows=cu_q_rows, seq_lens=seq_lens,
-                                         block_table=block_table, workspace=workspace), pool.data, lse, dev_status)
+    if (q is None or out is None or acc is None or cu_q_rows is None or seq_lens is None or block_table is None or
+            workspace is None):
+        _missing(fn, q=q, out=out, acc=acc, cu_q_rows=cu_q_rows, seq_lens=seq_lens, block_table=block_table,
+                 workspace=workspace)
+    handle = _on_device(fn, stream, pool.data, q, out, lse, acc, cu_q_rows, seq_lens, block_table, workspace,
+                        dev_status)
     batch = seq_lens.numel()
     if q.dim() != 3:
         _invalid(fn, "q must be [rows, heads, 512] (got %s)" % list(q.shape))
@@ -421,7 +427,9 @@ def kv_evict_select(acc, seq_lens, budget, keep_idx, keep_lens, sinks=0, recent=
     between), ascending, into keep_idx int32 [batch, >= budget], and their
     number into keep_lens int32 [batch]."""
     fn = "gw_kv_evict_select"
-    handle = _on_device(fn, stream, dict(acc=acc, seq_lens=seq_lens, keep_idx=keep_idx, keep_lens=keep_lens), dev_status)
+    if acc is None or seq_lens is None or keep_idx is None or keep_lens is None:
+        _missing(fn, acc=acc, seq_lens=seq_lens, keep_idx=keep_idx, keep_lens=keep_lens)
+    handle = _on_device(fn, stream, acc, seq_lens, keep_idx, keep_lens, dev_status)
     batch = seq_lens.numel()
     _vector(fn, "seq_lens", seq_lens, batch)
     _vector(fn, "keep_lens", keep_lens, batch)
@@ -438,8 +446,10 @@ def kv_evict_compact(pool, block_table, seq_lens, keep_idx, keep_lens, acc=None,
     """gw_kv_evict_compact: each sequence's kept rows moved to its front, in
     its own pages or into those of dst_block_table; acc moves along in place."""
     fn = "gw_kv_evict_compact"
-    handle = _on_device(fn, stream, dict(block_table=block_table, seq_lens=seq_lens, keep_idx=keep_idx,
-                                         keep_lens=keep_lens), pool.data, acc, dst_block_table, dev_status)
+    if block_table is None or seq_lens is None or keep_idx is None or keep_lens is None:
+        _missing(fn, block_table=block_table, seq_lens=seq_lens, keep_idx=keep_idx, keep_lens=keep_lens)
+    handle = _on_device(fn, stream, pool.data, block_table, seq_lens, keep_idx, keep_lens, acc, dst_block_table,
+                        dev_status)
     batch = seq_lens.numel()
     _vector(fn, "seq_lens", seq_lens, batch)
     _vector(fn, "keep_lens", keep_lens, batch)

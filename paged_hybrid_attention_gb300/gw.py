@@ -179,6 +179,16 @@ def _on_device(fn, stream, *tensors):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on this stream (None: the current one), out of
+    that stream's memory: a block of another stream's may still be read there
+    by work that came before."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -243,7 +253,7 @@ def rope_cs(theta, rot_dim, head_dim, max_pos, out=None, device="cuda", stream=N
     """gw_rope_cs: the float32 [max_pos, rot_dim/2, 2] (cos, sin) table of
     gw_kv_append, computed by the library on the GPU (into `out` if given)."""
     if out is None:
-        out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        out = _empty((max_pos, rot_dim // 2, 2), torch.float32, device, stream)
     _check(_lib.gw_rope_cs(_ptr(out), float(theta), int(rot_dim), int(head_dim), int(max_pos), _stream(stream)))
     return out
 
@@ -256,7 +266,7 @@ def rope_cs_scaled(theta, rot_dim, head_dim, max_pos, kind="none", factor=1.0, l
     if kind not in ROPE_KINDS:
         _invalid(fn, "unknown kind %r" % (kind,))
     if out is None:
-        out = torch.empty((max_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        out = _empty((max_pos, rot_dim // 2, 2), torch.float32, device, stream)
     handle = _on_device(fn, stream, out)
     _dense(fn, "out", out, torch.float32, max_pos, rot_dim // 2, 2)
     sc = RopeScaling(ROPE_KINDS[kind], 0, factor, low, high, orig_max_pos, amplitude)
@@ -274,7 +284,7 @@ def rope_rows(x, pos, rope_cs, out=None, rot_dim=None, interleaved=False, invers
     if x is None or pos is None or rope_cs is None:  # a call of _missing costs as much as all checks below
         _missing(fn, x=x, pos=pos, rope_cs=rope_cs)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     handle = _on_device(fn, stream, x, out, pos, rope_cs, dev_status)
     elem = ELEMS.get(x.dtype)
     if x.dim() != 3 or elem is None or out.dtype != x.dtype or out.shape != x.shape:

@@ -228,8 +228,8 @@ gw_status gw_rope_cs(float* rope_cs, double theta, int32_t rot_dim, int32_t head
  *             outside [0, max_pos) is left as it was in y (GW_DEV_POS_RANGE).
  *   rope_cs   float32 [max_pos][rot_dim/2][2], 16-byte aligned (gw_rope_cs,
  *             gw_rope_cs_scaled).
- *   head_dim in [2, 1024], rot_dim even in [2, head_dim].  num_rows or
- *   num_heads of 0 is a no-op.
+ *   head_dim in [2, 1024], rot_dim even in [2, head_dim], num_heads at most
+ *   2^30.  num_rows or num_heads of 0 is a no-op.
  * K rows that are to be cached with interleaved pairs: rotate them here, then
  * append them at position 0, whose angle is 0 (gw_kv_append then stores them
  * as they are; their slot says where they go).

@@ -28,6 +28,9 @@ gw_status fail(gw_status code, const char* fn, const char* fmt, ...) {
 // Bound on the strides that callers give (elements): offsets stay in 64 bits.
 constexpr int64_t kMaxRowStride = int64_t{1} << 40;
 
+// gw_rope_rows counts heads in 32 bits, some thousands past the last one.
+constexpr int32_t kMaxRopeHeads = 1 << 30;
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -211,6 +214,7 @@ gw_status gw_rope_rows(const void* x, int64_t x_row_stride, int64_t x_head_strid
   if (pairs != GW_PAIRS_HALF && pairs != GW_PAIRS_INTERLEAVED)
     return fail(GW_ERR_INVALID_ARG, fn, "unknown pairs %d", pairs);
   if (num_rows < 0 || num_heads < 0) return fail(GW_ERR_INVALID_ARG, fn, "num_rows < 0 or num_heads < 0");
+  if (num_heads > kMaxRopeHeads) return fail(GW_ERR_INVALID_ARG, fn, "num_heads (%d) above 2^30", num_heads);
   if (head_dim < 2 || head_dim > 1024 || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2)
     return fail(GW_ERR_INVALID_ARG, fn, "need head_dim in [2, 1024] and an even rot_dim in [2, head_dim] (%d, %d)",
                 head_dim, rot_dim);

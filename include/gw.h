@@ -265,7 +265,8 @@ typedef struct gw_rope_scaling {
  *   NONE    f_i = inv_f_i
  *   LINEAR  f_i = inv_f_i / factor                (positions interpolated)
  *   NTK     theta replaced by theta * factor^(head_dim / (head_dim - 2)), so
- *           that the lowest frequency of a full head is divided by factor
+ *           that the lowest frequency of a full head is divided by factor (a
+ *           product outside float64's normal range is an error)
  *   RAMP    n_i = orig_max_pos * inv_f_i / (2 pi) turns over the trained
  *           context, g_i = clamp((n_i - low) / (high - low), 0, 1),
  *           f_i = inv_f_i * (g_i + (1 - g_i) / factor)

@@ -291,7 +291,10 @@ gw_status gw_rope_cs_scaled(float* rope_cs, double theta, int32_t rot_dim, int32
   if (sc.kind == GW_ROPE_RAMP &&
       (!positive(sc.orig_max_pos) || !(sc.low >= 0.0) || !(sc.high > sc.low) || !std::isfinite(sc.high)))
     return fail(GW_ERR_INVALID_ARG, fn, "RAMP needs orig_max_pos > 0 and 0 <= low < high, all finite");
-  if (sc.kind == GW_ROPE_NTK) theta *= std::pow(sc.factor, static_cast<double>(head_dim) / (head_dim - 2));
+  if (sc.kind == GW_ROPE_NTK) {
+    theta *= std::pow(sc.factor, static_cast<double>(head_dim) / (head_dim - 2));
+    if (!std::isnormal(theta)) return fail(GW_ERR_INVALID_ARG, fn, "NTK: theta * factor^(...) leaves float64's range");
+  }
   RopeFreqs fr{};
   for (int i = 0; i < rot_dim / 2; ++i) {
     double f = std::pow(theta, (-2.0 * i) / head_dim);

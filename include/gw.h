@@ -78,9 +78,9 @@ typedef int32_t gw_status;
 #define GW_DEV_TIMEOUT 16    /* a bounded wait gave up (work abandoned)       */
 #define GW_DEV_WORKSPACE 32  /* the step needs more split-KV partials than the
                                 workspace was sized for (nothing computed)    */
-#define GW_DEV_KEEP_RANGE 64 /* keep_idx not ascending or outside [0, seq_len),
-                                or keep_lens outside [0, min(keep_stride,
-                                seq_len)]                                     */
+#define GW_DEV_KEEP_RANGE 64 /* keep_idx not ascending, below its place or
+                                outside [0, seq_len), or keep_lens outside
+                                [0, min(keep_stride, seq_len)]                */
 
 /* ---- pool description --------------------------------------------------- */
 #define GW_KV_BF16 0
@@ -520,7 +520,8 @@ gw_status gw_kv_evict_select(const float* acc, int64_t acc_stride, int32_t batch
  *              acc[b][keep_lens[b] .. seq_lens[b]) becomes 0, as a token
  *              appended there expects.
  *   keep_idx   as gw_kv_evict_select writes it (or any ascending choice).  An
- *              entry that is not above the one before it, or outside
+ *              entry that is not above the one before it, below its own place
+ *              i (as entries behind such a one can be) or outside
  *              [0, seq_lens[b]), is skipped (GW_DEV_KEEP_RANGE); so is its
  *              acc.  A sequence whose length is outside
  *              [0, max_pages_per_seq * 16] (GW_DEV_LEN_RANGE), or whose

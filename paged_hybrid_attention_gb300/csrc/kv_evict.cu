@@ -268,7 +268,8 @@ struct RowShape {
   static constexpr int kPageBytes = kPage * kBlk * 16;
 };
 
-// The source token of kept token i, or -1 if keep_idx does not ascend there.
+// The source token of kept token i, or -1 if keep_idx does not ascend there or
+// has fallen below i, where a row would move backwards.
 __device__ __forceinline__ int source_of(const int32_t* keep, int i, int L) {
   const int j = keep[i];
   const int before = i > 0 ? keep[i - 1] : -1;

@@ -129,3 +129,24 @@ def test_weights_of_many_tiles_a_block(layout, lens, heads, ctas):
     again = old.clone()
     out2, lse2 = c.run(again)
     assert torch.equal(again, acc) and torch.equal(out2, out) and torch.equal(lse2, lse)
+
+
+def test_entries_below_their_place_stay():
+    """Behind an entry that is skipped others can ascend and still lie below
+    their own place: they are skipped too, with their weights."""
+    c = Cache("folded", [100] * 4, 8)
+    keeps = [[5, 0, 1, 9], [-1, 0, 2, 3], [0, 1, 0, 1], [-3, -2, -1, 50]]
+    moves = [{0: 5, 3: 9}, {2: 2, 3: 3}, {0: 0, 1: 1}, {3: 50}]
+    before = c.pool.data.clone()
+    acc = torch.rand(4, c.width * 16, device="cuda")
+    want, old = acc.clone(), acc.clone()
+    gw.kv_evict_compact(c.pool, c.bt, c.n, torch.tensor(keeps, dtype=torch.int32, device="cuda"), G.i32([4] * 4), acc,
+                        dev_status=c.status)
+    assert int(c.status) == gw.GW_DEV_KEEP_RANGE
+    expect, src = before.clone().view(-1, 2, 80, 8, 16), before.view(-1, 2, 80, 8, 16)
+    for b, m in enumerate(moves):
+        for i, j in m.items():
+            expect[int(c.table[b, i // 16]), i % 16 // 8, :, i % 8] = src[int(c.table[b, j // 16]), j % 16 // 8, :, j % 8]
+            want[b, i] = old[b, j]
+        want[b, 4:100] = 0
+    assert torch.equal(c.pool.data, expect.reshape(-1)) and torch.equal(acc, want)

@@ -616,9 +616,11 @@ size_t gw_noalloc_scratch_bytes(void);
  * cannot take the whole GPU.  The decode and prompt-row kernels here are
  * persistent with one CTA per SM (their shared memory allows no second), and
  * deal their work round-robin over the CTAs they have, so a CTA cap is an SM
- * cap (gw_rope_rows keeps to the appends' limit; the combine, the eviction
- * calls and gw_rope_cs_scaled are short and not capped): a prefill lane launched with a cap of N and a decode lane with the
- * SM count minus N run side by side on disjoint SMs.  Results do not depend
+ * cap (gw_rope_rows keeps to the appends' limit, gw_kv_evict_compact to one
+ * block per allowed SM; the combine, with the weights pass beside it,
+ * gw_kv_evict_select and gw_rope_cs_scaled take a few to some tens of
+ * microseconds and are not capped): a prefill lane launched with a cap of N and
+ * a decode lane with the SM count minus N run side by side on disjoint SMs.  Results do not depend
  * on the cap (a work unit's arithmetic never depends on which CTA runs it).
  * The setting is per host thread and is read when a call launches (for a
  * CUDA graph: when it is captured).

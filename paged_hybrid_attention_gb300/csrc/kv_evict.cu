@@ -321,15 +321,13 @@ __device__ __forceinline__ void move_weights(float* acc, const int32_t* keep, in
   for (int64_t i = static_cast<int64_t>(n) + rank * kMoveThreads + tid; i < L; i += ctas * kMoveThreads) acc[i] = 0.f;
 }
 
+// One walk: column block pair `col` of sequence b, or its weights (-1).  It may
+// begin before the blocks' last one has ended: no two walks share a byte.
 template <int LAYOUT>
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactArgs a, int ctas) {
+__device__ __forceinline__ void compact_walk(const CompactArgs& a, int b, int col, int rank, int ctas) {
   using R = RowShape<LAYOUT>;
   constexpr int W = kWalkCols;
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.y, tid = threadIdx.x;
-  const int rank = static_cast<int>(blockIdx.x) % ctas;
-  const int col = static_cast<int>(blockIdx.x) / ctas - (a.acc ? 1 : 0);  // -1: the weights
+  const int tid = threadIdx.x;
   const int L = a.seq_lens[b], n = a.keep_lens[b];
   const bool reports = col == 0;
   if (L < 0 || L > a.max_pages * kPage) {  // as below, the same for all of a cluster
@@ -393,17 +391,41 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
   }
 }
 
+// A cluster of `ctas` blocks per walk, sequences along y; kTurns: fewer
+// clusters than walks, which take them in turn (a kernel of its own: the loop
+// takes 54 registers instead of 40, and held to 40 it spilled and cost every
+// move 2 to 3%).
+template <int LAYOUT, bool kTurns>
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactArgs a, int ctas) {
+  pdl_wait();
+  pdl_trigger();
+  const int rank = static_cast<int>(blockIdx.x) % ctas, first = static_cast<int>(blockIdx.x) / ctas;
+  if constexpr (kTurns) {
+    const int per_seq = RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0);
+    for (int walk = first; walk < per_seq * a.batch; walk += static_cast<int>(gridDim.x) / ctas)
+      compact_walk<LAYOUT>(a, walk / per_seq, walk % per_seq - (a.acc ? 1 : 0), rank, ctas);
+  } else {
+    compact_walk<LAYOUT>(a, blockIdx.y, first - (a.acc ? 1 : 0), rank, ctas);
+  }
+}
+
 template <int LAYOUT>
 cudaError_t launch_compact_layout(const CompactArgs& a, cudaStream_t st) {
   // As many blocks to a walk as leave the blocks of all walks on the GPU at
   // once, three per SM less a twelfth that clusters leave unused.  1 x 131072
   // folded rows to a quarter: eight 34 us, four 50, one 91; 3 x 131072: three
-  // 85, two 102, one 115; 8 x 131072: one 191, two 233.
-  const int64_t walks = static_cast<int64_t>(RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0)) * a.batch;
-  const int64_t room = 11 * static_cast<int64_t>(grid_ctas()) / (4 * walks);
+  // 85, two 102, one 115; 8 x 131072: one 191, two 233.  Under a CTA cap there
+  // are as many blocks as SMs are allowed, since three do not keep to one SM.
+  const int per_seq = RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0);
+  const int64_t walks = static_cast<int64_t>(per_seq) * a.batch;
+  const bool capped = grid_ctas() < num_sms();
+  const int64_t room = capped ? grid_ctas() / walks : 11 * static_cast<int64_t>(grid_ctas()) / (4 * walks);
   const int ctas = static_cast<int>(room < 1 ? 1 : room > kMaxMoveCtas ? kMaxMoveCtas : room);
-  const dim3 grid((RowShape<LAYOUT>::kBlk / kWalkCols + (a.acc ? 1 : 0)) * ctas, a.batch);
-  return launch_cluster(evict_compact_kernel<LAYOUT>, grid, dim3(kMoveThreads), ctas, st, a, ctas);
+  const int clusters = grid_ctas() / ctas;
+  if (capped && clusters < walks)
+    return launch_cluster(evict_compact_kernel<LAYOUT, true>, dim3(clusters * ctas), dim3(kMoveThreads), ctas, st, a, ctas);
+  return launch_cluster(evict_compact_kernel<LAYOUT, false>, dim3(per_seq * ctas, a.batch), dim3(kMoveThreads), ctas, st, a,
+                        ctas);
 }
 
 }  // namespace

@@ -150,3 +150,63 @@ def test_entries_below_their_place_stay():
             want[b, i] = old[b, j]
         want[b, 4:100] = 0
     assert torch.equal(c.pool.data, expect.reshape(-1)) and torch.equal(acc, want)
+
+
+@pytest.mark.parametrize("layout,batch", [("folded", 1), ("folded", 4), ("full", 2), ("folded_e4m3", 3)])
+@pytest.mark.parametrize("share", [0.25, "all but one"])
+def test_moves_under_a_cta_cap(layout, batch, share):
+    """Few blocks that take the walks in turn, and clusters that do: the same
+    bytes and weights."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    lens = [9001 - 1111 * b for b in range(batch)]
+    need = [(n + 15) // 16 for n in lens]
+    pool = gw.KVPool(layout, "e4m3" if layout == "folded_e4m3" else "bf16", sum(need))
+    start = torch.randint(0, 256, (pool.nbytes,), generator=g, device="cuda", dtype=torch.uint8)
+    table = torch.full((batch, max(need)), -1, dtype=torch.int32, device="cuda")
+    perm = torch.randperm(sum(need), generator=g, device="cuda").to(torch.int32)
+    keep = torch.full((batch, max(lens)), -5, dtype=torch.int32, device="cuda")
+    n = []
+    for b in range(batch):
+        table[b, :need[b]] = perm[sum(need[:b]):sum(need[:b + 1])]
+        k = _cut(lens[b], share, g)
+        keep[b, :len(k)] = k
+        n.append(len(k))
+    weights = torch.rand(batch, 16 * max(need), generator=g, device="cuda")
+    got = []
+    try:
+        for cap in (0, 1, 7, 50, 100, 130):
+            pool.data.copy_(start)
+            acc = weights.clone()
+            gw.set_max_ctas(cap)
+            gw.kv_evict_compact(pool, table, G.i32(lens), keep, G.i32(n), acc)
+            got.append((pool.data.clone(), acc))
+    finally:
+        gw.set_max_ctas(0)
+    for data, acc in got[1:]:
+        assert torch.equal(data, got[0][0]) and torch.equal(acc, got[0][1])
+
+
+def test_the_cta_cap_holds_for_moves():
+    """One block takes all 164 walks of four sequences in turn: many times the
+    time that they take at once."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    L, batch = 8192, 4
+    pool = gw.KVPool("folded", "bf16", batch * L // 16)
+    table = torch.arange(batch * L // 16, dtype=torch.int32, device="cuda").view(batch, -1)
+    keep = torch.stack([_cut(L, 0.5, g) for _ in range(batch)])
+    acc, lens, n = torch.rand(batch, L, device="cuda"), G.i32([L] * batch), G.i32([L // 2] * batch)
+    times = []
+    try:
+        for cap in (0, 1):
+            gw.set_max_ctas(cap)
+            for _ in range(2):
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                torch.cuda.synchronize()
+                a.record()
+                gw.kv_evict_compact(pool, table, lens, keep, n, acc)
+                b.record()
+                torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+    finally:
+        gw.set_max_ctas(0)
+    assert times[1] > 8 * times[0], times

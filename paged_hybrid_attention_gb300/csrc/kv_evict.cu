@@ -432,8 +432,11 @@ cudaError_t launch_compact_layout(const CompactArgs& a, cudaStream_t st) {
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t st) {
   // Lengths are device values: the row stride bounds them.  More blocks per
-  // sequence while each would still have 4096 tokens (8192 x 16 tokens: two
-  // blocks each 10.8 us, one 11.7, eight 11.6 before later steps).
+  // sequence while each would still have more than 4096 tokens.  With 1024 |
+  // 2048 | 4096 | 8192 | 16384 instead, 16 x 8192 tokens take 11.8 | 10.9 | 10.7 |
+  // 10.6 | 10.7 us, 16 x 16384 18.9 | 18.9 | 10.2 | 10.9 | 13.1, 1 x 8192 9.7 |
+  // 9.4 | 9.7 | 10.5 | 10.5, 8 x 131072 16.1 with any.  (128 x 16384, which fill
+  // the GPU with one block each: 84 | 84 | 37 | 21 | 14.)
   int ctas = 1;
   while (ctas < kMaxSelCtas && a.acc_stride > static_cast<int64_t>(4096) * ctas) ctas *= 2;
   return launch_cluster(evict_select_kernel, dim3(static_cast<unsigned>(a.batch) * ctas), dim3(kSelThreads), ctas, st, a, ctas);

@@ -433,7 +433,9 @@ gw_status gw_decode_attn_global_lse(const gw_kv_pool* pool, const void* q, void*
  * enter P.V to 2^-15, on an e4m3 pool to 2^-11 and 2^-23 of a chunk's largest.
  * Sequences without exactly one row, or of invalid length,
  * keep their acc row; so does every acc[b][j] with j >= seq_lens[b].  With
- * decay 0 the old values are not read (they may be anything).
+ * decay 0 the old values are not read (they may be anything).  A logit of NaN
+ * or +inf makes the row's head NaN and its own token's acc NaN; that head then
+ * adds nothing to the other tokens, whose acc stays usable.
  *
  *   acc        float32 [batch][acc_stride], 4-byte aligned, caller-owned;
  *              acc_stride >= max_pages_per_seq * 16.  A token's entry is 0

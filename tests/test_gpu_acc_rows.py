@@ -155,3 +155,18 @@ def test_rows_against_float64(layout, spread):
             (rel + logit + 2.0 ** -15) * size + floor * w.amax(-1, keepdim=True) * v.abs().sum(0))
         off = (out[b].double() - want).abs()
         assert bool((off <= tol).all()), (b, float((off - tol).max()))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("at", [0, 70, 699])
+def test_a_key_of_nan_stays_with_its_token(layout, at):
+    """One token's key holds a NaN: every head's logit of it is NaN, so its
+    acc is, the rows are, and the other tokens' weights take nothing."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = _rows(layout, torch.randn(700, 128, generator=g, device="cuda"), torch.randn(700, 512, generator=g, device="cuda"))
+    rows[at, 512 if layout != "full" else 0] = float("nan")
+    q = torch.randn(1, 8, 512, generator=g, device="cuda").to(torch.bfloat16)
+    out, _, acc = _attend(layout, [rows], q, 0.05)
+    assert bool(out.isnan().all()) and bool(acc[0, at].isnan())
+    rest = torch.arange(acc.shape[1], device="cuda") != at
+    assert bool((acc[0, rest] == 0).all())

@@ -28,7 +28,7 @@
 // straight on the stored tiles (K = 32 per MMA): q enters as two e4m3 terms
 // [q_hi; q_lo] stacked along N (one MMA of N = 2 HQ per K-step, the softmax
 // adds the two logit columns), and P as two e4m3 terms accumulated into O by
-// two MMAs per K-step.  (One 128-token tile of
+// two MMAs per K-step (four e5m2 terms with weights, see global_decode_kernel).  (One 128-token tile of
 // eight slots halves the MMAs per byte but leaves nothing streaming during
 // QK^T and the softmax, and was slower.)
 //

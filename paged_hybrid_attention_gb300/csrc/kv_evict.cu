@@ -50,7 +50,7 @@ constexpr uint32_t kNoToken = 0, kProtected = 0xffffffffu;
 // but make each block read eight times as many counts of the others.)  It
 // ends with the first digit all of whose keys are kept.  Then the blocks
 // exchange how many of their tokens are kept or tied, and write their indices
-// in order.  8 x 131072 tokens take 15.6 us, 4.2 MB of weights read once: short
+// in order.  8 x 131072 tokens take 15 to 16 us, 4.2 MB of weights read once: short
 // passes between barriers bound it (a pass over 16 keys a thread is 1.2 us, its
 // barrier and sums 1.5 us).
 constexpr int kSelThreads = 1024;
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const Sele
 // need no order among themselves, and the next step's rows may be on their way
 // while this one's are written.
 // 8 x 131072 folded rows to 32768 take 190 to 200 us: 924 MB read (the 64-byte
-// pieces that hold a kept row) and 316 MB written, 0.95 of a copy's rate; to
-// 122880, 470 us (384 at a copy's rate).  Few sequences are bound by a step's
+// pieces that hold a kept row) and 316 MB written, 0.92 to 0.96 of a copy's rate;
+// to 122880, 470 us (384 at a copy's rate).  Few sequences are bound by a step's
 // round trip, about 1.4 us: their walks get more blocks.  512 rows per block and
 // step are the best: 256 took 284 us, 1024 278 us; four column blocks a walk are
 // no faster, one takes 264 us.

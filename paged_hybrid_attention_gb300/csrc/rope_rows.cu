@@ -411,9 +411,10 @@ cudaError_t launch_rows(const RopeRowsArgs& a, cudaStream_t st) {
 // series and of a product.  Over 200000 random chains of that length the values
 // were off by 2^-42 at most (the host's arithmetic, against 113 bits); each is
 // rounded once to float32.
-// 262144 x 64 entries take 33 us (134 MB, the floor 20 us), 32768 x 128 15 us:
-// about forty FP32 operations an entry bound it, and at the start of a thread
-// some 700 more.
+// 262144 x 64 entries take 33.5 us (134 MB, the floor 20 us), 32768 x 128 14.6 us
+// (the floor 5): about forty FP32 operations an entry bound it, at the start of a
+// thread some 700 more, and a last wave that is not full: with three blocks to an
+// SM 456 run at once, and these tables have 1024 and 512.
 struct Ff {
   float h, l;
 };

@@ -14,7 +14,11 @@
  * and, beside the step, the rotation of q rows and tables for scaled contexts
  * (gw_rope_rows, gw_rope_cs_scaled), and the eviction of a global cache by the
  * attention its tokens draw (gw_decode_attn_global_acc, gw_kv_evict_select,
- * gw_kv_evict_compact), which the pages do not have.
+ * gw_kv_evict_compact), which the pages do not have; and the verification of
+ * drafted tokens: a layer's q and k norms, rotation and append in one call
+ * (gw_norm_rope_append), attention of a tree of drafts (gw_tree_attn_local,
+ * gw_tree_attn_global) and the commit of what the target accepted
+ * (gw_tree_accept, gw_kv_tree_move), which the pages leave to the engine.
  *
  * Sources of the operations (page title, section):
  *   [pegainfer] "Gemma 4" (pegainfer model page): intro, "Scheduling",
@@ -81,6 +85,9 @@ typedef int32_t gw_status;
 #define GW_DEV_KEEP_RANGE 64 /* keep_idx not ascending, below its place or
                                 outside [0, seq_len), or keep_lens outside
                                 [0, min(keep_stride, seq_len)]                */
+#define GW_DEV_TREE_RANGE 128 /* a draft's parent not before it, or a path not
+                                ascending, below its place or outside the
+                                drafts                                        */
 
 /* ---- pool description --------------------------------------------------- */
 #define GW_KV_BF16 0
@@ -542,6 +549,181 @@ gw_status gw_kv_evict_compact(const gw_kv_pool* pool, int32_t batch, const int32
                               int64_t keep_stride, const int32_t* keep_lens, const int32_t* dst_block_table,
                               int32_t dst_max_pages, float* acc, int64_t acc_stride, int32_t* dev_status,
                               void* stream);
+
+/*
+ * gw_norm_rope_append - from a layer's projection to its attention call in one
+ * pass: the norms of the q, k and v heads, the rotation of q and k, the page
+ * write of k and v, and the q rows that the attention calls take.
+ *
+ * [pegainfer] "Architecture notes": K passes k_norm and RoPE, and on global
+ * layers V is the same projection through a scale-free norm.  With
+ * r(x) = 1 / sqrt(mean(x^2) + eps) over a head's elements:
+ *
+ *   q' = rope(q r(q) q_weight)     bf16 [num_rows][num_q_heads][head_dim] at q_out
+ *   k' = rope(k r(k) k_weight)     to the pool
+ *   v' = v r(v), or v if !v_norm   to the pool
+ *
+ * rope as in gw_kv_append (half pairs of the first rot_dim dims).  Everything
+ * is float32 until one rounding, to bf16 or the pool's type.  On folded pools,
+ * whose unrotated K dims are V's, dims [128, 512) of q' are also multiplied by
+ * k_weight, so that attention over the pool is attention with
+ * K[128:] = V[128:] k_weight[128:].
+ *
+ *   q, k, v    bf16; element (r, h, d) at q[r*q_row_stride + h*q_head_stride +
+ *              d], strides in elements: heads are slices of a packed projection
+ *              or tensors of their own.  16-byte aligned, strides multiples of
+ *              8.  k and v have the pool's kv_heads.  On folded pools v is k
+ *              (the same pointer and strides) and v_norm is 1.
+ *   q_weight, k_weight  float32 [head_dim], 16-byte aligned.
+ *   eps        finite, > 0.
+ *   slot, pos, rope_cs, max_pos  as for gw_kv_append.  A row whose slot is out
+ *              of range is not written to the pool (GW_DEV_SLOT_RANGE), its q'
+ *              is; a row whose pos is out of range writes nothing
+ *              (GW_DEV_POS_RANGE).
+ *   q_out      16-byte aligned; q itself if q is contiguous, otherwise it
+ *              overlaps none of q, k, v.
+ * num_rows 0 is a no-op; num_q_heads in [1, 1024].  A head whose sum of squares
+ * exceeds float32 comes out as zeros, one with a NaN as NaN.
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED (as gw_kv_append),
+ * GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                              const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                              int64_t v_row_stride, int64_t v_head_stride, int32_t num_rows, int32_t num_q_heads,
+                              const float* q_weight, const float* k_weight, float eps, int32_t v_norm,
+                              const int32_t* slot, const int32_t* pos, const float* rope_cs, int32_t max_pos,
+                              void* q_out, int32_t* dev_status, void* stream);
+
+/* ---- verification of drafted tokens ---------------------------------------
+ * A verification step gives a sequence n <= 64 rows: row 0 the newest token,
+ * rows 1.. a tree of drafts behind it, each after its parent.  The rows are
+ * the last n tokens of the sequence: appended at slots of tokens
+ * [seq_len - n, seq_len) in row order (gw_kv_append, gw_norm_rope_append), at
+ * the positions of their depth (seq_len - n + depth), which several drafts
+ * share.  Per layer:
+ *
+ *   gw_norm_rope_append(...)            or the engine's norms and gw_kv_append
+ *   gw_tree_attn_local / _global(...)
+ *
+ * and once the target has chosen a token after each row:
+ *
+ *   gw_tree_accept(...)                 the accepted path and new lengths
+ *   gw_kv_tree_move(...)                its rows to the front, per kind of pool
+ */
+
+/*
+ * gw_tree_attn_local - attention of drafted trees on a LOCAL pool.
+ *
+ * Sequence b's n rows are its last n tokens.  With base = seq_lens[b] - n, row
+ * r (of q head h, KV head h / (num_q_heads / kv_heads)) sees
+ *
+ *   the cached tokens j in [0, base) with j > pos[r] - window, and
+ *   the drafts i in [0, n) with bit i of tree_mask[r] set and pos[i] > pos[r] - window,
+ *
+ * and gives o = sum_j softmax_j(scale * q . K_j) V_j over them, zeros if it
+ * sees nothing.  A tree's mask word has the bits of the row's ancestors and
+ * its own; any word is allowed (a row of another document, a prefix that sees
+ * itself both ways).  n = 1 with mask 1 is a decode row.
+ *
+ *   q, out, cu_q_rows, seq_lens, block_table, max_pages_per_seq, window, scale,
+ *              dev_status, stream  as for gw_decode_attn_local.
+ *   tree_mask  uint64 [total_rows], 8-byte aligned; bits from n on are ignored.
+ *   pos        int32 [total_rows]: the rows' positions, at least base (a row
+ *              before it sees nothing: GW_DEV_POS_RANGE).
+ *   max_q_rows  bound on n, in [1, 64].
+ *   workspace  of gw_tree_workspace_bytes(...) bytes, 256-byte aligned; needs no
+ *              initialisation.
+ * A sequence with more than max_q_rows rows, or a length below its rows or
+ * beyond the block table, gets zero rows (GW_DEV_LEN_RANGE).  Entries of the
+ * block table before base - window + 1 may be anything.  A page outside
+ * [0, num_pages) counts as zeros (GW_DEV_PAGE_RANGE).  An infinity or NaN in
+ * the V row of any token from max(0, base - window + 1) to seq_lens[b] reaches
+ * the sequence's rows of that KV head, as zero weights multiply it.
+ * The chunks of a sequence depend on its length, rows and window only: a row is
+ * bit-identical whatever else is in the batch.
+ * bf16 and e4m3 pools.  batch at most 512.
+ * Errors: those of gw_decode_attn_local; GW_ERR_INVALID_ARG (tree_mask or pos
+ * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^27 or
+ * more).
+ */
+gw_status gw_tree_attn_local(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
+                             const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                             int32_t max_pages_per_seq, const uint64_t* tree_mask, const int32_t* pos,
+                             int32_t max_q_rows, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
+
+/*
+ * gw_tree_attn_global - attention of drafted trees on a global pool, all three
+ * layouts: as gw_tree_attn_local without a window (every row sees the cached
+ * tokens [0, base)) and without positions.  num_q_heads 8, 16 or 32.
+ */
+gw_status gw_tree_attn_global(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
+                              const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const uint64_t* tree_mask, int32_t max_q_rows, float scale,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Workspace bytes of a gw_tree_attn_local (window >= 1) or gw_tree_attn_global
+ * (window ignored) call of at most this size; 0 on an invalid description. */
+size_t gw_tree_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch, int32_t max_pages_per_seq,
+                               int32_t max_q_rows, int32_t window);
+
+/*
+ * gw_tree_accept - the drafts that the target's choices accept.
+ *
+ * Sequence b with n rows (cu_q_rows): from the root, row 0, the path goes on to
+ * the lowest child i (parent[i] the present row) whose draft[i] equals
+ * target[present row], until there is none.
+ *
+ *   parent, draft, target  int32 [total_rows]: each row's parent (a row of the
+ *              same tree before it, counted from the tree's first row; the
+ *              root's is not read), its token, and the token that the target
+ *              chose after it.  A row whose parent is not before it is never
+ *              accepted (GW_DEV_TREE_RANGE).
+ *   path       int32 [batch][path_stride], path_stride >= max_q_rows: the
+ *              path's rows, ascending from 0; entries from path_lens[b] on are
+ *              left as they were.
+ *   path_lens  int32 [batch]: rows of the path (0 for a sequence without rows).
+ *   next_tokens  int32 [batch] or NULL: target of the path's last row (left as
+ *              it was for a sequence without rows).
+ *   new_lens   int32 [batch] or NULL: seq_lens[b] - n + path_lens[b]; may be
+ *              seq_lens itself if gw_kv_tree_move is not called after it (that
+ *              call takes the length before).
+ * A sequence with n outside [0, max_q_rows] or seq_lens[b] < n has path_lens 0
+ * and keeps its length (GW_DEV_LEN_RANGE).
+ * max_q_rows in [1, 64]; batch in [0, 65535], 0 is a no-op.
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_tree_accept(int32_t batch, const int32_t* cu_q_rows, const int32_t* seq_lens, int32_t max_q_rows,
+                         const int32_t* parent, const int32_t* draft, const int32_t* target, int32_t* path,
+                         int64_t path_stride, int32_t* path_lens, int32_t* next_tokens, int32_t* new_lens,
+                         int32_t* dev_status, void* stream);
+
+/*
+ * gw_kv_tree_move - the rows of the accepted path to the front of the drafts:
+ * for i in [0, path_lens[b]) the row of token seq_lens[b] - n + path[b][i] is
+ * copied to token seq_lens[b] - n + i, bytes as they are, in every pool of the
+ * call (the layers of a kind, whose sequences share a block table).
+ *
+ *   pools      host array of n_pools in [1, 64] descriptions that differ in
+ *              base and num_pages only, over different memory.  Every layout.
+ *   cu_q_rows, seq_lens, block_table, max_pages_per_seq  of the step, lengths
+ *              with all drafts.
+ *   path, path_lens  as gw_tree_accept writes them.  An entry that is not above
+ *              the one before it, below its place or outside the drafts is
+ *              skipped (GW_DEV_TREE_RANGE), as is a sequence whose path_lens is
+ *              outside [0, min(n, path_stride)]; a sequence with n outside
+ *              [0, 64] or a length outside [n, max_pages_per_seq * 16] is
+ *              skipped (GW_DEV_LEN_RANGE).
+ *   A row whose page is outside [0, num_pages) is not moved
+ *   (GW_DEV_PAGE_RANGE).  The pages of a sequence's drafts must be its own.
+ * batch in [0, 65535]; 0 is a no-op.
+ * Errors: GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED (as gw_kv_append),
+ * GW_ERR_CUDA.  Asynchronous on `stream`.
+ */
+gw_status gw_kv_tree_move(const gw_kv_pool* pools, int32_t n_pools, int32_t batch, const int32_t* cu_q_rows,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t max_pages_per_seq,
+                          const int32_t* path, int64_t path_stride, const int32_t* path_lens, int32_t* dev_status,
+                          void* stream);
 
 /*
  * gw_merge_lse - merge n_parts attention results of the same rows computed

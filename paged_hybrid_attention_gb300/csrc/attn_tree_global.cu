@@ -1,0 +1,598 @@
+// Attention of drafted trees on GLOBAL layers (gw_tree_attn_global), on the
+// tensor cores (tcgen05): head dim 512, one KV head, all three pool layouts.
+//
+// Row r of a sequence's n <= 64 rows sees the cached tokens [0, L - n) and the
+// drafts of its mask word.  All heads share the KV head, so 128 / HQ rows x HQ
+// heads are the 128 rows of two products over the same cached rows:
+//   S[128 x N]    = Q[128 x 512] . K^T        (UMMA M = 128)
+//   O[128 x 256] += P[128 x N] . V[:, half]   (UMMA M = 128, N = 256)
+// O[128 x 512] in fp32 would fill tensor memory, so a unit is (row block, chunk
+// of tiles, half of the output dims), and both halves compute S.
+//
+// A tile is 64 tokens (full layout: 32) in pages of 8-token x 16-byte blocks,
+// which are UMMA core matrices: K-major B operand of Q.K^T, MN-major B operand
+// of P.V.  A unit of the upper half reads no V[0:128) of a folded page, one of
+// the full layout only its half of V.
+// Tensor memory: S (two buffers, P over them), half of Q, the O half; the other
+// half of Q is in shared memory.
+// On the e4m3 pool q (scaled by an exact power of two per row) is a sum of two
+// e4m3 terms, as in the decode kernel, and P of three e5m2 ones.
+//
+// Warp roles (224 threads): warps 0-3 Q rows, softmax, epilogue (a thread owns
+// a row), warp 4 copies, warp 5 issues Q.K^T and owns tensor memory, warp 6
+// issues P.V.  Every wait is bounded (GW_DEV_TIMEOUT).
+#include "plan.cuh"
+#include "tcgen05.cuh"
+
+namespace gw {
+namespace {
+
+constexpr int kM = 128;
+constexpr int kThreads = 224;
+// O is rescaled when a logit exceeds the reference by more than kLazy; on the
+// e4m3 pool a new reference lies kBelowMax below its logit, so that weights
+// reach 2^15 and a long tail counts down to 2^-23 of the largest.
+constexpr float kLazy = 8.f, kBelowMax = 7.f;
+constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
+
+template <int LAYOUT>
+struct TL;
+template <>
+struct TL<GW_LAYOUT_GLOBAL_FOLDED> {
+  static constexpr bool kE4 = false;
+  static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0;
+  static constexpr int kPages = 4;   // pages of a tile
+  static constexpr int kBufs = 2;    // tiles in shared memory
+  __device__ static int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
+};
+template <>
+struct TL<GW_LAYOUT_GLOBAL_FULL> {
+  static constexpr bool kE4 = false;
+  static constexpr int kPageBytes = 32768, kBlk = 128, kVcb = 64;
+  static constexpr int kPages = 2;
+  static constexpr int kBufs = 2;
+  __device__ static int k_cb(int ks) { return 2 * ks; }
+};
+template <>
+struct TL<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
+  static constexpr bool kE4 = true;
+  static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0;
+  static constexpr int kPages = 4;
+  static constexpr int kBufs = 4;
+  __device__ static int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
+};
+
+template <int LAYOUT>
+struct TSmem {
+  using T = TL<LAYOUT>;
+  uint8_t tiles[T::kBufs][T::kPages * T::kPageBytes];
+  uint8_t q[kM * 512];  // Q dims [256, 512): [row block 16][16-byte block 32][8][16 B]; e4m3: hi, then lo
+  uint64_t full[T::kBufs], empty[T::kBufs], s_ready[2], p_ready[2], pfree[2];
+  uint64_t q_full, q_free, o_done, o_free;
+  int32_t mask[T::kBufs];  // pages of the tile that were loaded
+  uint32_t tmem_base;
+  int32_t ub[kMaxTreeBatch + 1 + 32];
+};
+static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FOLDED>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FULL>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3>) <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ uint32_t cm_off(int r, int c, int chunks) {
+  return static_cast<uint32_t>(((r >> 3) * chunks + c) * 128 + (r & 7) * 16);
+}
+__device__ __forceinline__ void zero16(uint32_t dst) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void store_f32x8(float* dst, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// x as two e4m3 terms, hi = e4m3(x) and lo = e4m3(x - hi), two values at a time.
+__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+  const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3)));
+  hi = h2;
+  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+}
+
+struct Unit {
+  int s, half, q0, nq, n, base, row0;
+  int k0, k1;  // keys [k0, k1)
+  int nt;      // tiles of them
+  int nc;
+};
+
+// Unit u: (chunk, row block, half), so that the units that read the same pages
+// run at the same time.
+template <int HQ, int KN>
+__device__ __forceinline__ Unit unit_of(const LocalArgs& a, const int32_t* ub, int u) {
+  constexpr int QB = kM / HQ;
+  Unit w;
+  w.s = plan_seq(ub, a.batch, u);
+  w.row0 = a.cu_q_rows[w.s];
+  w.n = a.cu_q_rows[w.s + 1] - w.row0;
+  const int L = a.seq_lens[w.s];
+  w.base = L - w.n;
+  const TreeSpan sp = tree_span(L, w.n, a.window, HQ, kTreeGlobalTiles);
+  w.nc = sp.chunks();
+  const int r = u - ub[w.s];
+  w.half = r & 1;
+  const int cb = r >> 1, c = cb / sp.blocks;
+  w.q0 = (cb - c * sp.blocks) * QB;
+  w.nq = min(QB, w.n - w.q0);
+  w.k0 = c * sp.ct * kTreeTile;
+  w.k1 = min(L, w.k0 + sp.ct * kTreeTile);
+  w.nt = (w.k1 - w.k0 + KN - 1) / KN;
+  return w;
+}
+
+template <int LAYOUT, int HQ>
+__global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArgs a) {
+  using T = TL<LAYOUT>;
+  using SM = TSmem<LAYOUT>;
+  constexpr bool kE4 = T::kE4;
+  constexpr int KN = T::kPages * kPage;  // keys of a tile
+  constexpr int NB = T::kBufs;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  SM& sm = *reinterpret_cast<SM*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  int32_t* st = a.status;
+
+  if (tid == 0) {
+    for (int b = 0; b < NB; ++b) {
+      mbar_init(&sm.full[b], 1);
+      mbar_init(&sm.empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.s_ready[b], 1);
+      mbar_init(&sm.p_ready[b], kM);
+      mbar_init(&sm.pfree[b], 1);
+    }
+    mbar_init(&sm.q_full, kM);
+    mbar_init(&sm.q_free, 1);
+    mbar_init(&sm.o_done, 1);
+    mbar_init(&sm.o_free, kM);
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tc::alloc(&sm.tmem_base, 512);
+    tc::relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  plan_tree(a, sm.ub, sm.ub + kMaxTreeBatch + 1, 2, HQ, kTreeGlobalTiles, 512);
+  const int total = sm.ub[a.batch];
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == 4) {
+    // --------------------------------------------------------- page copies
+    // lane j < kPages copies page j of a tile: the whole page, or per block of
+    // 8 tokens the columns that the unit reads
+    const uint64_t pol = policy_evict_last();  // the other half and row blocks read them too
+    uint32_t gi = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+      const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
+      for (int t = 0; t < w.nt; ++t, ++gi) {
+        const int b = gi % NB;
+        const uint32_t use = gi / NB;
+        const int k = w.k0 + t * KN + lane * kPage;
+        int32_t pg = -1;
+        if (lane < T::kPages && k < w.k1) {
+          pg = bt[k / kPage];
+          if (pg < 0 || pg >= a.num_pages) {
+            set_status(st, GW_DEV_PAGE_RANGE);
+            pg = -1;
+          }
+        }
+        const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0);
+        if (use > 0 && !warp_wait(&sm.empty[b], (use - 1) & 1, st)) { ok = false; break; }
+        uint32_t bytes = T::kPageBytes;
+        if (LAYOUT == GW_LAYOUT_GLOBAL_FULL)
+          bytes = 2 * (64 + 32) * 128;
+        else if (w.half)
+          bytes = 2 * (T::kBlk * 4 / 5) * 128;  // without V[0:128), a fifth of the row
+        if (lane == 0) {
+          sm.mask[b] = static_cast<int32_t>(loaded);
+          mbar_arrive_expect_tx(&sm.full[b], static_cast<uint32_t>(__popc(loaded)) * bytes);
+        }
+        __syncwarp();
+        if (pg >= 0) {
+          uint8_t* dst = sm.tiles[b] + lane * T::kPageBytes;
+          const uint8_t* src = a.pool + static_cast<int64_t>(pg) * T::kPageBytes;
+          if (LAYOUT == GW_LAYOUT_GLOBAL_FULL) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+              const int o = tb * T::kBlk * 128, v = o + (T::kVcb + 32 * w.half) * 128;
+              bulk_g2s(dst + o, src + o, 64 * 128, &sm.full[b], pol);
+              bulk_g2s(dst + v, src + v, 32 * 128, &sm.full[b], pol);
+            }
+          } else if (w.half) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+              const int o = (tb * T::kBlk + T::kBlk / 5) * 128;
+              bulk_g2s(dst + o, src + o, (T::kBlk * 4 / 5) * 128, &sm.full[b], pol);
+            }
+          } else {
+            bulk_g2s(dst, src, T::kPageBytes, &sm.full[b], pol);
+          }
+        }
+      }
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------- Q.K^T issue
+    const uint32_t id_s = kE4 ? tc::idesc_e4m3(kM, KN, false, false) : tc::idesc_bf16(kM, KN, false, false);
+    // Q dims [256, 512): no-swizzle K-major, 128 B between 16-byte blocks, then
+    // the next 8 rows; e4m3: 16 blocks a term, the lo term 32 KB behind
+    const uint64_t dq = tc::smem_desc(smem_u32(sm.q), 128, kE4 ? 2048 : 4096);
+    uint32_t i = 0;
+    int wt = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+      if (!warp_wait(&sm.q_full, wt & 1, st)) break;
+      for (int j = 0; j < w.nt; ++j, ++i) {
+        const int b = i % NB, sb = i & 1;
+        if (!warp_wait(&sm.full[b], (i / NB) & 1, st)) { ok = false; break; }
+        // this S buffer holds P of tile i - 2 until its P.V is done
+        if (i >= 2 && !warp_wait(&sm.pfree[sb], ((i >> 1) - 1) & 1, st)) { ok = false; break; }
+        const uint32_t ta = smem_u32(sm.tiles[b]);
+        const int mask = sm.mask[b];
+        const int key0 = w.k0 + j * KN;
+        if (mask != (1 << T::kPages) - 1 || key0 + KN > w.k1) {
+          // pages not loaded, and V rows behind the last key (K rows only make
+          // logits that are masked): finite zeros
+          for (int pgi = 0; pgi < T::kPages; ++pgi) {
+            if ((mask >> pgi) & 1) continue;
+            for (int o = lane * 16; o < T::kPageBytes; o += 32 * 16) zero16(ta + pgi * T::kPageBytes + o);
+          }
+          for (int k = max(w.k1 - key0, 0); k < KN; ++k)
+            for (int cb = lane; cb < (kE4 ? 32 : 64); cb += 32)
+              zero16(ta + ((k >> 3) * T::kBlk + T::kVcb + cb) * 128 + (k & 7) * 16);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        tc::fence_after();
+        const uint64_t dk = tc::smem_desc(ta, 128, T::kBlk * 128);
+        const uint32_t ds = tmem + kColS + KN * sb;
+        if constexpr (kE4) {
+#pragma unroll
+          for (int ks = 0; ks < 16; ++ks) {
+            const uint64_t bd = dk + ((T::k_cb(ks) * 128) >> 4);
+            if (ks < 8) {
+              tc::mma_e4m3_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, ks > 0);
+              tc::mma_e4m3_ts_warp(ds, tmem + kColQ + 64 + 8 * ks, bd, id_s, true);
+            } else {
+              tc::mma_e4m3_warp(ds, dq + (((ks - 8) * 256) >> 4), bd, id_s, true);
+              tc::mma_e4m3_warp(ds, dq + ((32768 + (ks - 8) * 256) >> 4), bd, id_s, true);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 32; ++ks) {
+            const uint64_t bd = dk + ((T::k_cb(ks) * 128) >> 4);
+            if (ks < 16)
+              tc::mma_bf16_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, ks > 0);
+            else
+              tc::mma_bf16_warp(ds, dq + (((ks - 16) * 256) >> 4), bd, id_s, true);
+          }
+        }
+        tc::commit_warp(&sm.s_ready[sb]);
+        if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
+      }
+    }
+  } else if (warp == 6) {
+    // ------------------------------------------------------- P.V issue
+    const uint32_t id_o = kE4 ? tc::idesc_e5m2_e4m3(kM, 256, false, true) : tc::idesc_bf16(kM, 256, false, true);
+    uint32_t i = 0;
+    int wt = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+      for (int j = 0; j < w.nt; ++j, ++i) {
+        const int b = i % NB, sb = i & 1;
+        if (j == 0 && wt >= 1 && !warp_wait(&sm.o_free, (wt - 1) & 1, st)) { ok = false; break; }
+        if (!warp_wait(&sm.p_ready[sb], (i >> 1) & 1, st)) { ok = false; break; }
+        tc::fence_after();
+        const uint32_t ta = smem_u32(sm.tiles[b]);
+        const uint64_t dv =
+            tc::smem_desc(ta + (T::kVcb + (kE4 ? 16 : 32) * w.half) * 128, T::kBlk * 128, 128);
+        const uint32_t p = tmem + kColS + KN * sb;
+        if constexpr (kE4) {
+          // K-steps of 32 keys; P's terms at columns 0, 16 and 32 of the S buffer
+#pragma unroll
+          for (int kk = 0; kk < KN / 32; ++kk) {
+            const uint64_t bd = dv + ((kk * 4 * T::kBlk * 128) >> 4);
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+              tc::mma_e4m3_ts_warp(tmem + kColO, p + 16 * term + 8 * kk, bd, id_o, !(j == 0 && kk == 0 && term == 0));
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < KN / 16; ++kk)
+            tc::mma_bf16_ts_warp(tmem + kColO, p + 8 * kk, dv + ((kk * 2 * T::kBlk * 128) >> 4), id_o,
+                                 !(j == 0 && kk == 0));
+        }
+        tc::commit_warp(&sm.empty[b]);
+        tc::commit_warp(&sm.pfree[sb]);
+        if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
+      }
+    }
+  } else {
+    // ---------------------------------------- Q rows, softmax, epilogue
+    const int r = tid;
+    const int qi = r / HQ, hd = r % HQ;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
+    const uint32_t qs = smem_u32(sm.q);
+    TreeRow seen{};
+    float sc_q = 1.f;  // e4m3: 2^-e of the row's scaling
+    auto load_q = [&](const Unit& w) {
+      const bool ok_row = qi < w.nq;
+      seen = TreeRow{0x7fffffff, 0};
+      if (ok_row) seen = tree_row(a, w.row0, w.q0 + qi, w.n, w.base, false);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (static_cast<int64_t>(w.row0 + w.q0 + (ok_row ? qi : 0)) * HQ + hd) * 512);
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kE4) {
+        float mq = 0.f;
+#pragma unroll 16
+        for (int c = 0; c < 64; ++c) {
+          const uint4 x = ok_row ? src[c] : none;
+          const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mq = fmaxf(mq, fmaxf(fabsf(__uint_as_float(u4[i] << 16)), fabsf(__uint_as_float(u4[i] & 0xFFFF0000u))));
+        }
+        const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
+        const int e = min(125, max(-125, 7 - ex));
+        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        sc_q = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        // an eighth (64 dims) at a time, the second reading from L1
+#pragma unroll 1
+        for (int part = 0; part < 8; ++part) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int c8 = 0; c8 < 8; ++c8) {
+            const uint4 x = ok_row ? src[8 * part + c8] : none;
+            const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int hv = 0; hv < 2; ++hv) {
+              const uint32_t w0 = u4[2 * hv], w1 = u4[2 * hv + 1];
+              uint32_t h0, l0, h1, l1;
+              split_e4m3(__uint_as_float(w0 << 16) * up, __uint_as_float(w0 & 0xFFFF0000u) * up, h0, l0);
+              split_e4m3(__uint_as_float(w1 << 16) * up, __uint_as_float(w1 & 0xFFFF0000u) * up, h1, l1);
+              hi[2 * c8 + hv] = h0 | (h1 << 16);
+              lo[2 * c8 + hv] = l0 | (l1 << 16);
+            }
+          }
+          if (part < 4) {  // dims [0, 256): hi at columns 0..63, lo at 64..127
+            tc::st16(tmem + lane_base + kColQ + 16 * part, hi);
+            tc::st16(tmem + lane_base + kColQ + 64 + 16 * part, lo);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t at = qs + cm_off(r, 4 * (part - 4) + c, 16);
+              sts16(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+              sts16(at + 32768, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+            }
+          }
+        }
+      } else {
+        uint32_t qv[128];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {  // dims [0, 256) -> tensor memory
+          const uint4 x = ok_row ? src[c] : none;
+          qv[4 * c] = x.x;
+          qv[4 * c + 1] = x.y;
+          qv[4 * c + 2] = x.z;
+          qv[4 * c + 3] = x.w;
+        }
+#pragma unroll
+        for (int blk = 0; blk < 4; ++blk)
+          tc::st32(tmem + lane_base + kColQ + 32 * blk, *reinterpret_cast<uint32_t(*)[32]>(&qv[32 * blk]));
+#pragma unroll 8
+        for (int c = 0; c < 32; ++c) {  // dims [256, 512) -> shared memory
+          const uint4 x = ok_row ? src[32 + c] : none;
+          sts16(qs + cm_off(r, c, 32), x.x, x.y, x.z, x.w);
+        }
+      }
+      tc::wait_st();
+      fence_proxy_async_smem();
+      tc::fence_before();
+      mbar_arrive(&sm.q_full);
+    };
+    uint32_t gi = 0;
+    int wt = 0;
+    if (static_cast<int>(blockIdx.x) < total) load_q(unit_of<HQ, KN>(a, sm.ub, blockIdx.x));
+    for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+      const bool row_ok = qi < w.nq;
+      const TreeRow row = seen;
+      const float sc = a.scale_log2 * sc_q;
+      float m_ref = -INFINITY;
+      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      bool ok = true;
+      for (int j = 0; j < w.nt; ++j, ++gi) {
+        const int b = gi & 1;
+        if (!warp_wait(&sm.s_ready[b], (gi >> 1) & 1, st)) { ok = false; break; }
+        tc::fence_after();
+        uint32_t sv[KN];
+#pragma unroll
+        for (int c0 = 0; c0 < KN; c0 += 32)
+          tc::ld32(tmem + lane_base + kColS + KN * b + c0, *reinterpret_cast<uint32_t(*)[32]>(&sv[c0]));
+        tc::wait_ld();
+        const int key0 = w.k0 + j * KN;
+        if (!(key0 >= row.kmin && key0 + KN <= w.base)) {  // drafts, or a row without keys
+          const uint64_t m = tree_tile_mask(row, w.base, key0);
+          const uint32_t m0 = static_cast<uint32_t>(m), m1 = static_cast<uint32_t>(m >> 32);
+#pragma unroll
+          for (int c = 0; c < KN; ++c)
+            if (!(((c < 32 ? m0 : m1) >> (c & 31)) & 1)) sv[c] = __float_as_uint(-INFINITY);
+        }
+        float mg[KN / 8];
+#pragma unroll
+        for (int g8 = 0; g8 < KN / 8; ++g8) {
+          const float* x = reinterpret_cast<const float*>(&sv[g8 * 8]);
+          mg[g8] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        }
+        float mraw = mg[0];
+#pragma unroll
+        for (int g8 = 1; g8 < KN / 8; ++g8) mraw = fmaxf(mraw, mg[g8]);
+        const float mx = mraw * sc;
+        const bool raise = mx > m_ref + kLazy + (kE4 ? kBelowMax : 0.f);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float m_new = raise ? mx - (kE4 ? kBelowMax : 0.f) : m_ref;
+          const float alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
+          if (__any_sync(0xffffffffu, raise && m_ref != -INFINITY)) {
+            // O *= alpha for this warp's rows once P.V of the tile before is done
+            if (!warp_wait(&sm.pfree[(gi - 1) & 1], ((gi - 1) >> 1) & 1, st)) { ok = false; break; }
+            tc::fence_after();
+#pragma unroll 1
+            for (int blk = 0; blk < 8; ++blk) {
+              uint32_t o[32];
+              const uint32_t ad = tmem + lane_base + kColO + 32 * blk;
+              tc::ld32(ad, o);
+              tc::wait_ld();
+              if (raise && m_ref != -INFINITY) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              }
+              tc::st32(ad, o);
+            }
+            tc::wait_st();
+          }
+          if (raise) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lp[i] *= alpha;
+            m_ref = m_new;
+          }
+        }
+        // p = 2^(s sc - m), rounded for the product; l sums it as rounded, so
+        // that numerator and denominator round alike
+        const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+        uint32_t pw[32];
+        if constexpr (kE4) {
+          uint32_t pl[16];
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(__uint_as_float(sv[4 * v + i]), sc, neg_m));
+            uint32_t w3[3];
+            lp[v & 3] += tc::split_e5m2(p[0], p[1], p[2], p[3], w3);
+            pw[v] = w3[0];
+            pw[16 + v] = w3[1];
+            pl[v] = w3[2];
+          }
+          tc::st16(tmem + lane_base + kColS + KN * b + 32, pl);
+          tc::st32(tmem + lane_base + kColS + KN * b, pw);
+        } else {
+#pragma unroll
+          for (int v = 0; v < KN / 2; ++v) {
+            const float p0 = ex2(fmaf(__uint_as_float(sv[2 * v]), sc, neg_m));
+            const float p1 = ex2(fmaf(__uint_as_float(sv[2 * v + 1]), sc, neg_m));
+            __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
+            lp[v & 3] += __low2float(pb) + __high2float(pb);
+            pw[v] = *reinterpret_cast<uint32_t*>(&pb);
+          }
+          if constexpr (KN == 64)
+            tc::st32(tmem + lane_base + kColS + KN * b, pw);
+          else
+            tc::st16(tmem + lane_base + kColS + KN * b, *reinterpret_cast<uint32_t(*)[16]>(&pw[0]));
+        }
+        tc::wait_st();
+        tc::fence_before();
+        mbar_arrive(&sm.p_ready[b]);
+      }
+      if (!ok) break;
+      const int next = u + gridDim.x;
+      if (next < total) {
+        if (!warp_wait(&sm.q_free, wt & 1, st)) break;
+        tc::fence_after();
+        load_q(unit_of<HQ, KN>(a, sm.ub, next));
+      }
+      // ---- epilogue: this half of O, as output rows or as a chunk's part
+      if (!warp_wait(&sm.o_done, wt & 1, st)) break;
+      tc::fence_after();
+      const float l = (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t part = static_cast<int64_t>(u) * a.part_rows + r;
+      if (w.nc > 1 && row_ok) a.part_ml[part] = make_float2(m_ref, l);
+      uint16_t* dst = a.out + (static_cast<int64_t>(w.row0 + w.q0 + qi) * HQ + hd) * 512 + 256 * w.half;
+#pragma unroll 1
+      for (int blk = 0; blk < 8; ++blk) {
+        uint32_t o[32];
+        tc::ld32(tmem + lane_base + kColO + 32 * blk, o);
+        tc::wait_ld();
+        if (row_ok && w.nc > 1) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) store_f32x8(a.part_o + part * 256 + blk * 32 + c, &o[c]);
+        } else if (row_ok) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[c + 2 * e]) * inv,
+                                                        __uint_as_float(o[c + 2 * e + 1]) * inv);
+              pk[e] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+            *reinterpret_cast<uint4*>(dst + blk * 32 + c) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before();
+      mbar_arrive(&sm.o_free);
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
+}
+
+template <int LAYOUT, int HQ>
+cudaError_t launch_lh(const LocalArgs& a, cudaStream_t st) {
+  auto kern = global_tree_kernel<LAYOUT, HQ>;
+  const size_t smem = sizeof(TSmem<LAYOUT>);
+  cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(grid_ctas()), dim3(kThreads), smem, st, a);
+}
+
+template <int LAYOUT>
+cudaError_t launch_l(const LocalArgs& a, cudaStream_t st) {
+  switch (a.num_q_heads) {
+    case 8: return launch_lh<LAYOUT, 8>(a, st);
+    case 16: return launch_lh<LAYOUT, 16>(a, st);
+    case 32: return launch_lh<LAYOUT, 32>(a, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_global_tree_tc(int layout, const LocalArgs& a, cudaStream_t st) {
+  if (layout == GW_LAYOUT_GLOBAL_FOLDED_E4M3) return launch_l<GW_LAYOUT_GLOBAL_FOLDED_E4M3>(a, st);
+  return layout == GW_LAYOUT_GLOBAL_FOLDED ? launch_l<GW_LAYOUT_GLOBAL_FOLDED>(a, st)
+                                           : launch_l<GW_LAYOUT_GLOBAL_FULL>(a, st);
+}
+
+}  // namespace gw

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
 
 #include "gw_internal.h"
@@ -640,6 +641,303 @@ gw_status gw_kv_evict_compact(const gw_kv_pool* pool, int32_t batch, const int32
   a.acc_stride = acc_stride;
   a.status = dev_status;
   return cuda_status(launch_evict_compact(pool->layout, a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+// Layout of a gw_tree_attn_* workspace: the plan, then (m, l) and the fp32 rows
+// of every unit of sequences that have several chunks.
+struct TreeLayout {
+  size_t unit_base, ml, o, total;
+  int part_rows;
+};
+
+static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch, int max_pages, int max_q_rows,
+                              int window) {
+  const bool local = pool->layout == GW_LAYOUT_LOCAL;
+  const int group = local ? num_q_heads / pool->kv_heads : num_q_heads;
+  const int per = 128 / group, copies = local ? pool->kv_heads : 2;
+  const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff,
+                                     local ? kTreeLocalTiles : kTreeGlobalTiles);
+  // the most units of a sequence, over its rows n: blocks x chunks, of which
+  // there are at most kTreeMaxChunks unless a block has one chunk
+  int64_t units = 0;
+  for (int n = 1; n <= max_q_rows; ++n) {
+    const int blocks = ceil_div(n, per), most = blocks < kTreeMaxChunks ? kTreeMaxChunks / blocks : 1;
+    const int64_t u = static_cast<int64_t>(blocks) * (chunks < most ? chunks : most);
+    if (u > units) units = u;
+  }
+  units *= static_cast<int64_t>(copies) * batch;
+  TreeLayout l{};
+  l.part_rows = group * (per < max_q_rows ? per : max_q_rows);
+  l.unit_base = 0;
+  l.ml = round_up(static_cast<size_t>(batch + 1) * 4, 256);
+  if (chunks == 1) {
+    l.o = l.total = l.ml;
+    return l;
+  }
+  l.o = l.ml + round_up(static_cast<size_t>(units) * l.part_rows * 8, 256);
+  l.total = l.o + round_up(static_cast<size_t>(units) * l.part_rows * 256 * 4, 256);
+  return l;
+}
+
+// The geometry that a gw_tree_attn_* call and its workspace share.
+static gw_status check_tree(const char* fn, const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch,
+                            int32_t max_pages_per_seq, int32_t max_q_rows, int32_t window) {
+  const bool local = pool->layout == GW_LAYOUT_LOCAL;
+  if (batch < 0) return fail(GW_ERR_INVALID_ARG, fn, "batch < 0");
+  if (num_q_heads < 1 || num_q_heads % pool->kv_heads)
+    return fail(GW_ERR_INVALID_ARG, fn, "num_q_heads (%d) must be a positive multiple of kv_heads (%d)", num_q_heads,
+                pool->kv_heads);
+  const int group = num_q_heads / pool->kv_heads;
+  if (local && group != 1 && group != 2 && group != 4 && group != 8)
+    return fail(GW_ERR_UNSUPPORTED, fn, "query heads per KV head must be 1, 2, 4 or 8 (got %d)", group);
+  if (!local && num_q_heads != 8 && num_q_heads != 16 && num_q_heads != 32)
+    return fail(GW_ERR_UNSUPPORTED, fn, "num_q_heads must be 8, 16 or 32 (got %d)", num_q_heads);
+  if (batch > kMaxTreeBatch)
+    return fail(GW_ERR_UNSUPPORTED, fn, "batch (%d) exceeds %d sequences per call", batch, kMaxTreeBatch);
+  if (local && window < 1) return fail(GW_ERR_INVALID_ARG, fn, "window must be >= 1");
+  if (max_pages_per_seq < 1 || max_pages_per_seq > 0x7fffffff / 16)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be in [1, 2^27)");
+  if (max_q_rows < 1 || max_q_rows > kMaxTreeRows)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_q_rows (%d) outside [1, %d]", max_q_rows, kMaxTreeRows);
+  return GW_OK;
+}
+
+size_t gw_tree_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch, int32_t max_pages_per_seq,
+                               int32_t max_q_rows, int32_t window) {
+  const char* fn = "gw_tree_workspace_bytes";
+  g_err[0] = 0;
+  if (check_pool(pool, fn, false) != GW_OK) return 0;
+  if (check_tree(fn, pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window) != GW_OK) return 0;
+  return tree_layout(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window).total;
+}
+
+static gw_status tree_attn(const char* fn, bool local, const gw_kv_pool* pool, const void* q, void* out,
+                           int32_t num_q_heads, int32_t batch, const int32_t* cu_q_rows, const int32_t* seq_lens,
+                           const int32_t* block_table, int32_t max_pages_per_seq, const uint64_t* tree_mask,
+                           const int32_t* pos, int32_t max_q_rows, int32_t window, float scale, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  g_err[0] = 0;
+  gw_status s = check_pool(pool, fn);
+  if (s != GW_OK) return s;
+  if (local && pool->layout != GW_LAYOUT_LOCAL) return fail(GW_ERR_INVALID_ARG, fn, "pool layout is not LOCAL");
+  if (!local && pool->layout == GW_LAYOUT_LOCAL) return fail(GW_ERR_INVALID_ARG, fn, "pool layout is not GLOBAL");
+  s = check_tree(fn, pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window);
+  if (s != GW_OK) return s;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(GW_ERR_INVALID_ARG, fn, "scale must be finite and > 0");
+  if (batch == 0) return GW_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return fail(GW_ERR_INVALID_ARG, fn, "q/out NULL or not 16-byte aligned");
+  if (!cu_q_rows || !seq_lens || !block_table || !aligned(cu_q_rows, 4) || !aligned(seq_lens, 4) ||
+      !aligned(block_table, 4))
+    return fail(GW_ERR_INVALID_ARG, fn, "cu_q_rows/seq_lens/block_table NULL or misaligned");
+  if (!tree_mask || !aligned(tree_mask, 8)) return fail(GW_ERR_INVALID_ARG, fn, "tree_mask NULL or not 8-byte aligned");
+  if (local && (!pos || !aligned(pos, 4))) return fail(GW_ERR_INVALID_ARG, fn, "pos NULL or misaligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  if (!workspace || !aligned(workspace, 256)) return fail(GW_ERR_INVALID_ARG, fn, "workspace NULL or not 256-byte aligned");
+  const TreeLayout w = tree_layout(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window);
+  if (workspace_bytes < w.total)
+    return fail(GW_ERR_WORKSPACE, fn, "workspace_bytes %zu < %zu needed", workspace_bytes, w.total);
+  LocalArgs a{};
+  a.pool = static_cast<const uint8_t*>(pool->base);
+  a.num_pages = pool->num_pages;
+  a.kv_heads = pool->kv_heads;
+  a.num_q_heads = num_q_heads;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.batch = batch;
+  a.cu_q_rows = cu_q_rows;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.max_pages = max_pages_per_seq;
+  a.window = local ? window : 0x7fffffff;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.unit_base = reinterpret_cast<int32_t*>(ws + w.unit_base);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.status = dev_status;
+  a.tree_mask = tree_mask;
+  a.tree_pos = pos;
+  a.max_q_rows = max_q_rows;
+  a.part_rows = w.part_rows;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(local ? launch_local_tree(pool->dtype, num_q_heads / pool->kv_heads, a, st)
+                           : launch_global_tree(pool->layout, a, st),
+                     fn);
+}
+
+gw_status gw_tree_attn_local(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
+                             const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                             int32_t max_pages_per_seq, const uint64_t* tree_mask, const int32_t* pos,
+                             int32_t max_q_rows, int32_t window, float scale, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
+  return tree_attn("gw_tree_attn_local", true, pool, q, out, num_q_heads, batch, cu_q_rows, seq_lens, block_table,
+                   max_pages_per_seq, tree_mask, pos, max_q_rows, window, scale, workspace, workspace_bytes,
+                   dev_status, stream);
+}
+
+gw_status gw_tree_attn_global(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
+                              const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,
+                              int32_t max_pages_per_seq, const uint64_t* tree_mask, int32_t max_q_rows, float scale,
+                              void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  return tree_attn("gw_tree_attn_global", false, pool, q, out, num_q_heads, batch, cu_q_rows, seq_lens, block_table,
+                   max_pages_per_seq, tree_mask, nullptr, max_q_rows, 0, scale, workspace, workspace_bytes, dev_status,
+                   stream);
+}
+
+gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                              const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                              int64_t v_row_stride, int64_t v_head_stride, int32_t num_rows, int32_t num_q_heads,
+                              const float* q_weight, const float* k_weight, float eps, int32_t v_norm,
+                              const int32_t* slot, const int32_t* pos, const float* rope_cs, int32_t max_pos,
+                              void* q_out, int32_t* dev_status, void* stream) {
+  const char* fn = "gw_norm_rope_append";
+  g_err[0] = 0;
+  gw_status s = check_pool(pool, fn);
+  if (s != GW_OK) return s;
+  if (num_rows < 0) return fail(GW_ERR_INVALID_ARG, fn, "num_rows < 0");
+  if (num_q_heads < 1 || num_q_heads > 1024)
+    return fail(GW_ERR_INVALID_ARG, fn, "num_q_heads (%d) outside [1, 1024]", num_q_heads);
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(GW_ERR_INVALID_ARG, fn, "eps must be finite and > 0");
+  if (max_pos < 1) return fail(GW_ERR_INVALID_ARG, fn, "max_pos must be >= 1");
+  if (num_rows == 0) return GW_OK;
+  if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
+    return fail(GW_ERR_INVALID_ARG, fn, "q/k/v/q_out NULL or not 16-byte aligned");
+  for (int64_t d : {q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride})
+    if (d < 0 || d > kMaxRowStride || d % 8)
+      return fail(GW_ERR_INVALID_ARG, fn, "a stride (%lld) is negative, above 2^40 or not a multiple of 8 elements",
+                  static_cast<long long>(d));
+  if (!q_weight || !k_weight || !aligned(q_weight, 16) || !aligned(k_weight, 16))
+    return fail(GW_ERR_INVALID_ARG, fn, "q_weight/k_weight NULL or not 16-byte aligned");
+  if (!slot || !pos || !aligned(slot, 4) || !aligned(pos, 4)) return fail(GW_ERR_INVALID_ARG, fn, "slot/pos NULL or misaligned");
+  if (!rope_cs || !aligned(rope_cs, 16)) return fail(GW_ERR_INVALID_ARG, fn, "rope_cs NULL or not 16-byte aligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  const bool same_kv = k == v && (num_rows == 1 || k_row_stride == v_row_stride);  // a global pool has one KV head
+  const bool folded = pool->layout == GW_LAYOUT_GLOBAL_FOLDED || pool->layout == GW_LAYOUT_GLOBAL_FOLDED_E4M3;
+  if (folded && (!same_kv || !v_norm))
+    return fail(GW_ERR_INVALID_ARG, fn, "a folded pool's K and V are one projection: v must be k, with v_norm");
+  using wide = unsigned __int128;
+  const wide dim = pool->head_dim, rows1 = num_rows - 1, q0 = reinterpret_cast<uintptr_t>(q_out);
+  const wide out_end = q0 + (wide(num_rows) * num_q_heads * dim) * 2;
+  auto overlaps = [&](const void* x, int64_t row, int64_t head, int heads) {
+    const wide x0 = reinterpret_cast<uintptr_t>(x);
+    return x0 < out_end && q0 < x0 + (rows1 * row + wide(heads - 1) * head + dim) * 2;
+  };
+  if (q == q_out) {
+    if ((num_q_heads > 1 && wide(q_head_stride) != dim) || (num_rows > 1 && wide(q_row_stride) != num_q_heads * dim))
+      return fail(GW_ERR_INVALID_ARG, fn, "in place, q must be contiguous");
+  } else if (overlaps(q, q_row_stride, q_head_stride, num_q_heads)) {
+    return fail(GW_ERR_INVALID_ARG, fn, "q_out overlaps q and is not the same rows");
+  }
+  if (overlaps(k, k_row_stride, k_head_stride, pool->kv_heads) || overlaps(v, v_row_stride, v_head_stride, pool->kv_heads))
+    return fail(GW_ERR_INVALID_ARG, fn, "q_out overlaps k or v");
+  NormRopeArgs a{};
+  a.pool = static_cast<uint8_t*>(pool->base);
+  a.num_pages = pool->num_pages;
+  a.kv_heads = pool->kv_heads;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.k_row = k_row_stride;
+  a.k_head = k_head_stride;
+  a.v_row = v_row_stride;
+  a.v_head = v_head_stride;
+  a.num_rows = num_rows;
+  a.num_q_heads = num_q_heads;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.v_norm = v_norm != 0;
+  a.tied = pool->layout != GW_LAYOUT_LOCAL && same_kv;
+  a.slot = slot;
+  a.pos = pos;
+  a.rope_cs = rope_cs;
+  a.max_pos = max_pos;
+  a.out = static_cast<uint16_t*>(q_out);
+  a.status = dev_status;
+  a.early_inputs = g_early_inputs ? 1 : 0;
+  return cuda_status(launch_norm_rope(pool->layout, pool->dtype, a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+gw_status gw_tree_accept(int32_t batch, const int32_t* cu_q_rows, const int32_t* seq_lens, int32_t max_q_rows,
+                         const int32_t* parent, const int32_t* draft, const int32_t* target, int32_t* path,
+                         int64_t path_stride, int32_t* path_lens, int32_t* next_tokens, int32_t* new_lens,
+                         int32_t* dev_status, void* stream) {
+  const char* fn = "gw_tree_accept";
+  g_err[0] = 0;
+  if (batch < 0 || batch > 65535) return fail(GW_ERR_INVALID_ARG, fn, "batch (%d) outside [0, 65535]", batch);
+  if (max_q_rows < 1 || max_q_rows > kMaxTreeRows)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_q_rows (%d) outside [1, %d]", max_q_rows, kMaxTreeRows);
+  if (path_stride < max_q_rows || path_stride > kMaxRowStride)
+    return fail(GW_ERR_INVALID_ARG, fn, "path_stride below max_q_rows or above 2^40");
+  if (batch == 0) return GW_OK;
+  const void* in[] = {cu_q_rows, seq_lens, parent, draft, target, path, path_lens};
+  for (const void* p : in)
+    if (!p || !aligned(p, 4))
+      return fail(GW_ERR_INVALID_ARG, fn, "cu_q_rows/seq_lens/parent/draft/target/path/path_lens NULL or misaligned");
+  if (!aligned(next_tokens, 4) || !aligned(new_lens, 4)) return fail(GW_ERR_INVALID_ARG, fn, "next_tokens/new_lens misaligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  if (seq_lens == path_lens) return fail(GW_ERR_INVALID_ARG, fn, "seq_lens and path_lens are the same array");
+  TreeAcceptArgs a{};
+  a.batch = batch;
+  a.max_q_rows = max_q_rows;
+  a.cu_q_rows = cu_q_rows;
+  a.seq_lens = seq_lens;
+  a.parent = parent;
+  a.draft = draft;
+  a.target = target;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.path_lens = path_lens;
+  a.next_tokens = next_tokens;
+  a.new_lens = new_lens;
+  a.status = dev_status;
+  return cuda_status(launch_tree_accept(a, static_cast<cudaStream_t>(stream)), fn);
+}
+
+gw_status gw_kv_tree_move(const gw_kv_pool* pools, int32_t n_pools, int32_t batch, const int32_t* cu_q_rows,
+                          const int32_t* seq_lens, const int32_t* block_table, int32_t max_pages_per_seq,
+                          const int32_t* path, int64_t path_stride, const int32_t* path_lens, int32_t* dev_status,
+                          void* stream) {
+  const char* fn = "gw_kv_tree_move";
+  g_err[0] = 0;
+  if (!pools) return fail(GW_ERR_INVALID_ARG, fn, "pools is NULL");
+  if (n_pools < 1 || n_pools > kMaxTreePools)
+    return fail(GW_ERR_INVALID_ARG, fn, "n_pools (%d) outside [1, %d]", n_pools, kMaxTreePools);
+  TreeMoveArgs a{};
+  for (int i = 0; i < n_pools; ++i) {
+    const gw_status s = check_pool(pools + i, fn);
+    if (s != GW_OK) return s;
+    if (pools[i].layout != pools[0].layout || pools[i].dtype != pools[0].dtype || pools[i].kv_heads != pools[0].kv_heads)
+      return fail(GW_ERR_INVALID_ARG, fn, "pool %d differs from the first in layout, dtype or kv_heads", i);
+    a.pools[i] = static_cast<uint8_t*>(pools[i].base);
+    a.num_pages[i] = pools[i].num_pages;
+    for (int j = 0; j < i; ++j)
+      if (a.pools[j] == a.pools[i]) return fail(GW_ERR_INVALID_ARG, fn, "pools %d and %d are the same memory", j, i);
+  }
+  if (batch < 0 || batch > 65535) return fail(GW_ERR_INVALID_ARG, fn, "batch (%d) outside [0, 65535]", batch);
+  if (max_pages_per_seq < 1 || max_pages_per_seq > 0x7fffffff / 16)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be in [1, 2^27)");
+  if (path_stride < 1 || path_stride > kMaxRowStride) return fail(GW_ERR_INVALID_ARG, fn, "path_stride < 1 or above 2^40");
+  if (batch == 0) return GW_OK;
+  const void* in[] = {cu_q_rows, seq_lens, block_table, path, path_lens};
+  for (const void* p : in)
+    if (!p || !aligned(p, 4))
+      return fail(GW_ERR_INVALID_ARG, fn, "cu_q_rows/seq_lens/block_table/path/path_lens NULL or misaligned");
+  if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
+  a.page_bytes = static_cast<int64_t>(page_bytes(pools));
+  a.pieces = static_cast<int32_t>(a.page_bytes / (16 * kPageTokens));
+  a.batch = batch;
+  a.cu_q_rows = cu_q_rows;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.max_pages = max_pages_per_seq;
+  a.path = path;
+  a.path_stride = path_stride;
+  a.path_lens = path_lens;
+  a.status = dev_status;
+  return cuda_status(launch_tree_move(pools->layout, pools->dtype, n_pools, a, static_cast<cudaStream_t>(stream)), fn);
 }
 
 gw_status gw_merge_lse(int32_t n_parts, const void* const* o_parts, const float* const* lse_parts, void* out,

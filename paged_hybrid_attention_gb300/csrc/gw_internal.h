@@ -58,6 +58,56 @@ __host__ __device__ __forceinline__ int global_chunks(int L) {
   return ((L + 15) / 16 + cpg - 1) / cpg;
 }
 
+// ---- drafted trees (gw_tree_attn_*) ------------------------------------------
+// A work unit is (sequence, KV head or half of the output dims, block of
+// 128 rows, chunk of key tiles); a tile is 64 tokens, aligned to 64.  Chunks
+// depend on the sequence's own length, rows and window only, as the decode's.
+constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask word
+constexpr int kMaxTreeBatch = 512;  // sequences of a call: their plan is in shared memory
+constexpr int kTreeTile = 64;
+constexpr int kTreeMaxChunks = 64;
+
+// Chunks of `tiles` tiles, `min_tiles` each or that doubled until there are at
+// most kTreeMaxChunks / blocks of them (`blocks` row blocks share the GPU).
+__host__ __device__ __forceinline__ int tree_chunk_tiles(int tiles, int min_tiles, int blocks) {
+  const int most = blocks < kTreeMaxChunks ? kTreeMaxChunks / blocks : 1;
+  int ct = min_tiles;
+  while ((tiles - 1) / ct + 1 > most) ct *= 2;
+  return ct;
+}
+
+struct TreeSpan {
+  int first;   // first tile
+  int tiles;   // tiles [first, first + tiles)
+  int blocks;  // blocks of 128 rows
+  int ct;      // tiles of a chunk
+  __host__ __device__ int chunks() const { return (tiles - 1) / ct + 1; }
+};
+
+// Of n rows over L >= n >= 1 tokens: `group` heads share a tile's rows.  Rows
+// sit at tokens L - n and later, so the first key of any is L - n - window + 1.
+__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int group, int min_tiles) {
+  TreeSpan s;
+  const int lo = L - n - window + 1;
+  s.first = lo > 0 ? lo / kTreeTile : 0;
+  s.tiles = (L - 1) / kTreeTile - s.first + 1;
+  const int per = 128 / group;
+  s.blocks = (n + per - 1) / per;
+  s.ct = tree_chunk_tiles(s.tiles, min_tiles, s.blocks);
+  return s;
+}
+// A bound on a sequence's chunks over L <= 16 * max_pages and n <= max_rows.
+__host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_rows, int window, int min_tiles) {
+  // tokens in sight: all, or window - 1 cached ones and the drafts, in tiles they need not begin
+  const int64_t all = (static_cast<int64_t>(max_pages) * 16 + kTreeTile - 1) / kTreeTile;
+  const int64_t seen = (static_cast<int64_t>(window) + max_rows + kTreeTile - 3) / kTreeTile + 1;
+  const int64_t c = ((all < seen ? all : seen) + min_tiles - 1) / min_tiles;
+  return static_cast<int>(c < kTreeMaxChunks ? c : kTreeMaxChunks);
+}
+// Smallest chunks, in tiles (attn_prompt_tc.cu, attn_tree_global.cu).
+constexpr int kTreeLocalTiles = 4;
+constexpr int kTreeGlobalTiles = 8;
+
 // Workspace layout (offsets from the 256-byte aligned workspace base):
 //   [0, 256)          reserved
 //   [256, ub_end)     int32 unit_base[batch + 1], rounded up to 256 bytes
@@ -106,6 +156,11 @@ struct LocalArgs {
   float* acc;      // [batch][acc_stride]
   int64_t acc_stride;
   float decay;
+  // Drafted trees (gw_tree_attn_*); tree_mask null: none.
+  const uint64_t* tree_mask;  // [total_rows]: visible drafts of each row
+  const int32_t* tree_pos;    // [total_rows], local only
+  int32_t max_q_rows;         // bound on a sequence's rows
+  int32_t part_rows;          // rows of a unit's partials
 };
 
 struct AppendArgs {
@@ -222,6 +277,72 @@ struct CompactArgs {
   int32_t* status;
 };
 cudaError_t launch_evict_compact(int layout, const CompactArgs& a, cudaStream_t st);
+// gw_norm_rope_append: strides in elements; `tied`: v is k's projection (one
+// global KV head); `run`: heads per warp, set by the launch.
+struct NormRopeArgs {
+  uint8_t* pool;
+  int64_t num_pages;
+  int32_t kv_heads;
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  int32_t num_rows, num_q_heads;
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+  int32_t v_norm, tied, run;
+  const int32_t* slot;
+  const int32_t* pos;
+  const float* rope_cs;
+  int32_t max_pos;
+  uint16_t* out;
+  int32_t* status;
+  int32_t early_inputs;  // gw_set_early_inputs: slot, pos and RoPE rows read before the wait
+};
+cudaError_t launch_norm_rope(int layout, int dtype, const NormRopeArgs& a, cudaStream_t st);
+
+constexpr int kMaxTreePools = 64;  // pools of a gw_kv_tree_move call
+// gw_tree_accept
+struct TreeAcceptArgs {
+  int32_t batch;
+  int32_t max_q_rows;
+  const int32_t* cu_q_rows;
+  const int32_t* seq_lens;
+  const int32_t* parent;
+  const int32_t* draft;
+  const int32_t* target;
+  int32_t* path;
+  int64_t path_stride;
+  int32_t* path_lens;
+  int32_t* next_tokens;  // or null
+  int32_t* new_lens;     // or null
+  int32_t* status;
+};
+// gw_tree_attn_*: the attention kernel, then the merge of the chunks of the
+// sequences that have several
+cudaError_t launch_local_tree(int dtype, int group, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_global_tree(int layout, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_local_tree_tc(int dtype, int group, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_global_tree_tc(int layout, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st);
+// gw_kv_tree_move
+struct TreeMoveArgs {
+  uint8_t* pools[kMaxTreePools];
+  int64_t num_pages[kMaxTreePools];
+  int64_t page_bytes;
+  int32_t pieces;  // 16-byte pieces of a token
+  int32_t batch;
+  const int32_t* cu_q_rows;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  int32_t max_pages;
+  const int32_t* path;
+  int64_t path_stride;
+  const int32_t* path_lens;
+  int32_t* status;
+};
+cudaError_t launch_tree_move(int layout, int dtype, int n_pools, const TreeMoveArgs& a, cudaStream_t st);
 cudaError_t launch_bw_probe(const void* buf, int64_t chunks, int32_t* status, cudaStream_t st);
 cudaError_t launch_bw_probe_tma(const void* buf, int64_t pages, int32_t* status, cudaStream_t st);
 cudaError_t launch_wait_selftest(int32_t* status, int32_t* result, int64_t limit_ns, cudaStream_t st);

@@ -14,31 +14,17 @@ __device__ __forceinline__ bool plan_len_ok(const LocalArgs& a, int L) {
   return L >= 1 && static_cast<int64_t>(L) <= static_cast<int64_t>(a.max_pages) * kPage;
 }
 
-// ub[s] = units of the decode-row sequences before s (ub[batch] = total),
-// with units_of(L) the units of one decode row of length L.  Rows of invalid
-// length (L < 1 or beyond the block table) get no units.  Must be called by
-// every thread of the block; scratch holds 32 ints.  With `publish`, CTA 0
-// also stores the plan to the workspace for the combine kernel and raises
-// GW_DEV_LEN_RANGE for invalid rows; without it (a plan made before the wait
-// on the previous kernel) nothing is written to global memory, and
-// publish_plan does both once the wait is over.
-template <class UnitsOf>
-__device__ void plan_in_smem(const LocalArgs& a, int32_t* ub, int32_t* scratch, UnitsOf units_of,
-                             bool publish = true) {
+// ub[s] = units of the sequences before s (ub[batch] = total), with count(s)
+// the units of sequence s.  Must be called by every thread of the block;
+// scratch holds 32 ints.
+template <class CountOf>
+__device__ __forceinline__ void plan_scan(int batch, int32_t* ub, int32_t* scratch, CountOf count) {
   const int nt = blockDim.x, t = threadIdx.x;
-  const int per = (a.batch + nt - 1) / nt;
-  const int s0 = min(a.batch, t * per), s1 = min(a.batch, s0 + per);
+  const int per = (batch + nt - 1) / nt;
+  const int s0 = min(batch, t * per), s1 = min(batch, s0 + per);
   int mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const int n = a.cu_q_rows[s + 1] - a.cu_q_rows[s];
-    const int L = a.seq_lens[s];
-    int units = 0;
-    if (n == 1) {
-      if (plan_len_ok(a, L))
-        units = units_of(L);
-      else if (blockIdx.x == 0 && publish)
-        set_status(a.status, GW_DEV_LEN_RANGE);
-    }
+    const int units = count(s);
     ub[s] = units;  // per-sequence count for now
     mine += units;
   }
@@ -68,10 +54,102 @@ __device__ void plan_in_smem(const LocalArgs& a, int32_t* ub, int32_t* scratch, 
     ub[s] = run;
     run += c;
   }
-  if (t == nt - 1) ub[a.batch] = run;
+  if (t == nt - 1) ub[batch] = run;
   __syncthreads();
+}
+
+// The plan of a decode call: plan_scan over the decode-row sequences, with
+// units_of(L) the units of one decode row of length L.  Rows of invalid length
+// (L < 1 or beyond the block table) get no units.  With `publish`, CTA 0
+// also stores the plan to the workspace for the combine kernel and raises
+// GW_DEV_LEN_RANGE for invalid rows; without it (a plan made before the wait
+// on the previous kernel) nothing is written to global memory, and
+// publish_plan does both once the wait is over.
+template <class UnitsOf>
+__device__ void plan_in_smem(const LocalArgs& a, int32_t* ub, int32_t* scratch, UnitsOf units_of,
+                             bool publish = true) {
+  plan_scan(a.batch, ub, scratch, [&](int s) {
+    const int n = a.cu_q_rows[s + 1] - a.cu_q_rows[s];
+    const int L = a.seq_lens[s];
+    if (n != 1) return 0;
+    if (plan_len_ok(a, L)) return units_of(L);
+    if (blockIdx.x == 0 && publish) set_status(a.status, GW_DEV_LEN_RANGE);
+    return 0;
+  });
   if (blockIdx.x == 0 && publish)
-    for (int s = t; s <= a.batch; s += nt) a.unit_base[s] = ub[s];
+    for (int s = threadIdx.x; s <= a.batch; s += blockDim.x) a.unit_base[s] = ub[s];
+}
+
+// The plan of a gw_tree_attn_* call: a sequence's units are `copies` (KV heads,
+// or halves of the output dims) x row blocks x chunks.  Sequences without rows
+// have none; nor have those with more rows than max_q_rows, a length below
+// their rows or beyond the block table (GW_DEV_LEN_RANGE), whose output rows
+// become zeros here.  CTA 0 stores the plan for the merge.
+__device__ __forceinline__ void plan_tree(const LocalArgs& a, int32_t* ub, int32_t* scratch, int copies, int group,
+                                          int min_tiles, int head_dim) {
+  auto rows_of = [&](int s) { return a.cu_q_rows[s + 1] - a.cu_q_rows[s]; };
+  auto valid = [&](int s) {
+    const int n = rows_of(s), L = a.seq_lens[s];
+    return n >= 1 && n <= a.max_q_rows && L >= n && plan_len_ok(a, L);
+  };
+  plan_scan(a.batch, ub, scratch, [&](int s) {
+    if (!valid(s)) return 0;
+    const TreeSpan sp = tree_span(a.seq_lens[s], rows_of(s), a.window, group, min_tiles);
+    return copies * sp.blocks * sp.chunks();
+  });
+  for (int s = blockIdx.x; s < a.batch; s += gridDim.x) {
+    if (ub[s + 1] != ub[s]) continue;
+    const int n = rows_of(s);
+    if (n == 0) continue;
+    if (threadIdx.x == 0) set_status(a.status, GW_DEV_LEN_RANGE);
+    uint4* row = reinterpret_cast<uint4*>(a.out + static_cast<int64_t>(a.cu_q_rows[s]) * a.num_q_heads * head_dim);
+    const int64_t pieces = static_cast<int64_t>(n) * a.num_q_heads * head_dim / 8;
+    for (int64_t i = threadIdx.x; i < pieces; i += blockDim.x) row[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s <= a.batch; s += blockDim.x) a.unit_base[s] = ub[s];
+}
+
+// The keys of a tree's row: cached tokens [kmin, base) and the drafts of
+// `drafts`, bit i of which is token base + i.
+struct TreeRow {
+  int kmin;
+  uint64_t drafts;
+};
+
+// Row r of sequence s (n rows at tokens [base, base + n), first row row0); one
+// at a position before the drafts' first sees nothing (GW_DEV_POS_RANGE).
+// `windowed`: tokens at positions up to pos - window are not seen, drafts by
+// their own positions.
+__device__ __forceinline__ TreeRow tree_row(const LocalArgs& a, int row0, int r, int n, int base, bool windowed) {
+  TreeRow t;
+  t.kmin = 0;
+  t.drafts = a.tree_mask[row0 + r] & (n < 64 ? (1ull << n) - 1 : ~0ull);
+  if (windowed) {
+    const int pos = a.tree_pos[row0 + r];
+    if (pos < base) {
+      set_status(a.status, GW_DEV_POS_RANGE);
+      t.kmin = 0x7fffffff;
+      t.drafts = 0;
+      return t;
+    }
+    t.kmin = max(0, pos - a.window + 1);
+    if (t.kmin > base)  // else no draft is as far back
+      for (int i = 0; i < n; ++i)
+        if (a.tree_pos[row0 + i] < t.kmin) t.drafts &= ~(1ull << i);
+  }
+  return t;
+}
+
+// The keys of tile [key0, key0 + 64) that the row sees, a bit each.
+__device__ __forceinline__ uint64_t tree_tile_mask(const TreeRow& t, int base, int key0) {
+  const int lo = t.kmin - key0, hi = min(64, base - key0);  // cached: bits [lo, hi)
+  uint64_t m = 0;
+  if (hi > 0 && lo < hi) m = (hi < 64 ? (1ull << hi) - 1 : ~0ull) & (lo > 0 ? ~0ull << lo : ~0ull);
+  const int d = base - key0;  // the first draft's bit
+  if (d >= 0 && d < 64) m |= t.drafts << d;
+  if (d < 0 && d > -64) m |= t.drafts >> -d;
+  return m;
 }
 
 // The global half of a plan made with publish = false, once the previous

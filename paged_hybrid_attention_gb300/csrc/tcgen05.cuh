@@ -45,6 +45,36 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N, bool a_mn_m
   return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 10);
 }
 
+// e5m2 A and e4m3 B.
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return idesc_e4m3(M, N, a_mn_major, b_mn_major) | (1u << 7);
+}
+
+// Four softmax weights in three e5m2 terms each, w[term] holding their bytes: an
+// e5m2 number is the upper byte of an fp16 one, so the weights, rounded to fp16,
+// are cut by masks and exact differences into terms of three bits, 2^-9 of a
+// weight in all.  Weights of up to 2^15 are in range, down to 2^-16, where two
+// e4m3 terms would end at 2^-10 and lose a long tail.  Returns the sum of the
+// weights as the terms hold them.
+__device__ __forceinline__ float split_e5m2(float p0, float p1, float p2, float p3, uint32_t (&w)[3]) {
+  __half2 x[2] = {__floats2half2_rn(p0, p1), __floats2half2_rn(p2, p3)};
+  __half2 used[2];
+#pragma unroll
+  for (int term = 0; term < 3; ++term) {
+    uint32_t a0 = *reinterpret_cast<uint32_t*>(&x[0]), a1 = *reinterpret_cast<uint32_t*>(&x[1]);
+    w[term] = __byte_perm(a0, a1, 0x7531);
+    a0 &= 0xff00ff00u;
+    a1 &= 0xff00ff00u;
+    const __half2 t0 = *reinterpret_cast<__half2*>(&a0), t1 = *reinterpret_cast<__half2*>(&a1);
+    used[0] = term == 0 ? t0 : __hadd2(used[0], t0);
+    used[1] = term == 0 ? t1 : __hadd2(used[1], t1);
+    x[0] = __hsub2(x[0], t0);
+    x[1] = __hsub2(x[1], t1);
+  }
+  const float2 u0 = __half22float2(used[0]), u1 = __half22float2(used[1]);
+  return (u0.x + u0.y) + (u1.x + u1.y);
+}
+
 __device__ __forceinline__ void alloc(uint32_t* smem_dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_dst)),
                "r"(ncols)

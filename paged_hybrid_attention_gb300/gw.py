@@ -23,6 +23,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 GW_OK, GW_ERR_INVALID_ARG, GW_ERR_UNSUPPORTED, GW_ERR_WORKSPACE, GW_ERR_CUDA = 0, 1, 2, 3, 4
 GW_DEV_SLOT_RANGE, GW_DEV_POS_RANGE, GW_DEV_PAGE_RANGE, GW_DEV_LEN_RANGE = 1, 2, 4, 8
 GW_DEV_TIMEOUT, GW_DEV_WORKSPACE, GW_DEV_KEEP_RANGE = 16, 32, 64
+GW_DEV_TREE_RANGE = 128
 KV_BF16, KV_E4M3 = 0, 1
 LAYOUT_LOCAL, LAYOUT_GLOBAL_FOLDED, LAYOUT_GLOBAL_FULL, LAYOUT_GLOBAL_FOLDED_E4M3 = 0, 1, 2, 3
 LAYOUTS = {"local": LAYOUT_LOCAL, "folded": LAYOUT_GLOBAL_FOLDED, "full": LAYOUT_GLOBAL_FULL,
@@ -34,7 +35,9 @@ EXPORTS = ["gw_pool_page_bytes", "gw_kv_append", "gw_decode_attn_local", "gw_dec
            "gw_set_early_inputs", "gw_rope_cs", "gw_wait_selftest", "gw_bw_probe_tma",
            "gw_decode_attn_global_lse", "gw_merge_lse", "gw_append_decode_attn_local",
            "gw_append_decode_attn_global", "gw_rope_rows", "gw_rope_cs_scaled",
-           "gw_decode_attn_global_acc", "gw_attn_acc_workspace_bytes", "gw_kv_evict_select", "gw_kv_evict_compact"]
+           "gw_decode_attn_global_acc", "gw_attn_acc_workspace_bytes", "gw_kv_evict_select", "gw_kv_evict_compact",
+           "gw_norm_rope_append", "gw_tree_attn_local", "gw_tree_attn_global", "gw_tree_workspace_bytes",
+           "gw_tree_accept", "gw_kv_tree_move"]
 
 
 ELEMS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
@@ -90,6 +93,20 @@ _lib.gw_kv_evict_select.argtypes = [_vp, _i64, _i32, _vp, _i32, _i32, _i32, _vp,
 _lib.gw_kv_evict_select.restype = _i32
 _lib.gw_kv_evict_compact.argtypes = [_P, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _vp]
 _lib.gw_kv_evict_compact.restype = _i32
+_lib.gw_norm_rope_append.argtypes = [_P, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _f32,
+                                     _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp]
+_lib.gw_norm_rope_append.restype = _i32
+_lib.gw_tree_attn_local.argtypes = [_P, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _f32, _vp, _sz,
+                                    _vp, _vp]
+_lib.gw_tree_attn_local.restype = _i32
+_lib.gw_tree_attn_global.argtypes = [_P, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _f32, _vp, _sz, _vp, _vp]
+_lib.gw_tree_attn_global.restype = _i32
+_lib.gw_tree_workspace_bytes.argtypes = [_P, _i32, _i32, _i32, _i32, _i32]
+_lib.gw_tree_workspace_bytes.restype = _sz
+_lib.gw_tree_accept.argtypes = [_i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
+_lib.gw_tree_accept.restype = _i32
+_lib.gw_kv_tree_move.argtypes = [_P, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp]
+_lib.gw_kv_tree_move.restype = _i32
 _lib.gw_merge_lse.argtypes = [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
 _lib.gw_merge_lse.restype = _i32
 _lib.gw_rope_cs.argtypes = [_vp, ctypes.c_double, _i32, _i32, _i32, _vp]
@@ -477,6 +494,160 @@ def kv_evict_compact(pool, block_table, seq_lens, keep_idx, keep_lens, acc=None,
     _check(_lib.gw_kv_evict_compact(pool.desc, batch, block_table.data_ptr(), pages, seq_lens.data_ptr(),
                                     keep_idx.data_ptr(), keep_stride, keep_lens.data_ptr(), _addr(dst_block_table),
                                     dst_pages, _addr(acc), acc_stride, _addr(dev_status), handle))
+
+
+def norm_rope_append(pool, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out, eps=1e-6, v_norm=True,
+                     dev_status=None, stream=None):
+    """gw_norm_rope_append: the norms of q, k and v heads, the rotation of q and
+    k, k and v written to the pool at `slot`, q into `out` [rows, heads, dim]
+    (q itself if it is contiguous).  q, k, v are bf16 [rows, heads, dim] of any
+    strides that keep heads at 16-byte boundaries; on a folded pool v is k."""
+    fn = "gw_norm_rope_append"
+    if (q is None or k is None or v is None or q_weight is None or k_weight is None or slot is None or pos is None or
+            rope_cs is None or out is None):
+        _missing(fn, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, slot=slot, pos=pos, rope_cs=rope_cs, out=out)
+    handle = _on_device(fn, stream, pool.data, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out, dev_status)
+    dim, rot = pool.desc.head_dim, pool.desc.rot_dim
+    rows = slot.numel()
+    for name, t, heads in (("q", q, None), ("k", k, pool.kv_heads), ("v", v, pool.kv_heads)):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or (
+                heads is not None and t.shape[1] != heads):
+            _invalid(fn, "%s must be bfloat16 [%d, %s, %d] (got %s %s)" %
+                     (name, rows, "heads" if heads is None else heads, dim, t.dtype, list(t.shape)))
+        if t.stride(2) != 1:
+            _invalid(fn, "the last dimension of %s must have stride 1" % name)
+    hq = q.shape[1]
+    _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
+    _dense(fn, "q_weight", q_weight, torch.float32, dim)
+    _dense(fn, "k_weight", k_weight, torch.float32, dim)
+    _vector(fn, "slot", slot, rows)
+    _vector(fn, "pos", pos, rows)
+    max_pos = rope_cs.shape[0]
+    _dense(fn, "rope_cs", rope_cs, torch.float32, max_pos, rot // 2, 2)
+    qr, qh, _ = q.stride()
+    kr, kh, _ = k.stride()
+    vr, vh, _ = v.stride()
+    _check(_lib.gw_norm_rope_append(pool.desc, q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, v.data_ptr(), vr, vh, rows,
+                                    hq, q_weight.data_ptr(), k_weight.data_ptr(), float(eps), 1 if v_norm else 0,
+                                    slot.data_ptr(), pos.data_ptr(), rope_cs.data_ptr(), max_pos, out.data_ptr(),
+                                    _addr(dev_status), handle))
+
+
+def alloc_workspace_tree(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows=64, window=1024, device="cuda"):
+    """The workspace of tree_attn_local / _global calls of at most this size."""
+    n = _lib.gw_tree_workspace_bytes(pool.desc, num_q_heads, batch, max_pages_per_seq, max_q_rows, window)
+    if n == 0:
+        raise GwError(GW_ERR_INVALID_ARG, last_error() or "invalid workspace request")
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def _tree_args(fn, dim, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, pos, workspace, dev_status, stream):
+    """The checks that the tree attention calls share: (stream, rows' heads, batch, pages)."""
+    if (q is None or out is None or cu_q_rows is None or seq_lens is None or block_table is None or
+            tree_mask is None or workspace is None):
+        _missing(fn, q=q, out=out, cu_q_rows=cu_q_rows, seq_lens=seq_lens, block_table=block_table,
+                 tree_mask=tree_mask, workspace=workspace)
+    handle = _on_device(fn, stream, pool.data, q, out, cu_q_rows, seq_lens, block_table, tree_mask, pos, workspace,
+                        dev_status)
+    batch = seq_lens.numel()
+    if q.dim() != 3:
+        _invalid(fn, "q must be [rows, heads, %d] (got %s)" % (dim, list(q.shape)))
+    rows, hq = q.shape[0], q.shape[1]
+    _dense(fn, "q", q, torch.bfloat16, rows, hq, dim)
+    _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
+    _dense(fn, "tree_mask", tree_mask, torch.int64, rows)
+    _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
+    _vector(fn, "seq_lens", seq_lens, batch)
+    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    if not workspace.is_contiguous():
+        _invalid(fn, "workspace must be contiguous")
+    return handle, rows, hq, batch, block_table.shape[1]
+
+
+def tree_attn_local(pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, pos, workspace, window, scale=None,
+                    max_q_rows=64, dev_status=None, stream=None):
+    """gw_tree_attn_local: the last rows of each sequence, a tree of drafts, over
+    its window: tree_mask int64 [rows] holds each row's visible drafts as bits,
+    pos int32 [rows] the rows' positions."""
+    fn = "gw_tree_attn_local"
+    if pos is None:
+        _missing(fn, pos=pos)
+    handle, rows, hq, batch, pages = _tree_args(fn, 256, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask,
+                                                pos, workspace, dev_status, stream)
+    _vector(fn, "pos", pos, rows)
+    scale = 1.0 / math.sqrt(256) if scale is None else scale
+    _check(_lib.gw_tree_attn_local(pool.desc, q.data_ptr(), out.data_ptr(), hq, batch, cu_q_rows.data_ptr(),
+                                   seq_lens.data_ptr(), block_table.data_ptr(), pages, tree_mask.data_ptr(),
+                                   pos.data_ptr(), int(max_q_rows), int(window), float(scale), workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _addr(dev_status), handle))
+
+
+def tree_attn_global(pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, workspace, scale=None, max_q_rows=64,
+                     dev_status=None, stream=None):
+    """gw_tree_attn_global: tree_attn_local over a global pool, without a window."""
+    fn = "gw_tree_attn_global"
+    handle, _, hq, batch, pages = _tree_args(fn, 512, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, None,
+                                             workspace, dev_status, stream)
+    scale = 1.0 / math.sqrt(512) if scale is None else scale
+    _check(_lib.gw_tree_attn_global(pool.desc, q.data_ptr(), out.data_ptr(), hq, batch, cu_q_rows.data_ptr(),
+                                    seq_lens.data_ptr(), block_table.data_ptr(), pages, tree_mask.data_ptr(),
+                                    int(max_q_rows), float(scale), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), _addr(dev_status), handle))
+
+
+def tree_accept(cu_q_rows, seq_lens, parent, draft, target, path, path_lens, next_tokens=None, new_lens=None,
+                max_q_rows=None, dev_status=None, stream=None):
+    """gw_tree_accept: into path int32 [batch, >= max_q_rows] and path_lens the
+    rows of each tree whose drafts the target chose, from the root on; the
+    target's token after the last into next_tokens, the lengths with the path
+    alone into new_lens.  max_q_rows: path's columns if None (at most 64)."""
+    fn = "gw_tree_accept"
+    if (cu_q_rows is None or seq_lens is None or parent is None or draft is None or target is None or path is None or
+            path_lens is None):
+        _missing(fn, cu_q_rows=cu_q_rows, seq_lens=seq_lens, parent=parent, draft=draft, target=target, path=path,
+                 path_lens=path_lens)
+    handle = _on_device(fn, stream, cu_q_rows, seq_lens, parent, draft, target, path, path_lens, next_tokens, new_lens,
+                        dev_status)
+    batch, rows = seq_lens.numel(), parent.numel()
+    _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
+    _vector(fn, "seq_lens", seq_lens, batch)
+    _vector(fn, "parent", parent, rows)
+    _vector(fn, "draft", draft, rows)
+    _vector(fn, "target", target, rows)
+    _vector(fn, "path_lens", path_lens, batch)
+    if next_tokens is not None:
+        _vector(fn, "next_tokens", next_tokens, batch)
+    if new_lens is not None:
+        _vector(fn, "new_lens", new_lens, batch)
+    stride = _row_stride(fn, "path", path, torch.int32, batch)
+    most = min(path.shape[1], 64) if max_q_rows is None else int(max_q_rows)
+    if path.shape[1] < most:
+        _invalid(fn, "path has %d columns, max_q_rows is %d" % (path.shape[1], most))
+    _check(_lib.gw_tree_accept(batch, cu_q_rows.data_ptr(), seq_lens.data_ptr(), most, parent.data_ptr(),
+                               draft.data_ptr(), target.data_ptr(), path.data_ptr(), stride, path_lens.data_ptr(),
+                               _addr(next_tokens), _addr(new_lens), _addr(dev_status), handle))
+
+
+def kv_tree_move(pools, cu_q_rows, seq_lens, block_table, path, path_lens, dev_status=None, stream=None):
+    """gw_kv_tree_move: the accepted rows of each sequence moved to the front of
+    its drafts, in every pool of `pools` (layers of a kind, at most 64)."""
+    fn = "gw_kv_tree_move"
+    if cu_q_rows is None or seq_lens is None or block_table is None or path is None or path_lens is None:
+        _missing(fn, cu_q_rows=cu_q_rows, seq_lens=seq_lens, block_table=block_table, path=path, path_lens=path_lens)
+    handle = _on_device(fn, stream, cu_q_rows, seq_lens, block_table, path, path_lens, dev_status,
+                        *[p.data for p in pools])
+    batch = seq_lens.numel()
+    _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
+    _vector(fn, "seq_lens", seq_lens, batch)
+    _vector(fn, "path_lens", path_lens, batch)
+    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    stride = _row_stride(fn, "path", path, torch.int32, batch)
+    descs = (PoolDesc * len(pools))(*[p.desc for p in pools])
+    _check(_lib.gw_kv_tree_move(descs, len(pools), batch, cu_q_rows.data_ptr(), seq_lens.data_ptr(),
+                                block_table.data_ptr(), block_table.shape[1], path.data_ptr(), stride,
+                                path_lens.data_ptr(), _addr(dev_status), handle))
 
 
 def merge_lse(outs, lses, out, lse_out=None, stream=None):

@@ -802,6 +802,10 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
   if (num_rows == 0) return GW_OK;
   if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
     return fail(GW_ERR_INVALID_ARG, fn, "q/k/v/q_out NULL or not 16-byte aligned");
+  // the stride of a dimension of one is not used
+  if (num_rows == 1) q_row_stride = k_row_stride = v_row_stride = 0;
+  if (num_q_heads == 1) q_head_stride = 0;
+  if (pool->kv_heads == 1) k_head_stride = v_head_stride = 0;
   for (int64_t d : {q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride})
     if (d < 0 || d > kMaxRowStride || d % 8)
       return fail(GW_ERR_INVALID_ARG, fn, "a stride (%lld) is negative, above 2^40 or not a multiple of 8 elements",
@@ -811,7 +815,7 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
   if (!slot || !pos || !aligned(slot, 4) || !aligned(pos, 4)) return fail(GW_ERR_INVALID_ARG, fn, "slot/pos NULL or misaligned");
   if (!rope_cs || !aligned(rope_cs, 16)) return fail(GW_ERR_INVALID_ARG, fn, "rope_cs NULL or not 16-byte aligned");
   if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
-  const bool same_kv = k == v && (num_rows == 1 || k_row_stride == v_row_stride);  // a global pool has one KV head
+  const bool same_kv = k == v && k_row_stride == v_row_stride;  // a global pool has one KV head
   const bool folded = pool->layout == GW_LAYOUT_GLOBAL_FOLDED || pool->layout == GW_LAYOUT_GLOBAL_FOLDED_E4M3;
   if (folded && (!same_kv || !v_norm))
     return fail(GW_ERR_INVALID_ARG, fn, "a folded pool's K and V are one projection: v must be k, with v_norm");

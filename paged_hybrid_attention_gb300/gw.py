@@ -105,7 +105,7 @@ _lib.gw_tree_workspace_bytes.argtypes = [_P, _i32, _i32, _i32, _i32, _i32]
 _lib.gw_tree_workspace_bytes.restype = _sz
 _lib.gw_tree_accept.argtypes = [_i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
 _lib.gw_tree_accept.restype = _i32
-_lib.gw_kv_tree_move.argtypes = [_P, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp]
+_lib.gw_kv_tree_move.argtypes = [ctypes.c_char_p, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _vp, _vp]
 _lib.gw_kv_tree_move.restype = _i32
 _lib.gw_merge_lse.argtypes = [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp]
 _lib.gw_merge_lse.restype = _i32
@@ -190,9 +190,10 @@ def _on_device(fn, stream, *tensors):
             _invalid(fn, "tensors on %s and %s" % (tensors[0].device, t.device))
     if dev < 0:
         _invalid(fn, "tensors on %s, not on a CUDA device" % tensors[0].device)
-    if dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
+    if dev != torch._C._cuda_getDevice() or (stream is not None and stream.device.index != dev):
         _invalid(fn, "tensors on %s, but the current device or the stream is another" % tensors[0].device)
-    # the raw handle costs 0.1 us, a torch.cuda.Stream object 2.9 us
+    # the raw handle costs 0.1 us, a torch.cuda.Stream object 2.9 us (and the
+    # device's number 0.1 us, torch.cuda.current_device() 0.23 us)
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -212,11 +213,21 @@ def _addr(t):
 
 def _dense(fn, name, t, dtype, *shape):
     """`t` has this dtype and shape (None: any length) and is contiguous."""
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     want = tuple(m if n is None else n for n, m in zip(shape, t.shape)) if None in shape else shape
     if t.dtype != dtype or t.shape != want or len(want) != len(shape):
         _invalid(fn, "%s must be %s of shape %s (got %s %s)" % (name, dtype, list(shape), t.dtype, list(t.shape)))
     if not t.is_contiguous():
         _invalid(fn, "%s must be contiguous" % name)
+
+
+def _table(fn, name, t, rows):
+    """The columns of `t`, int32 [rows, columns], contiguous."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or t.dtype != torch.int32 or not t.is_contiguous():
+        _dense(fn, name, t, torch.int32, rows, None)
+    return shape[1]
 
 
 def _vector(fn, name, t, n):
@@ -509,14 +520,19 @@ def norm_rope_append(pool, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out,
     handle = _on_device(fn, stream, pool.data, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out, dev_status)
     dim, rot = pool.desc.head_dim, pool.desc.rot_dim
     rows = slot.numel()
-    for name, t, heads in (("q", q, None), ("k", k, pool.kv_heads), ("v", v, pool.kv_heads)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[0] != rows or t.shape[2] != dim or (
-                heads is not None and t.shape[1] != heads):
-            _invalid(fn, "%s must be bfloat16 [%d, %s, %d] (got %s %s)" %
-                     (name, rows, "heads" if heads is None else heads, dim, t.dtype, list(t.shape)))
-        if t.stride(2) != 1:
-            _invalid(fn, "the last dimension of %s must have stride 1" % name)
-    hq = q.shape[1]
+    hq = q.shape[1] if q.dim() == 3 else 0
+    bf16, kv = torch.bfloat16, (rows, pool.kv_heads, dim)
+    if (q.shape != (rows, hq, dim) or k.shape != kv or v.shape != kv or q.dtype != bf16 or k.dtype != bf16 or
+            v.dtype != bf16):
+        for name, t, heads in (("q", q, "heads"), ("k", k, pool.kv_heads), ("v", v, pool.kv_heads)):
+            if t.dtype != bf16 or t.dim() != 3 or t.shape != (rows, t.shape[1] if t is q else heads, dim):
+                _invalid(fn, "%s must be bfloat16 [%d, %s, %d] (got %s %s)" %
+                         (name, rows, heads, dim, t.dtype, list(t.shape)))
+    qr, qh, q1 = q.stride()
+    kr, kh, k1 = k.stride()
+    vr, vh, v1 = v.stride()
+    if q1 != 1 or k1 != 1 or v1 != 1:
+        _invalid(fn, "the last dimension of q, k and v must have stride 1")
     _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
     _dense(fn, "q_weight", q_weight, torch.float32, dim)
     _dense(fn, "k_weight", k_weight, torch.float32, dim)
@@ -524,9 +540,6 @@ def norm_rope_append(pool, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out,
     _vector(fn, "pos", pos, rows)
     max_pos = rope_cs.shape[0]
     _dense(fn, "rope_cs", rope_cs, torch.float32, max_pos, rot // 2, 2)
-    qr, qh, _ = q.stride()
-    kr, kh, _ = k.stride()
-    vr, vh, _ = v.stride()
     _check(_lib.gw_norm_rope_append(pool.desc, q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, v.data_ptr(), vr, vh, rows,
                                     hq, q_weight.data_ptr(), k_weight.data_ptr(), float(eps), 1 if v_norm else 0,
                                     slot.data_ptr(), pos.data_ptr(), rope_cs.data_ptr(), max_pos, out.data_ptr(),
@@ -560,10 +573,10 @@ def _tree_args(fn, dim, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mas
     _dense(fn, "tree_mask", tree_mask, torch.int64, rows)
     _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
     _vector(fn, "seq_lens", seq_lens, batch)
-    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    pages = _table(fn, "block_table", block_table, batch)
     if not workspace.is_contiguous():
         _invalid(fn, "workspace must be contiguous")
-    return handle, rows, hq, batch, block_table.shape[1]
+    return handle, rows, hq, batch, pages
 
 
 def tree_attn_local(pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, pos, workspace, window, scale=None,
@@ -642,12 +655,13 @@ def kv_tree_move(pools, cu_q_rows, seq_lens, block_table, path, path_lens, dev_s
     _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
     _vector(fn, "seq_lens", seq_lens, batch)
     _vector(fn, "path_lens", path_lens, batch)
-    _dense(fn, "block_table", block_table, torch.int32, batch, None)
+    pages = _table(fn, "block_table", block_table, batch)
     stride = _row_stride(fn, "path", path, torch.int32, batch)
-    descs = (PoolDesc * len(pools))(*[p.desc for p in pools])
+    # the descriptions side by side, as a C array of them
+    descs = b"".join([bytes(p.desc) for p in pools])
     _check(_lib.gw_kv_tree_move(descs, len(pools), batch, cu_q_rows.data_ptr(), seq_lens.data_ptr(),
-                                block_table.data_ptr(), block_table.shape[1], path.data_ptr(), stride,
-                                path_lens.data_ptr(), _addr(dev_status), handle))
+                                block_table.data_ptr(), pages, path.data_ptr(), stride, path_lens.data_ptr(),
+                                _addr(dev_status), handle))
 
 
 def merge_lse(outs, lses, out, lse_out=None, stream=None):

@@ -165,7 +165,7 @@ def test_accept_refuses(bad):
 def _move(pools=None, count=None, batch=2, cu=M, lens=M, table=M, pages=64, path=M, stride=16, n=M, status=0):
     pools = pools or [_desc(), _desc(base=2 * M)]
     arr = (gw.PoolDesc * len(pools))(*pools)
-    return gw.lib().gw_kv_tree_move(arr, len(pools) if count is None else count, batch, _at(cu), _at(lens), _at(table),
+    return gw.lib().gw_kv_tree_move(bytes(arr), len(pools) if count is None else count, batch, _at(cu), _at(lens), _at(table),
                                     pages, _at(path), stride, _at(n), _at(status) if status else None, None)
 
 

@@ -36,16 +36,6 @@
 //   warp 5     Q.K^T issue (elect.sync) and TMEM owner
 //   warp 7     P.V issue, so that neither contraction's issue waits on the other
 // Every wait is bounded; a timeout raises GW_DEV_TIMEOUT and the CTA stops.
-//
-// Drafted trees (gw_tree_attn_local, kTree): the same kernel over work units of
-// (sequence, KV head, block of rows, chunk of key tiles).  A row sees the cached
-// tokens of its window and the drafts of its mask word; a tile that holds
-// neither a window's edge nor drafts takes the mask-free path.  K and V are
-// read once for all rows of a KV head's group, so a call is bound by memory
-// (16 drafts of 2 heads: 32 flop/B): what counts is that the producers run on
-// over the units' boundaries.  A sequence of several chunks writes each unit's
-// unnormalised rows and (m, l) for launch_local_tree's merge.
-#include "plan.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"
 namespace gw {
@@ -55,9 +45,6 @@ constexpr int kTM = 128;              // rows per work tile (UMMA M)
 constexpr int kTN = 64;               // keys per key tile (UMMA N of S)
 constexpr int kTcThreads = 256;
 constexpr float kTcLazy = 8.f;
-// trees on e4m3 pools: how far a new reference lies below its logit, so that P's
-// e5m2 terms use their range (2^15 down to 2^-16)
-constexpr float kTreeBelowMax = 7.f;
 // TMEM columns: S buffers at 0 and 64, Q at 128..255, O at 256..511
 constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
 constexpr uint32_t kPlane = kTN * 128;  // one 128-byte chunk column of a K/V tile: 64 rows x 128 B
@@ -67,7 +54,7 @@ constexpr int kKS = 3, kVS = 3;         // K and V stages
 template <int DT>
 constexpr int chunks_of() { return DT == GW_KV_BF16 ? 4 : 2; }
 
-template <int DT, bool kTree = false>
+template <int DT>
 struct TcSmem {
   static constexpr int kC = chunks_of<DT>();
   uint8_t k[kKS][kC * kPlane];    // [chunk][64 keys][128 B], 128-byte swizzled
@@ -77,9 +64,7 @@ struct TcSmem {
   uint64_t q_full, q_free, o_done, o_free;
   int32_t kmask[kKS], vmask[kVS];  // pages of the K / V tile that were loaded (bits 0-3)
   uint32_t tmem_base;
-  int32_t ub[kTree ? kMaxTreeBatch + 1 + 32 : 1];  // trees: the plan (+ scan scratch)
 };
-static_assert(sizeof(TcSmem<GW_KV_BF16, true>) <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void zero16(uint32_t dst) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
@@ -124,65 +109,38 @@ __device__ __forceinline__ int prompt_seq(const int32_t* base, int batch, int t)
 
 struct WorkTile {
   int s, g, q0, nq, P0, lo, hi, t_lo, t_hi, row0;
-  int n, nc;  // trees: the sequence's rows and chunks
 };
 
-// Work tile `tile` of the plan `base`: of the prompt rows, or of a tree's unit
-// (row blocks of a chunk are neighbours, so that its K and V come from L2 for
-// all but the first).
-template <int G, bool kTree>
-__device__ __forceinline__ WorkTile work_tile(const LocalArgs& a, const int32_t* base, int tile) {
+template <int G>
+__device__ __forceinline__ WorkTile work_tile(const LocalArgs& a, int tile) {
   constexpr int BQ = kTM / G;
   WorkTile w;
-  w.s = prompt_seq(base, a.batch, tile);
+  w.s = prompt_seq(a.prompt_base, a.batch, tile);
   const int n = a.cu_q_rows[w.s + 1] - a.cu_q_rows[w.s];
-  const int r0 = tile - base[w.s];
-  const int L = a.seq_lens[w.s];
-  w.P0 = L - n;
-  w.row0 = a.cu_q_rows[w.s];
-  w.n = n;
-  if constexpr (kTree) {
-    const TreeSpan sp = tree_span(L, n, a.window, G, kTreeLocalTiles);
-    w.nc = sp.chunks();
-    const int gc = r0 / sp.blocks, c = gc % w.nc;
-    w.g = gc / w.nc;
-    w.q0 = (r0 - gc * sp.blocks) * BQ;
-    w.t_lo = sp.first + c * sp.ct;
-    w.t_hi = min(sp.first + sp.tiles, w.t_lo + sp.ct) - 1;
-    w.lo = max(max(0, w.P0 - a.window + 1), w.t_lo * kTN);
-    w.hi = min(L - 1, w.t_hi * kTN + kTN - 1);
-    w.nq = min(BQ, n - w.q0);
-    return w;
-  }
   const int nqb = (n + BQ - 1) / BQ;
+  const int r0 = tile - a.prompt_base[w.s];
   w.g = r0 / nqb;
   const int qb = r0 % nqb;
+  const int L = a.seq_lens[w.s];
+  w.P0 = L - n;
   w.q0 = qb * BQ;
   w.nq = min(BQ, n - w.q0);
   w.lo = max(0, w.P0 + w.q0 - a.window + 1);
   w.hi = w.P0 + w.q0 + w.nq - 1;
   w.t_lo = w.lo / kTN;
   w.t_hi = w.hi / kTN;
-  w.nc = 1;
+  w.row0 = a.cu_q_rows[w.s];
   return w;
 }
 
-// 8 floats at a 32-byte boundary: whole sectors, as a lane has a row of its own.
-__device__ __forceinline__ void store_f32x8(float* dst, const uint32_t* x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
-template <int DT, int G, bool kTree>
+template <int DT, int G>
 __global__ void __launch_bounds__(kTcThreads, 1)
     local_prompt_tc_kernel(const LocalArgs a, const __grid_constant__ CUtensorMap kv_map) {
   constexpr int BQ = kTM / G;
   constexpr bool kE4 = DT == GW_KV_E4M3;
   constexpr int kC = chunks_of<DT>();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  using SM = TcSmem<DT, kTree>;
-  SM& sm = *reinterpret_cast<SM*>(smem_raw);
+  TcSmem<DT>& sm = *reinterpret_cast<TcSmem<DT>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   int32_t* st = a.status;
 
@@ -208,9 +166,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  const int32_t* const base = kTree ? sm.ub : a.prompt_base;
-  if constexpr (kTree) plan_tree(a, sm.ub, sm.ub + kMaxTreeBatch + 1, a.kv_heads, G, kTreeLocalTiles, 256);
-  const int total = base[a.batch];
+  const int total = a.prompt_base[a.batch];
   if (warp == 5) {
     tc::alloc(&sm.tmem_base, 512);
     tc::relinquish();
@@ -232,7 +188,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t gi = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const WorkTile w = work_tile<G, kTree>(a, base, tile);
+      const WorkTile w = work_tile<G>(a, tile);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
       for (int t = w.t_lo; t <= w.t_hi; ++t, ++gi) {
         const int ns = is_v ? kVS : kKS;
@@ -274,7 +230,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int wt = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++wt) {
-      const WorkTile w = work_tile<G, kTree>(a, base, tile);
+      const WorkTile w = work_tile<G>(a, tile);
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full, wt & 1, st))) break;
       const int nt = w.t_hi - w.t_lo + 1;
       for (int j = 0; j < nt; ++j, ++gi) {
@@ -314,14 +270,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 7) {
     // ------------------------------------------------------- P.V issue
-    const uint32_t id_o = !kE4    ? tc::idesc_bf16(kTM, 256, false, true)
-                          : kTree ? tc::idesc_e5m2_e4m3(kTM, 256, false, true)
-                                  : tc::idesc_e4m3(kTM, 256, false, true);
+    const uint32_t id_o = kE4 ? tc::idesc_e4m3(kTM, 256, false, true) : tc::idesc_bf16(kTM, 256, false, true);
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
     for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x, ++wt) {
-      const WorkTile w = work_tile<G, kTree>(a, base, tile);
+      const WorkTile w = work_tile<G>(a, tile);
       const int nt = w.t_hi - w.t_lo + 1;
       for (int j = 0; j < nt; ++j, ++gi) {
         const int b = static_cast<int>(gi % kVS), sb = gi & 1;
@@ -352,8 +306,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t bd = tc::smem_desc_sw128(va + kk * 4096, kPlane);
             tc::mma_e4m3_ts_warp(tmem + kColO, tmem + kColS + 64 * sb + 8 * kk, bd, id_o, !(j == 0 && kk == 0));
             tc::mma_e4m3_ts_warp(tmem + kColO, tmem + kColS + 64 * sb + 16 + 8 * kk, bd, id_o, true);
-            if constexpr (kTree)  // a third term (e5m2), at 32..47
-              tc::mma_e4m3_ts_warp(tmem + kColO, tmem + kColS + 64 * sb + 32 + 8 * kk, bd, id_o, true);
           }
         } else {
 #pragma unroll
@@ -377,13 +329,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // largest |q| in [128, 256) and split into two e4m3 terms; sc_q = 2^-e
     // scales the logits back (1 for bf16 pools)
     float sc_q = 1.f;
-    TreeRow seen{};  // trees: the keys of the row whose q was loaded last
     auto load_q = [&](const WorkTile& w) {
       const bool ok_row = qi < w.nq;
-      if constexpr (kTree) {
-        seen = TreeRow{0x7fffffff, 0};
-        if (ok_row) seen = tree_row(a, w.row0, w.q0 + qi, w.n, w.P0, true);
-      }
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (static_cast<int64_t>(w.row0 + w.q0 + (ok_row ? qi : 0)) * a.num_q_heads + w.g * G + hh) * 256);
       if constexpr (kE4) {
@@ -444,15 +391,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     uint32_t gi = 0;
     int wt = 0;
-    if (static_cast<int>(blockIdx.x) < total) load_q(work_tile<G, kTree>(a, base, blockIdx.x));
+    if (static_cast<int>(blockIdx.x) < total) load_q(work_tile<G>(a, blockIdx.x));
     for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++wt) {
-      const WorkTile w = work_tile<G, kTree>(a, base, tile);
+      const WorkTile w = work_tile<G>(a, tile);
       const bool row_ok = qi < w.nq;
       const int pos = w.P0 + w.q0 + qi;
       // this row's keys: [kmin, kmax] (empty for rows past the prompt)
-      const TreeRow row = seen;
-      const int kmin = kTree ? row.kmin : max(w.lo, pos - a.window + 1);
-      const int kmax = kTree ? w.P0 - 1 : row_ok ? pos : -1;
+      const int kmin = max(w.lo, pos - a.window + 1), kmax = row_ok ? pos : -1;
       float m_ref = -INFINITY;            // reference max, scaled log2 units
       float lp[4] = {0.f, 0.f, 0.f, 0.f};  // partial sums of the rounded weights
       const int nt = w.t_hi - w.t_lo + 1;
@@ -467,18 +412,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::wait_ld();
         const int key0 = (w.t_lo + j) * kTN;
         if (!(key0 >= kmin && key0 + kTN - 1 <= kmax)) {
-          // edge tile for this row: keys outside [kmin, kmax] get -inf, drafts by their bits
-          if constexpr (kTree) {
-            const uint64_t m = tree_tile_mask(row, w.P0, key0);
-            const uint32_t m0 = static_cast<uint32_t>(m), m1 = static_cast<uint32_t>(m >> 32);
+          // edge tile for this row: keys outside [kmin, kmax] get -inf
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!(((c < 32 ? m0 : m1) >> (c & 31)) & 1)) sv[c] = __float_as_uint(-INFINITY);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (key0 + c < kmin || key0 + c > kmax) sv[c] = __float_as_uint(-INFINITY);
-          }
+          for (int c = 0; c < 64; ++c)
+            if (key0 + c < kmin || key0 + c > kmax) sv[c] = __float_as_uint(-INFINITY);
         }
         float mg[8];
 #pragma unroll
@@ -489,10 +426,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float mraw = fmaxf(fmaxf(fmaxf(mg[0], mg[1]), fmaxf(mg[2], mg[3])), fmaxf(fmaxf(mg[4], mg[5]), fmaxf(mg[6], mg[7])));
         const float sc = a.scale_log2 * sc_q;  // sc_q: the row's q descale (e4m3 pools)
         const float mx = mraw * sc;            // -inf stays -inf (scale > 0)
-        constexpr float kBelow = kTree && kE4 ? kTreeBelowMax : 0.f;
-        const bool raise = mx > m_ref + (kTcLazy + kBelow);  // false while the row has no key
+        const bool raise = mx > m_ref + kTcLazy;  // false while the row has no key
         if (__any_sync(0xffffffffu, raise)) {
-          const float m_new = raise ? mx - kBelow : m_ref;
+          const float m_new = raise ? mx : m_ref;
           const float alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
           if (__any_sync(0xffffffffu, raise && m_ref != -INFINITY)) {
             // O *= alpha for this warp's rows once P.V of the previous tile is done
@@ -527,22 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // key yet uses m = 0 so that no inf - inf arises
         const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
         uint32_t pw[32];
-        if constexpr (kE4 && kTree) {
-          // three e5m2 terms, 4 keys per column: at columns 0..15, 16..31 and 32..47
-          uint32_t pl[16];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) {
-            float p[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(__uint_as_float(sv[4 * u + i]), sc, neg_m));
-            uint32_t w3[3];
-            lp[u & 3] += tc::split_e5m2(p[0], p[1], p[2], p[3], w3);
-            pw[u] = w3[0];
-            pw[16 + u] = w3[1];
-            pl[u] = w3[2];
-          }
-          tc::st16(tmem + lane_base + kColS + 64 * b + 32, pl);
-        } else if constexpr (kE4) {
+        if constexpr (kE4) {
           // P = P_hi + P_lo, two e4m3 terms (p <= 2^8 under the lazy max), 4
           // keys per column: P_hi at columns 0..15, P_lo at 16..31
 #pragma unroll
@@ -581,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (next < total) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_free, wt & 1, st))) break;
         tc::fence_after();
-        load_q(work_tile<G, kTree>(a, base, next));
+        load_q(work_tile<G>(a, next));
       }
       // ---- epilogue: O / l -> bf16
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.o_done, wt & 1, st))) break;
@@ -589,23 +510,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const float l = (lp[0] + lp[1]) + (lp[2] + lp[3]);
       const float inv = l > 0.f ? 1.f / l : 0.f;
       uint16_t* dst = a.out + (static_cast<int64_t>(w.row0 + w.q0 + qi) * a.num_q_heads + w.g * G + hh) * 256;
-      if (kTree && w.nc > 1) {
-        // ---- a chunk's part of the rows: unnormalised, with its (m, l)
-        const int64_t part = static_cast<int64_t>(tile) * a.part_rows + hh * min(BQ, a.max_q_rows) + qi;
-        if (row_ok) a.part_ml[part] = make_float2(m_ref, l);
-#pragma unroll 1
-        for (int blk = 0; blk < 8; ++blk) {
-          uint32_t o[32];
-          tc::ld32(tmem + lane_base + kColO + 32 * blk, o);
-          tc::wait_ld();
-          if (row_ok)
-#pragma unroll
-            for (int c = 0; c < 32; c += 8) store_f32x8(a.part_o + part * 256 + blk * 32 + c, &o[c]);
-        }
-        tc::fence_before();
-        mbar_arrive(&sm.o_free);
-        continue;
-      }
 #pragma unroll 1
       for (int blk = 0; blk < 8; blk += 2) {
         uint32_t o[64];
@@ -639,26 +543,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int DT, int G, bool kTree>
+template <int DT, int G>
 cudaError_t launch_g(const LocalArgs& a, cudaStream_t st) {
   CUtensorMap map;
   cudaError_t e = make_local_kv_map(a, &map, DT);
   if (e != cudaSuccess) return e;
-  auto kern = local_prompt_tc_kernel<DT, G, kTree>;
-  const size_t smem = sizeof(TcSmem<DT, kTree>);
+  auto kern = local_prompt_tc_kernel<DT, G>;
+  const size_t smem = sizeof(TcSmem<DT>);
   e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(grid_ctas()), dim3(kTcThreads), smem, st, a, map);
 }
 
 
-template <int DT, bool kTree>
+template <int DT>
 cudaError_t launch_dt(int group, const LocalArgs& a, cudaStream_t st) {
   switch (group) {
-    case 1: return launch_g<DT, 1, kTree>(a, st);
-    case 2: return launch_g<DT, 2, kTree>(a, st);
-    case 4: return launch_g<DT, 4, kTree>(a, st);
-    case 8: return launch_g<DT, 8, kTree>(a, st);
+    case 1: return launch_g<DT, 1>(a, st);
+    case 2: return launch_g<DT, 2>(a, st);
+    case 4: return launch_g<DT, 4>(a, st);
+    case 8: return launch_g<DT, 8>(a, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -666,12 +570,7 @@ cudaError_t launch_dt(int group, const LocalArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_local_prompt_tc(int dtype, int group, const LocalArgs& a, cudaStream_t st) {
-  return dtype == GW_KV_E4M3 ? launch_dt<GW_KV_E4M3, false>(group, a, st)
-                             : launch_dt<GW_KV_BF16, false>(group, a, st);
-}
-
-cudaError_t launch_local_tree_tc(int dtype, int group, const LocalArgs& a, cudaStream_t st) {
-  return dtype == GW_KV_E4M3 ? launch_dt<GW_KV_E4M3, true>(group, a, st) : launch_dt<GW_KV_BF16, true>(group, a, st);
+  return dtype == GW_KV_E4M3 ? launch_dt<GW_KV_E4M3>(group, a, st) : launch_dt<GW_KV_BF16>(group, a, st);
 }
 
 }  // namespace gw

@@ -1,5 +1,5 @@
 // Attention of drafted trees: launchers, and the merge of the chunks of long
-// sequences.  The attention kernels are attn_prompt_tc.cu (local layers) and
+// sequences.  The attention kernels are attn_tree_local.cu (local layers) and
 // attn_tree_global.cu (global layers); both write rows of single-chunk
 // sequences themselves.
 //
@@ -12,81 +12,96 @@
 namespace gw {
 namespace {
 
-// A warp merges 256 dims of one (row, head); a lane owns 8 dims, and lanes
-// fetch the chunks' (m, l) two each (kTreeMaxChunks).  Chunks are added in
-// order, so a row does not depend on its companions.  kLocal: units are (KV
-// head, chunk, row block), else (chunk, row block, half of the dims).
+// A block merges 32 of the 256 dims of 32 rows of a unit, a lane a row: parts lie
+// as [unit][8-column block 32][row][8], so that what a warp stores or reads at a
+// time is 1 KB in one piece.  The rows' weights are put in shared memory first; a
+// warp then takes a column block.  Chunks are added in order, so a row does not depend
+// on its companions.  kLocal: units are (KV head, chunk, row block), else (chunk,
+// row block, half of the dims).  134 MB of parts (8 x 128 rows in 64 chunks).
+constexpr int kMergeWarps = 4;
+
+__device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
+  asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "l"(p));
+}
+
 template <bool kLocal>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const LocalArgs a, int group) {
-  constexpr int kSlices = kLocal ? 1 : 2;
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const LocalArgs a, int group, int copies,
+                                                                      int blocks) {
+  __shared__ float w[kTreeMaxChunks][32];
+  __shared__ float top[kMergeWarps][32], inv_sum[32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int slice = static_cast<int>(task % kSlices);
-  const int h = static_cast<int>(task / kSlices % a.num_q_heads);
-  const int64_t sr = task / kSlices / a.num_q_heads;
-  const int r = static_cast<int>(sr % a.max_q_rows);
-  const int s = static_cast<int>(sr / a.max_q_rows);
-  if (s >= a.batch) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int groups = (a.part_rows + 31) / 32;  // of 32 rows, in a unit
+  int task = blockIdx.x;
+  const int c8 = task % (32 / kMergeWarps) * kMergeWarps + warp;
+  task /= 32 / kMergeWarps;
+  const int pg = task % groups;
+  task /= groups;
+  const int qb = task % blocks;
+  task /= blocks;
+  const int copy = task % copies;  // KV head or half
+  const int s = task / copies;
   const int row0 = a.cu_q_rows[s], n = a.cu_q_rows[s + 1] - row0, L = a.seq_lens[s];
   const int ub = a.unit_base[s], units = a.unit_base[s + 1] - ub;
-  if (r >= n || units == 0) return;
+  if (units == 0) return;
   const TreeSpan sp = tree_span(L, n, a.window, group, kLocal ? kTreeLocalTiles : kTreeGlobalTiles);
   const int nc = sp.chunks();
-  if (nc == 1) return;  // the attention kernel has written it
-  const int per = 128 / group, cap = min(per, a.max_q_rows);
-  const int qb = r / per, q = r - qb * per;
-  // unit of chunk c: u0 + c * ustep; the row's place in a unit
-  const int64_t u0 = ub + (kLocal ? h / group * nc * sp.blocks + qb : qb * 2 + slice);
-  const int ustep = kLocal ? sp.blocks : 2 * sp.blocks;
-  const int place = kLocal ? h % group * cap + q : q * group + h;
-  const int64_t first = u0 * a.part_rows + place, step = static_cast<int64_t>(ustep) * a.part_rows;
-  float2 ml[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int c = lane + 32 * k;
-    ml[k] = c < nc ? a.part_ml[first + c * step] : make_float2(-INFINITY, 0.f);
+  if (nc == 1 || qb >= sp.blocks) return;  // the attention kernel has written it
+  const int place = pg * 32 + lane, q = qb * (128 / group) + place / group;
+  const bool ok = place < a.part_rows && q < n;
+  const int64_t u0 = ub + (kLocal ? copy * nc * sp.blocks + qb : qb * 2 + copy);
+  const int64_t step = (kLocal ? sp.blocks : 2 * sp.blocks) * static_cast<int64_t>(a.part_rows);
+  const float2* ml = a.part_ml + u0 * a.part_rows + place;
+  float M = -INFINITY;
+  for (int c = warp; c < nc; c += kMergeWarps) {
+    const float m = ok ? ml[c * step].x : -INFINITY;
+    w[c][lane] = m;
+    M = fmaxf(M, m);
   }
-  float M = fmaxf(ml[0].x, ml[1].x);
+  top[warp][lane] = M;
+  __syncthreads();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float w[2], den = 0.f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) w[k] = M == -INFINITY ? 0.f : ex2(ml[k].x - M);
+  for (int k = 0; k < kMergeWarps; ++k) M = fmaxf(M, top[k][lane]);
+  for (int c = warp; c < nc; c += kMergeWarps) w[c][lane] = M == -INFINITY ? 0.f : ex2(w[c][lane] - M);
+  __syncthreads();
+  if (warp == 0) {
+    float den = 0.f;
+    for (int c = 0; c < nc; ++c) den = fmaf(w[c][lane], ok ? ml[c * step].y : 0.f, den);
+    inv_sum[lane] = den > 0.f ? 1.f / den : 0.f;
+  }
+  __syncthreads();
+  if (!ok) return;
+  const float inv = inv_sum[lane];
+  const int head = kLocal ? copy * group + place % group : place % group;
+  uint16_t* dst = a.out + ((static_cast<int64_t>(row0) + q) * a.num_q_heads + head) * (kLocal ? 256 : 512) +
+                  (kLocal ? 0 : 256 * copy);
+  const float* po = a.part_o + ((u0 * 32 + c8) * a.part_rows + place) * 8;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const float* po = a.part_o + first * 256 + lane * 8;
-#pragma unroll 8
+#pragma unroll 16
   for (int c = 0; c < nc; ++c) {
-    const float4 x = *reinterpret_cast<const float4*>(po + c * step * 256);
-    const float4 y = *reinterpret_cast<const float4*>(po + c * step * 256 + 4);
-    const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
-    const float lc = __shfl_sync(0xffffffffu, c < 32 ? ml[0].y : ml[1].y, c & 31);
-    den = fmaf(wc, lc, den);
-    acc[0] = fmaf(wc, x.x, acc[0]);
-    acc[1] = fmaf(wc, x.y, acc[1]);
-    acc[2] = fmaf(wc, x.z, acc[2]);
-    acc[3] = fmaf(wc, x.w, acc[3]);
-    acc[4] = fmaf(wc, y.x, acc[4]);
-    acc[5] = fmaf(wc, y.y, acc[5]);
-    acc[6] = fmaf(wc, y.z, acc[6]);
-    acc[7] = fmaf(wc, y.w, acc[7]);
+    float x[8];
+    load_f32x8(po + c * step * 256, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[c][lane], x[k], acc[k]);
   }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
   uint32_t pk[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    pk[i] = *reinterpret_cast<uint32_t*>(&b);
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    pk[k] = *reinterpret_cast<uint32_t*>(&b);
   }
-  *reinterpret_cast<uint4*>(a.out + ((static_cast<int64_t>(row0) + r) * a.num_q_heads + h) * (256 * kSlices) +
-                            256 * slice + 8 * lane) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  *reinterpret_cast<uint4*>(dst + 8 * c8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
 }
 
 template <bool kLocal>
 cudaError_t launch_merge(const LocalArgs& a, int group, cudaStream_t st) {
-  const int64_t warps = static_cast<int64_t>(a.batch) * a.max_q_rows * a.num_q_heads * (kLocal ? 1 : 2);
-  return launch_pdl(tree_merge_kernel<kLocal>, dim3(static_cast<unsigned>((warps + 7) / 8)), dim3(256), 0, st, a, group);
+  const int copies = kLocal ? a.kv_heads : 2, per = 128 / group, blocks = (a.max_q_rows + per - 1) / per;
+  const int64_t grid = static_cast<int64_t>(a.batch) * copies * blocks * ((a.part_rows + 31) / 32) * (32 / kMergeWarps);
+  return launch_pdl(tree_merge_kernel<kLocal>, dim3(static_cast<unsigned>(grid)), dim3(kMergeWarps * 32), 0, st, a,
+                    group, copies, blocks);
 }
 
 }  // namespace

@@ -18,9 +18,14 @@
 // On the e4m3 pool q (scaled by an exact power of two per row) is a sum of two
 // e4m3 terms, as in the decode kernel, and P of three e5m2 ones.
 //
-// Warp roles (224 threads): warps 0-3 Q rows, softmax, epilogue (a thread owns
-// a row), warp 4 copies, warp 5 issues Q.K^T and owns tensor memory, warp 6
-// issues P.V.  Every wait is bounded (GW_DEV_TIMEOUT).
+//
+// Warp roles (352 threads): warps 0-3 softmax (a thread owns a row), 4-7 Q rows
+// and epilogue, 8 copies, 9 issues Q.K^T and owns tensor memory, 10 issues P.V.
+// At a unit's end the softmax warps go on with the next unit's first tiles: half
+// of its Q waits in registers, the other half is copied once the last Q.K^T is
+// done, and only the next P.V waits for O to be read (with the softmax warps
+// loading Q and storing O themselves, 10 us between two units, 8 to 50 us long).
+// Every wait is bounded (GW_DEV_TIMEOUT).
 #include "plan.cuh"
 #include "tcgen05.cuh"
 
@@ -28,12 +33,13 @@ namespace gw {
 namespace {
 
 constexpr int kM = 128;
-constexpr int kThreads = 224;
+constexpr int kThreads = 352;
 // O is rescaled when a logit exceeds the reference by more than kLazy; on the
 // e4m3 pool a new reference lies kBelowMax below its logit, so that weights
 // reach 2^15 and a long tail counts down to 2^-23 of the largest.
 constexpr float kLazy = 8.f, kBelowMax = 7.f;
 constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
+constexpr int kRowRing = 4;  // units whose rows' keys are in shared memory
 
 template <int LAYOUT>
 struct TL;
@@ -58,7 +64,7 @@ struct TL<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
   static constexpr bool kE4 = true;
   static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0;
   static constexpr int kPages = 4;
-  static constexpr int kBufs = 4;
+  static constexpr int kBufs = 3;
   __device__ static int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
 };
 
@@ -67,10 +73,12 @@ struct TSmem {
   using T = TL<LAYOUT>;
   uint8_t tiles[T::kBufs][T::kPages * T::kPageBytes];
   uint8_t q[kM * 512];  // Q dims [256, 512): [row block 16][16-byte block 32][8][16 B]; e4m3: hi, then lo
-  uint64_t full[T::kBufs], empty[T::kBufs], s_ready[2], p_ready[2], pfree[2];
+  uint64_t full[T::kBufs], empty[T::kBufs], s_ready[2], p_ready[2], pfree[2], stat_full, stat_free;
   uint64_t q_full, q_free, o_done, o_free;
   int32_t mask[T::kBufs];  // pages of the tile that were loaded
   uint32_t tmem_base;
+  float stat_inv[kM];  // 1 / l of each row
+  float scale[T::kE4 ? kRowRing : 1][T::kE4 ? kM : 1];  // e4m3: 2^-e of each row's scaling
   int32_t ub[kMaxTreeBatch + 1 + 32];
 };
 static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FOLDED>) <= 232448, "shared memory of one CTA");
@@ -157,13 +165,15 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
       mbar_init(&sm.p_ready[b], kM);
       mbar_init(&sm.pfree[b], 1);
     }
+    mbar_init(&sm.stat_full, kM);
+    mbar_init(&sm.stat_free, kM);
     mbar_init(&sm.q_full, kM);
     mbar_init(&sm.q_free, 1);
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.o_free, kM);
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tc::alloc(&sm.tmem_base, 512);
     tc::relinquish();
   }
@@ -176,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   tc::fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // --------------------------------------------------------- page copies
     // lane j < kPages copies page j of a tile: the whole page, or per block of
     // 8 tokens the columns that the unit reads
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s = kE4 ? tc::idesc_e4m3(kM, KN, false, false) : tc::idesc_bf16(kM, KN, false, false);
     // Q dims [256, 512): no-swizzle K-major, 128 B between 16-byte blocks, then
@@ -294,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ------------------------------------------------------- P.V issue
     const uint32_t id_o = kE4 ? tc::idesc_e5m2_e4m3(kM, 256, false, true) : tc::idesc_bf16(kM, 256, false, true);
     uint32_t i = 0;
@@ -331,97 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
-  } else {
-    // ---------------------------------------- Q rows, softmax, epilogue
-    const int r = tid;
-    const int qi = r / HQ, hd = r % HQ;
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ softmax
+    const int r = tid, qi = r / HQ;
     const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-    const uint32_t qs = smem_u32(sm.q);
-    TreeRow seen{};
-    float sc_q = 1.f;  // e4m3: 2^-e of the row's scaling
-    auto load_q = [&](const Unit& w) {
-      const bool ok_row = qi < w.nq;
-      seen = TreeRow{0x7fffffff, 0};
-      if (ok_row) seen = tree_row(a, w.row0, w.q0 + qi, w.n, w.base, false);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(w.row0 + w.q0 + (ok_row ? qi : 0)) * HQ + hd) * 512);
-      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (kE4) {
-        float mq = 0.f;
-#pragma unroll 16
-        for (int c = 0; c < 64; ++c) {
-          const uint4 x = ok_row ? src[c] : none;
-          const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mq = fmaxf(mq, fmaxf(fabsf(__uint_as_float(u4[i] << 16)), fabsf(__uint_as_float(u4[i] & 0xFFFF0000u))));
-        }
-        const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
-        const int e = min(125, max(-125, 7 - ex));
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-        sc_q = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        // an eighth (64 dims) at a time, the second reading from L1
-#pragma unroll 1
-        for (int part = 0; part < 8; ++part) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
-            const uint4 x = ok_row ? src[8 * part + c8] : none;
-            const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int hv = 0; hv < 2; ++hv) {
-              const uint32_t w0 = u4[2 * hv], w1 = u4[2 * hv + 1];
-              uint32_t h0, l0, h1, l1;
-              split_e4m3(__uint_as_float(w0 << 16) * up, __uint_as_float(w0 & 0xFFFF0000u) * up, h0, l0);
-              split_e4m3(__uint_as_float(w1 << 16) * up, __uint_as_float(w1 & 0xFFFF0000u) * up, h1, l1);
-              hi[2 * c8 + hv] = h0 | (h1 << 16);
-              lo[2 * c8 + hv] = l0 | (l1 << 16);
-            }
-          }
-          if (part < 4) {  // dims [0, 256): hi at columns 0..63, lo at 64..127
-            tc::st16(tmem + lane_base + kColQ + 16 * part, hi);
-            tc::st16(tmem + lane_base + kColQ + 64 + 16 * part, lo);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t at = qs + cm_off(r, 4 * (part - 4) + c, 16);
-              sts16(at, hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-              sts16(at + 32768, lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
-            }
-          }
-        }
-      } else {
-        uint32_t qv[128];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {  // dims [0, 256) -> tensor memory
-          const uint4 x = ok_row ? src[c] : none;
-          qv[4 * c] = x.x;
-          qv[4 * c + 1] = x.y;
-          qv[4 * c + 2] = x.z;
-          qv[4 * c + 3] = x.w;
-        }
-#pragma unroll
-        for (int blk = 0; blk < 4; ++blk)
-          tc::st32(tmem + lane_base + kColQ + 32 * blk, *reinterpret_cast<uint32_t(*)[32]>(&qv[32 * blk]));
-#pragma unroll 8
-        for (int c = 0; c < 32; ++c) {  // dims [256, 512) -> shared memory
-          const uint4 x = ok_row ? src[32 + c] : none;
-          sts16(qs + cm_off(r, c, 32), x.x, x.y, x.z, x.w);
-        }
-      }
-      tc::wait_st();
-      fence_proxy_async_smem();
-      tc::fence_before();
-      mbar_arrive(&sm.q_full);
+    auto row_of = [&](const Unit& w) {
+      return qi < w.nq ? tree_row(a, w.row0, w.q0 + qi, w.n, w.base, false) : TreeRow{0, 0x7fffffff, 1.f};
     };
     uint32_t gi = 0;
     int wt = 0;
-    if (static_cast<int>(blockIdx.x) < total) load_q(unit_of<HQ, KN>(a, sm.ub, blockIdx.x));
+    TreeRow next_row{0, 0x7fffffff, 1.f};
+    if (static_cast<int>(blockIdx.x) < total) next_row = row_of(unit_of<HQ, KN>(a, sm.ub, blockIdx.x));
     for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
       const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
       const bool row_ok = qi < w.nq;
-      const TreeRow row = seen;
-      const float sc = a.scale_log2 * sc_q;
+      const TreeRow row = next_row;
+      const int next = u + gridDim.x;
+      if (next < total) next_row = row_of(unit_of<HQ, KN>(a, sm.ub, next));  // in flight over this unit
+      float sc = a.scale_log2;
       float m_ref = -INFINITY;
       float lp[4] = {0.f, 0.f, 0.f, 0.f};
       bool ok = true;
@@ -429,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         const int b = gi & 1;
         if (!warp_wait(&sm.s_ready[b], (gi >> 1) & 1, st)) { ok = false; break; }
         tc::fence_after();
+        if (kE4 && j == 0) sc = a.scale_log2 * sm.scale[wt % kRowRing][r];  // written before Q was handed over
         uint32_t sv[KN];
 #pragma unroll
         for (int c0 = 0; c0 < KN; c0 += 32)
@@ -518,28 +456,158 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         mbar_arrive(&sm.p_ready[b]);
       }
       if (!ok) break;
+      const float l = (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      if (w.nc > 1 && row_ok) a.part_ml[static_cast<int64_t>(u) * a.part_rows + r] = make_float2(m_ref, l);
+      if (wt >= 1 && !warp_wait(&sm.stat_free, (wt - 1) & 1, st)) break;
+      sm.stat_inv[r] = l > 0.f ? 1.f / l : 0.f;
+      mbar_arrive(&sm.stat_full);
+    }
+  } else {
+    // ------------------------------------------------- Q rows and epilogue
+    const int r = tid - kM;
+    const int qi = r / HQ, hd = r % HQ;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t qs = smem_u32(sm.q);
+    auto row_src = [&](const Unit& w, int row) {  // row `row` of the unit's 128
+      return a.q + (static_cast<int64_t>(w.row0 + w.q0 + row / HQ) * HQ + row % HQ) * 512;
+    };
+    // The next unit's dims [0, 256) of this thread's row, as tensor memory wants
+    // them: bf16, or e4m3 hi (64 words) then lo.
+    uint32_t qv[128];
+    float up = 1.f;
+    auto split16 = [&](const uint4& x, const uint4& y, uint32_t* hi, uint32_t* lo) {  // 16 dims: 4 words of each term
+      const uint32_t u8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t h0, l0, h1, l1;
+        split_e4m3(__uint_as_float(u8[2 * i] << 16) * up, __uint_as_float(u8[2 * i] & 0xFFFF0000u) * up, h0, l0);
+        split_e4m3(__uint_as_float(u8[2 * i + 1] << 16) * up, __uint_as_float(u8[2 * i + 1] & 0xFFFF0000u) * up, h1, l1);
+        hi[i] = h0 | (h1 << 16);
+        lo[i] = l0 | (l1 << 16);
+      }
+    };
+    auto load_q = [&](const Unit& w, int wt) {
+      const bool ok_row = qi < w.nq;
+      const uint4* src = reinterpret_cast<const uint4*>(row_src(w, ok_row ? r : 0));
+      const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kE4) {
+        float mq = 0.f;
+        if (ok_row) {
+#pragma unroll 16
+          for (int c = 0; c < 64; ++c) {
+            const uint4 x = src[c];
+            const uint32_t u4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              mq = fmaxf(mq, fmaxf(fabsf(__uint_as_float(u4[i] << 16)), fabsf(__uint_as_float(u4[i] & 0xFFFF0000u))));
+          }
+        }
+        const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
+        const int e = min(125, max(-125, 7 - ex));
+        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        sm.scale[wt % kRowRing][r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          split16(ok_row ? src[2 * c] : none, ok_row ? src[2 * c + 1] : none, &qv[4 * c], &qv[64 + 4 * c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint4 x = ok_row ? src[c] : none;
+          qv[4 * c] = x.x;
+          qv[4 * c + 1] = x.y;
+          qv[4 * c + 2] = x.z;
+          qv[4 * c + 3] = x.w;
+        }
+        // the other half is copied when its room is free: into L2 now
+        if (ok_row) prefetch_l2(src + 32, 512);
+      }
+    };
+    auto store_q = [&](const Unit& w) {
+      auto store_low = [&]() {
+#pragma unroll
+        for (int blk = 0; blk < 4; ++blk)
+          tc::st32(tmem + lane_base + kColQ + 32 * blk, *reinterpret_cast<uint32_t(*)[32]>(&qv[32 * blk]));
+      };
+      if constexpr (kE4) {
+        store_low();
+        const bool ok_row = qi < w.nq;
+        const uint4* src = reinterpret_cast<const uint4*>(row_src(w, ok_row ? r : 0)) + 32;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+        for (int c = 0; c < 16; ++c) {
+          uint32_t hi[4], lo[4];
+          split16(ok_row ? src[2 * c] : none, ok_row ? src[2 * c + 1] : none, hi, lo);
+          const uint32_t at = qs + cm_off(r, c, 16);
+          sts16(at, hi[0], hi[1], hi[2], hi[3]);
+          sts16(at + 32768, lo[0], lo[1], lo[2], lo[3]);
+        }
+      } else {
+        // a warp's 32 rows, 8 rows x 4 blocks of 16 bytes at a time: whole sectors
+        // from memory, 512 contiguous bytes of shared memory
+        const int rows = w.nq * HQ;
+        const int row0 = 32 * (warp & 3) + (lane & 7);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int row = row0 + 8 * g;
+          const uint16_t* src = row_src(w, row < rows ? row : 0) + 256 + 8 * (lane >> 3);
+          const uint32_t at = qs + cm_off(row, lane >> 3, 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (row < rows)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 512 * i), "l"(src + 32 * i)
+                           : "memory");
+            else
+              zero16(at + 512 * i);
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        store_low();
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      tc::wait_st();
+      fence_proxy_async_smem();
+      tc::fence_before();
+      mbar_arrive(&sm.q_full);
+    };
+    if (static_cast<int>(blockIdx.x) < total) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, blockIdx.x);
+      load_q(w, 0);
+      store_q(w);
+    }
+    int wt = 0;
+    for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
+      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
       const int next = u + gridDim.x;
       if (next < total) {
+        const Unit wn = unit_of<HQ, KN>(a, sm.ub, next);
+        load_q(wn, wt + 1);
         if (!warp_wait(&sm.q_free, wt & 1, st)) break;
         tc::fence_after();
-        load_q(unit_of<HQ, KN>(a, sm.ub, next));
+        store_q(wn);
       }
       // ---- epilogue: this half of O, as output rows or as a chunk's part
+      if (!warp_wait(&sm.stat_full, wt & 1, st)) break;
+      const float inv = sm.stat_inv[r];
+      mbar_arrive(&sm.stat_free);
       if (!warp_wait(&sm.o_done, wt & 1, st)) break;
       tc::fence_after();
-      const float l = (lp[0] + lp[1]) + (lp[2] + lp[3]);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t part = static_cast<int64_t>(u) * a.part_rows + r;
-      if (w.nc > 1 && row_ok) a.part_ml[part] = make_float2(m_ref, l);
+      const bool row_ok = qi < w.nq;
+      // a part's columns by eights, [8-column block 32][row][8]: a warp's store is
+      // then 1 KB in one piece (by rows, 32 lines: reading O took 3 us)
+      float* const part = a.part_o + (static_cast<int64_t>(u) * 32 * a.part_rows + r) * 8;
       uint16_t* dst = a.out + (static_cast<int64_t>(w.row0 + w.q0 + qi) * HQ + hd) * 512 + 256 * w.half;
 #pragma unroll 1
       for (int blk = 0; blk < 8; ++blk) {
         uint32_t o[32];
         tc::ld32(tmem + lane_base + kColO + 32 * blk, o);
         tc::wait_ld();
+        if (blk == 7) {  // O has been read
+          tc::fence_before();
+          mbar_arrive(&sm.o_free);
+        }
         if (row_ok && w.nc > 1) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) store_f32x8(a.part_o + part * 256 + blk * 32 + c, &o[c]);
+          for (int c = 0; c < 32; c += 8) store_f32x8(part + static_cast<int64_t>(blk * 4 + c / 8) * a.part_rows * 8, &o[c]);
         } else if (row_ok) {
 #pragma unroll
           for (int c = 0; c < 32; c += 8) {
@@ -555,14 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
         __syncwarp();
       }
-      tc::fence_before();
-      mbar_arrive(&sm.o_free);
     }
   }
 
   tc::fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc::fence_after();
     tc::dealloc(tmem, 512);
   }

@@ -65,15 +65,15 @@ __host__ __device__ __forceinline__ int global_chunks(int L) {
 constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask word
 constexpr int kMaxTreeBatch = 512;  // sequences of a call: their plan is in shared memory
 constexpr int kTreeTile = 64;
-constexpr int kTreeMaxChunks = 64;
+constexpr int kTreeMaxChunks = 38;
 
-// Chunks of `tiles` tiles, `min_tiles` each or that doubled until there are at
-// most kTreeMaxChunks / blocks of them (`blocks` row blocks share the GPU).
-__host__ __device__ __forceinline__ int tree_chunk_tiles(int tiles, int min_tiles, int blocks) {
+// Tiles of a chunk: `tiles` tiles in even chunks of at most `aim`, or longer ones
+// where that would be more than kTreeMaxChunks / blocks of them (`blocks` row
+// blocks share the GPU).
+__host__ __device__ __forceinline__ int tree_chunk_tiles(int tiles, int aim, int blocks) {
   const int most = blocks < kTreeMaxChunks ? kTreeMaxChunks / blocks : 1;
-  int ct = min_tiles;
-  while ((tiles - 1) / ct + 1 > most) ct *= 2;
-  return ct;
+  const int want = (tiles - 1) / aim + 1, chunks = want < most ? want : most;
+  return (tiles - 1) / chunks + 1;
 }
 
 struct TreeSpan {
@@ -86,27 +86,27 @@ struct TreeSpan {
 
 // Of n rows over L >= n >= 1 tokens: `group` heads share a tile's rows.  Rows
 // sit at tokens L - n and later, so the first key of any is L - n - window + 1.
-__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int group, int min_tiles) {
+__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int group, int aim) {
   TreeSpan s;
   const int lo = L - n - window + 1;
   s.first = lo > 0 ? lo / kTreeTile : 0;
   s.tiles = (L - 1) / kTreeTile - s.first + 1;
   const int per = 128 / group;
   s.blocks = (n + per - 1) / per;
-  s.ct = tree_chunk_tiles(s.tiles, min_tiles, s.blocks);
+  s.ct = tree_chunk_tiles(s.tiles, aim, s.blocks);
   return s;
 }
 // A bound on a sequence's chunks over L <= 16 * max_pages and n <= max_rows.
-__host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_rows, int window, int min_tiles) {
+__host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_rows, int window, int aim) {
   // tokens in sight: all, or window - 1 cached ones and the drafts, in tiles they need not begin
   const int64_t all = (static_cast<int64_t>(max_pages) * 16 + kTreeTile - 1) / kTreeTile;
   const int64_t seen = (static_cast<int64_t>(window) + max_rows + kTreeTile - 3) / kTreeTile + 1;
-  const int64_t c = ((all < seen ? all : seen) + min_tiles - 1) / min_tiles;
+  const int64_t c = ((all < seen ? all : seen) + aim - 1) / aim;
   return static_cast<int>(c < kTreeMaxChunks ? c : kTreeMaxChunks);
 }
-// Smallest chunks, in tiles (attn_prompt_tc.cu, attn_tree_global.cu).
-constexpr int kTreeLocalTiles = 4;
-constexpr int kTreeGlobalTiles = 8;
+// Tiles of a chunk, at most (attn_tree_local.cu, attn_tree_global.cu).
+constexpr int kTreeLocalTiles = 18;
+constexpr int kTreeGlobalTiles = 24;
 
 // Workspace layout (offsets from the 256-byte aligned workspace base):
 //   [0, 256)          reserved

@@ -86,7 +86,7 @@ __device__ void plan_in_smem(const LocalArgs& a, int32_t* ub, int32_t* scratch, 
 // their rows or beyond the block table (GW_DEV_LEN_RANGE), whose output rows
 // become zeros here.  CTA 0 stores the plan for the merge.
 __device__ __forceinline__ void plan_tree(const LocalArgs& a, int32_t* ub, int32_t* scratch, int copies, int group,
-                                          int min_tiles, int head_dim) {
+                                          int aim, int head_dim) {
   auto rows_of = [&](int s) { return a.cu_q_rows[s + 1] - a.cu_q_rows[s]; };
   auto valid = [&](int s) {
     const int n = rows_of(s), L = a.seq_lens[s];
@@ -94,7 +94,7 @@ __device__ __forceinline__ void plan_tree(const LocalArgs& a, int32_t* ub, int32
   };
   plan_scan(a.batch, ub, scratch, [&](int s) {
     if (!valid(s)) return 0;
-    const TreeSpan sp = tree_span(a.seq_lens[s], rows_of(s), a.window, group, min_tiles);
+    const TreeSpan sp = tree_span(a.seq_lens[s], rows_of(s), a.window, group, aim);
     return copies * sp.blocks * sp.chunks();
   });
   for (int s = blockIdx.x; s < a.batch; s += gridDim.x) {
@@ -111,10 +111,12 @@ __device__ __forceinline__ void plan_tree(const LocalArgs& a, int32_t* ub, int32
 }
 
 // The keys of a tree's row: cached tokens [kmin, base) and the drafts of
-// `drafts`, bit i of which is token base + i.
+// `drafts`, bit i of which is token base + i; and what its logits are scaled by
+// (q's scaling undone, on e4m3 pools).
 struct TreeRow {
-  int kmin;
   uint64_t drafts;
+  int kmin;
+  float scale;
 };
 
 // Row r of sequence s (n rows at tokens [base, base + n), first row row0); one
@@ -124,6 +126,7 @@ struct TreeRow {
 __device__ __forceinline__ TreeRow tree_row(const LocalArgs& a, int row0, int r, int n, int base, bool windowed) {
   TreeRow t;
   t.kmin = 0;
+  t.scale = 1.f;
   t.drafts = a.tree_mask[row0 + r] & (n < 64 ? (1ull << n) - 1 : ~0ull);
   if (windowed) {
     const int pos = a.tree_pos[row0 + r];

@@ -259,4 +259,4 @@ def test_binding_refuses():
         with pytest.raises(gw.GwError):
             gw.tree_attn_local(*call, max_q_rows=4)
     with pytest.raises(gw.GwError, match="workspace_bytes"):
-        gw.tree_attn_local(*args[:5], torch.zeros(1, 64, dtype=torch.int32, device="cuda"), *args[6:8], c.ws, 1024)
+        gw.tree_attn_local(*args[:5], torch.zeros(1, 512, dtype=torch.int32, device="cuda"), *args[6:8], c.ws, 1 << 20)

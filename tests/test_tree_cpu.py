@@ -103,11 +103,9 @@ def test_attn_unsupported_workspace_and_empty():
         assert need > 0 and _global(desc=_desc(layout, dtype), hq=32, pages=512, ws_bytes=need - 1) == gw.GW_ERR_WORKSPACE
 
 
-def _chunks(tiles, least, blocks):
-    most, ct = max(1, 64 // blocks), least
-    while -(-tiles // ct) > most:
-        ct *= 2
-    return -(-tiles // ct)
+def _chunks(tiles, aim, blocks):
+    chunks = min(-(-tiles // aim), max(1, 38 // blocks))
+    return -(-tiles // -(-tiles // chunks))
 
 
 @pytest.mark.parametrize("layout,heads,kvh,window", [
@@ -117,7 +115,7 @@ def _chunks(tiles, least, blocks):
 def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
     """No mix of rows and lengths up to the bounds needs more units than the workspace holds."""
     local = layout == gw.LAYOUT_LOCAL
-    group, copies, least = (heads // kvh, kvh, 4) if local else (heads, 2, 8)
+    group, copies, aim = (heads // kvh, kvh, 18) if local else (heads, 2, 24)
     got = gw.lib().gw_tree_workspace_bytes(ctypes.byref(_desc(layout, kvh=kvh, base=0)), heads, 3, pages, rows, window)
     cap = group * min(128 // group, rows)
     worst = 0
@@ -129,7 +127,7 @@ def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
             if L < n:
                 continue
             first = max(0, L - n - window + 1) // 64 if local else 0
-            nc = _chunks((L - 1) // 64 - first + 1, least, blocks)
+            nc = _chunks((L - 1) // 64 - first + 1, aim, blocks)
             if nc > 1:
                 worst = max(worst, copies * blocks * nc)
     assert got >= 3 * worst * cap * (256 * 4 + 8)  # both kinds write parts of 256 dims

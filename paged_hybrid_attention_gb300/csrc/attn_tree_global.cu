@@ -26,6 +26,8 @@
 // done, and only the next P.V waits for O to be read (with the softmax warps
 // loading Q and storing O themselves, 10 us between two units, 8 to 50 us long).
 // Every wait is bounded (GW_DEV_TIMEOUT).
+#include <type_traits>
+
 #include "plan.cuh"
 #include "tcgen05.cuh"
 
@@ -33,7 +35,7 @@ namespace gw {
 namespace {
 
 constexpr int kM = 128;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
 // O is rescaled when a logit exceeds the reference by more than kLazy; on the
 // e4m3 pool a new reference lies kBelowMax below its logit, so that weights
 // reach 2^15 and a long tail counts down to 2^-23 of the largest.
@@ -49,7 +51,8 @@ struct TL<GW_LAYOUT_GLOBAL_FOLDED> {
   static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0;
   static constexpr int kPages = 4;   // pages of a tile
   static constexpr int kBufs = 2;    // tiles in shared memory
-  __device__ static int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
+  static constexpr int kSteps = 32;  // K-steps of Q.K^T (32 bytes of a row each)
+  __device__ static constexpr int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
 };
 template <>
 struct TL<GW_LAYOUT_GLOBAL_FULL> {
@@ -57,7 +60,8 @@ struct TL<GW_LAYOUT_GLOBAL_FULL> {
   static constexpr int kPageBytes = 32768, kBlk = 128, kVcb = 64;
   static constexpr int kPages = 2;
   static constexpr int kBufs = 2;
-  __device__ static int k_cb(int ks) { return 2 * ks; }
+  static constexpr int kSteps = 32;
+  __device__ static constexpr int k_cb(int ks) { return 2 * ks; }
 };
 template <>
 struct TL<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
@@ -65,7 +69,37 @@ struct TL<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
   static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0;
   static constexpr int kPages = 4;
   static constexpr int kBufs = 3;
-  __device__ static int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
+  static constexpr int kSteps = 16;
+  __device__ static constexpr int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
+};
+
+// The column blocks of a tile in two parts: V's half that the unit multiplies P
+// with, and the rest of what Q.K^T reads (the folded layouts' K is partly V).
+template <int LAYOUT>
+struct Parts {
+  using T = TL<LAYOUT>;
+  static constexpr int kV = T::kE4 ? 16 : 32;  // blocks of V's half
+  // Whether the parts are copied and released on their own.  The bf16 layouts have
+  // room for two tiles, and a call waits on their copies (a tile 1.60 us, in parts
+  // 1.40); the e4m3 one has three and waits on Q.K^T (1.45 us, in parts 1.55).
+  static constexpr bool kApart = !T::kE4;
+  __device__ static constexpr int v0(int half) { return T::kVcb + kV * half; }
+  // runs [first, end) of the rest
+  __device__ static constexpr int runs(int half) { return kApart && LAYOUT != GW_LAYOUT_GLOBAL_FULL && half ? 2 : 1; }
+  __device__ static constexpr int first(int half, int i) {
+    if (LAYOUT == GW_LAYOUT_GLOBAL_FULL) return 0;
+    if (!kApart) return half ? kV / 2 : 0;
+    return half == 0 ? kV : i == 0 ? kV / 2 : 2 * kV;
+  }
+  __device__ static constexpr int end(int half, int i) {
+    if (LAYOUT == GW_LAYOUT_GLOBAL_FULL) return 64;
+    return kApart && half == 1 && i == 0 ? kV : T::kBlk;
+  }
+  __device__ static constexpr int rest(int half) {  // blocks that warp 8 copies
+    if (!kApart) return half ? T::kBlk - kV / 2 : T::kBlk;
+    return end(half, 0) - first(half, 0) + (runs(half) > 1 ? end(half, 1) - first(half, 1) : 0);
+  }
+  __device__ static constexpr bool in_v(int half, int cb) { return kApart && cb >= v0(half) && cb < v0(half) + kV; }
 };
 
 template <int LAYOUT>
@@ -73,7 +107,7 @@ struct TSmem {
   using T = TL<LAYOUT>;
   uint8_t tiles[T::kBufs][T::kPages * T::kPageBytes];
   uint8_t q[kM * 512];  // Q dims [256, 512): [row block 16][16-byte block 32][8][16 B]; e4m3: hi, then lo
-  uint64_t full[T::kBufs], empty[T::kBufs], s_ready[2], p_ready[2], pfree[2], stat_full, stat_free;
+  uint64_t kfull[T::kBufs], kempty[T::kBufs], vfull[T::kBufs], vempty[T::kBufs], s_ready[2], p_ready[2], pfree[2], stat_full, stat_free;
   uint64_t q_full, q_free, o_done, o_free;
   int32_t mask[T::kBufs];  // pages of the tile that were loaded
   uint32_t tmem_base;
@@ -157,8 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
 
   if (tid == 0) {
     for (int b = 0; b < NB; ++b) {
-      mbar_init(&sm.full[b], 1);
-      mbar_init(&sm.empty[b], 1);
+      mbar_init(&sm.kfull[b], 1);
+      mbar_init(&sm.kempty[b], 1);
+      mbar_init(&sm.vfull[b], 1);
+      mbar_init(&sm.vempty[b], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.s_ready[b], 1);
@@ -186,58 +222,64 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   tc::fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 8) {
+  if (warp == 8 || warp == 11) {
     // --------------------------------------------------------- page copies
-    // lane j < kPages copies page j of a tile: the whole page, or per block of
-    // 8 tokens the columns that the unit reads
+    // warp 11 copies V's half, warp 8 the rest; lane l takes 8-token block l % 2
+    // of page l / 2 of a tile
+    using PT = Parts<LAYOUT>;
+    const bool is_v = warp == 11;
+    uint64_t* const fulls = is_v ? sm.vfull : sm.kfull;
+    uint64_t* const empties = is_v ? sm.vempty : sm.kempty;
     const uint64_t pol = policy_evict_last();  // the other half and row blocks read them too
-    uint32_t gi = 0;
+    const int page = lane >> 1, tb = lane & 1;
+    uint32_t gi = 0, halves = 0;  // bit b: the half of buffer b's last tile
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
+    for (int u = blockIdx.x; u < total && ok && (PT::kApart || !is_v); u += gridDim.x) {
       const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
+      const uint32_t bytes = 128 * (is_v ? PT::kV : w.half ? PT::rest(1) : PT::rest(0));  // of an 8-token block
       for (int t = 0; t < w.nt; ++t, ++gi) {
         const int b = gi % NB;
         const uint32_t use = gi / NB;
-        const int k = w.k0 + t * KN + lane * kPage;
+        const int k = w.k0 + t * KN + page * kPage;
         int32_t pg = -1;
-        if (lane < T::kPages && k < w.k1) {
+        if (page < T::kPages && k < w.k1) {
           pg = bt[k / kPage];
           if (pg < 0 || pg >= a.num_pages) {
-            set_status(st, GW_DEV_PAGE_RANGE);
+            if (!is_v) set_status(st, GW_DEV_PAGE_RANGE);
             pg = -1;
           }
         }
-        const uint32_t loaded = __ballot_sync(0xffffffffu, pg >= 0);
-        if (use > 0 && !warp_wait(&sm.empty[b], (use - 1) & 1, st)) { ok = false; break; }
-        uint32_t bytes = T::kPageBytes;
-        if (LAYOUT == GW_LAYOUT_GLOBAL_FULL)
-          bytes = 2 * (64 + 32) * 128;
-        else if (w.half)
-          bytes = 2 * (T::kBlk * 4 / 5) * 128;  // without V[0:128), a fifth of the row
+        const uint32_t blocks = __ballot_sync(0xffffffffu, pg >= 0);  // bits 2 j, 2 j + 1: page j
+        if (use > 0 && !warp_wait(&empties[b], (use - 1) & 1, st)) { ok = false; break; }
+        // the rest's columns of one half are V's of the other: after a tile of the
+        // other half they are free once its P.V is done (which is after its Q.K^T)
+        if (PT::kApart && !is_v && use > 0 && static_cast<int>((halves >> b) & 1) != w.half &&
+            !warp_wait(&sm.vempty[b], (use - 1) & 1, st)) {
+          ok = false;
+          break;
+        }
+        halves = (halves & ~(1u << b)) | (static_cast<uint32_t>(w.half) << b);
         if (lane == 0) {
-          sm.mask[b] = static_cast<int32_t>(loaded);
-          mbar_arrive_expect_tx(&sm.full[b], static_cast<uint32_t>(__popc(loaded)) * bytes);
+          if (!is_v) {
+            int mask = 0;
+#pragma unroll
+            for (int j = 0; j < T::kPages; ++j) mask |= ((blocks >> (2 * j)) & 1) << j;
+            sm.mask[b] = mask;
+          }
+          mbar_arrive_expect_tx(&fulls[b], static_cast<uint32_t>(__popc(blocks)) * bytes);
         }
         __syncwarp();
         if (pg >= 0) {
-          uint8_t* dst = sm.tiles[b] + lane * T::kPageBytes;
-          const uint8_t* src = a.pool + static_cast<int64_t>(pg) * T::kPageBytes;
-          if (LAYOUT == GW_LAYOUT_GLOBAL_FULL) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-              const int o = tb * T::kBlk * 128, v = o + (T::kVcb + 32 * w.half) * 128;
-              bulk_g2s(dst + o, src + o, 64 * 128, &sm.full[b], pol);
-              bulk_g2s(dst + v, src + v, 32 * 128, &sm.full[b], pol);
-            }
-          } else if (w.half) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-              const int o = (tb * T::kBlk + T::kBlk / 5) * 128;
-              bulk_g2s(dst + o, src + o, (T::kBlk * 4 / 5) * 128, &sm.full[b], pol);
-            }
+          uint8_t* dst = sm.tiles[b] + page * T::kPageBytes + tb * T::kBlk * 128;
+          const uint8_t* src = a.pool + static_cast<int64_t>(pg) * T::kPageBytes + tb * T::kBlk * 128;
+          auto copy = [&](int cb0, int cb1) {
+            bulk_g2s(dst + cb0 * 128, src + cb0 * 128, (cb1 - cb0) * 128, &fulls[b], pol);
+          };
+          if (is_v) {
+            copy(PT::v0(w.half), PT::v0(w.half) + PT::kV);
           } else {
-            bulk_g2s(dst, src, T::kPageBytes, &sm.full[b], pol);
+            for (int i = 0; i < PT::runs(w.half); ++i) copy(PT::first(w.half, i), PT::end(w.half, i));
           }
         }
       }
@@ -256,50 +298,60 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
       if (!warp_wait(&sm.q_full, wt & 1, st)) break;
       for (int j = 0; j < w.nt; ++j, ++i) {
         const int b = i % NB, sb = i & 1;
-        if (!warp_wait(&sm.full[b], (i / NB) & 1, st)) { ok = false; break; }
+        if (!warp_wait(&sm.kfull[b], (i / NB) & 1, st)) { ok = false; break; }
         // this S buffer holds P of tile i - 2 until its P.V is done
         if (i >= 2 && !warp_wait(&sm.pfree[sb], ((i >> 1) - 1) & 1, st)) { ok = false; break; }
         const uint32_t ta = smem_u32(sm.tiles[b]);
         const int mask = sm.mask[b];
-        const int key0 = w.k0 + j * KN;
-        if (mask != (1 << T::kPages) - 1 || key0 + KN > w.k1) {
-          // pages not loaded, and V rows behind the last key (K rows only make
-          // logits that are masked): finite zeros
+        if (mask != (1 << T::kPages) - 1) {  // pages not loaded: zeros
+          if (Parts<LAYOUT>::kApart && !warp_wait(&sm.vfull[b], (i / NB) & 1, st)) { ok = false; break; }
           for (int pgi = 0; pgi < T::kPages; ++pgi) {
             if ((mask >> pgi) & 1) continue;
             for (int o = lane * 16; o < T::kPageBytes; o += 32 * 16) zero16(ta + pgi * T::kPageBytes + o);
           }
-          for (int k = max(w.k1 - key0, 0); k < KN; ++k)
-            for (int cb = lane; cb < (kE4 ? 32 : 64); cb += 32)
-              zero16(ta + ((k >> 3) * T::kBlk + T::kVcb + cb) * 128 + (k & 7) * 16);
         }
         fence_proxy_async_smem();
         __syncwarp();
         tc::fence_after();
         const uint64_t dk = tc::smem_desc(ta, 128, T::kBlk * 128);
         const uint32_t ds = tmem + kColS + KN * sb;
-        if constexpr (kE4) {
-#pragma unroll
-          for (int ks = 0; ks < 16; ++ks) {
-            const uint64_t bd = dk + ((T::k_cb(ks) * 128) >> 4);
+        auto step = [&](int ks, bool more) {
+          const uint64_t bd = dk + ((T::k_cb(ks) * 128) >> 4);
+          if constexpr (kE4) {
             if (ks < 8) {
-              tc::mma_e4m3_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, ks > 0);
+              tc::mma_e4m3_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, more);
               tc::mma_e4m3_ts_warp(ds, tmem + kColQ + 64 + 8 * ks, bd, id_s, true);
             } else {
-              tc::mma_e4m3_warp(ds, dq + (((ks - 8) * 256) >> 4), bd, id_s, true);
+              tc::mma_e4m3_warp(ds, dq + (((ks - 8) * 256) >> 4), bd, id_s, more);
               tc::mma_e4m3_warp(ds, dq + ((32768 + (ks - 8) * 256) >> 4), bd, id_s, true);
             }
-          }
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < 32; ++ks) {
-            const uint64_t bd = dk + ((T::k_cb(ks) * 128) >> 4);
+          } else {
             if (ks < 16)
-              tc::mma_bf16_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, ks > 0);
+              tc::mma_bf16_ts_warp(ds, tmem + kColQ + 8 * ks, bd, id_s, more);
             else
-              tc::mma_bf16_warp(ds, dq + (((ks - 16) * 256) >> 4), bd, id_s, true);
+              tc::mma_bf16_warp(ds, dq + (((ks - 16) * 256) >> 4), bd, id_s, more);
           }
+        };
+        // the K-steps outside V's half (the first of all is one of them), then,
+        // once it is there, those in it
+        auto steps = [&](auto half, bool v) {
+#pragma unroll
+          for (int ks = 0; ks < T::kSteps; ++ks)
+            if (Parts<LAYOUT>::in_v(half, T::k_cb(ks)) == v) step(ks, ks > 0);
+        };
+        auto issue = [&](bool v) {
+          if (w.half)
+            steps(std::integral_constant<int, 1>{}, v);
+          else
+            steps(std::integral_constant<int, 0>{}, v);
+        };
+        issue(false);
+        if (Parts<LAYOUT>::kApart && LAYOUT != GW_LAYOUT_GLOBAL_FULL) {
+          if (!warp_wait(&sm.vfull[b], (i / NB) & 1, st)) { ok = false; break; }
+          tc::fence_after();
+          issue(true);
         }
+        if (Parts<LAYOUT>::kApart) tc::commit_warp(&sm.kempty[b]);
         tc::commit_warp(&sm.s_ready[sb]);
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
@@ -315,9 +367,20 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
       for (int j = 0; j < w.nt; ++j, ++i) {
         const int b = i % NB, sb = i & 1;
         if (j == 0 && wt >= 1 && !warp_wait(&sm.o_free, (wt - 1) & 1, st)) { ok = false; break; }
+        if (Parts<LAYOUT>::kApart && !warp_wait(&sm.vfull[b], (i / NB) & 1, st)) { ok = false; break; }
         if (!warp_wait(&sm.p_ready[sb], (i >> 1) & 1, st)) { ok = false; break; }
-        tc::fence_after();
         const uint32_t ta = smem_u32(sm.tiles[b]);
+        const int key0 = w.k0 + j * KN;
+        if (key0 + KN > w.k1) {
+          // V rows behind the last key (K rows there only made logits that were
+          // masked): zero weights must meet finite values
+          for (int k = max(w.k1 - key0, 0); k < KN; ++k)
+            for (int cb = lane; cb < Parts<LAYOUT>::kV; cb += 32)
+              zero16(ta + ((k >> 3) * T::kBlk + Parts<LAYOUT>::v0(w.half) + cb) * 128 + (k & 7) * 16);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc::fence_after();
         const uint64_t dv =
             tc::smem_desc(ta + (T::kVcb + (kE4 ? 16 : 32) * w.half) * 128, T::kBlk * 128, 128);
         const uint32_t p = tmem + kColS + KN * sb;
@@ -336,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
             tc::mma_bf16_ts_warp(tmem + kColO, p + 8 * kk, dv + ((kk * 2 * T::kBlk * 128) >> 4), id_o,
                                  !(j == 0 && kk == 0));
         }
-        tc::commit_warp(&sm.empty[b]);
+        tc::commit_warp(Parts<LAYOUT>::kApart ? &sm.vempty[b] : &sm.kempty[b]);
         tc::commit_warp(&sm.pfree[sb]);
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }

@@ -657,11 +657,10 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
   const int per = 128 / group, copies = local ? pool->kv_heads : 2;
   const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff,
                                      local ? kTreeLocalTiles : kTreeGlobalTiles);
-  // the most units of a sequence, over its rows n: blocks x chunks, of which
-  // there are at most kTreeMaxChunks unless a block has one chunk
+  // the most units of a sequence, over its rows n
   int64_t units = 0;
   for (int n = 1; n <= max_q_rows; ++n) {
-    const int blocks = ceil_div(n, per), most = blocks < kTreeMaxChunks ? kTreeMaxChunks / blocks : 1;
+    const int blocks = ceil_div(n, per), most = tree_most_chunks(blocks);
     const int64_t u = static_cast<int64_t>(blocks) * (chunks < most ? chunks : most);
     if (u > units) units = u;
   }

@@ -104,7 +104,7 @@ def test_attn_unsupported_workspace_and_empty():
 
 
 def _chunks(tiles, aim, blocks):
-    chunks = min(-(-tiles // aim), max(1, 38 // blocks))
+    chunks = min(-(-tiles // aim), 38, max(1, 76 // blocks))
     return -(-tiles // -(-tiles // chunks))
 
 

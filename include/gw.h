@@ -641,7 +641,7 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  * the sequence's rows of that KV head, as zero weights multiply it.
  * The chunks of a sequence depend on its length, rows and window only: a row is
  * bit-identical whatever else is in the batch.
- * bf16 and e4m3 pools.  batch at most 512.
+ * bf16 and e4m3 pools.  batch at most 256.
  * Errors: those of gw_decode_attn_local; GW_ERR_INVALID_ARG (tree_mask or pos
  * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^27 or
  * more).

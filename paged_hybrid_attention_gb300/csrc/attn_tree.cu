@@ -45,8 +45,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   const int copy = task % copies;  // KV head or half
   const int s = task / copies;
   const int row0 = a.cu_q_rows[s], n = a.cu_q_rows[s + 1] - row0, L = a.seq_lens[s];
-  const int ub = a.unit_base[s], units = a.unit_base[s + 1] - ub;
-  if (units == 0) return;
+  const int ub = a.unit_base[s];
+  if (ub < 0) return;
   const TreeSpan sp = tree_span(L, n, a.window, group, kLocal ? kTreeLocalTiles : kTreeGlobalTiles);
   const int nc = sp.chunks();
   if (nc == 1 || qb >= sp.blocks) return;  // the attention kernel has written it

@@ -113,7 +113,7 @@ struct TSmem {
   uint32_t tmem_base;
   float stat_inv[kM];  // 1 / l of each row
   float scale[T::kE4 ? kRowRing : 1][T::kE4 ? kM : 1];  // e4m3: 2^-e of each row's scaling
-  int32_t ub[kMaxTreeBatch + 1 + 32];
+  TreePlan plan;
 };
 static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FOLDED>) <= 232448, "shared memory of one CTA");
 static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FULL>) <= 232448, "shared memory of one CTA");
@@ -156,17 +156,18 @@ struct Unit {
 // Unit u: (chunk, row block, half), so that the units that read the same pages
 // run at the same time.
 template <int HQ, int KN>
-__device__ __forceinline__ Unit unit_of(const LocalArgs& a, const int32_t* ub, int u) {
+__device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan, int u) {
   constexpr int QB = kM / HQ;
   Unit w;
-  w.s = plan_seq(ub, a.batch, u);
+  const int at = plan_seq(plan.ub, a.batch, u);
+  w.s = plan.seq[at];
   w.row0 = a.cu_q_rows[w.s];
   w.n = a.cu_q_rows[w.s + 1] - w.row0;
   const int L = a.seq_lens[w.s];
   w.base = L - w.n;
   const TreeSpan sp = tree_span(L, w.n, a.window, HQ, kTreeGlobalTiles);
   w.nc = sp.chunks();
-  const int r = u - ub[w.s];
+  const int r = u - plan.ub[at];
   w.half = r & 1;
   const int cb = r >> 1, c = cb / sp.blocks;
   w.q0 = (cb - c * sp.blocks) * QB;
@@ -215,8 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   }
   pdl_wait();
   pdl_trigger();
-  plan_tree(a, sm.ub, sm.ub + kMaxTreeBatch + 1, 2, HQ, kTreeGlobalTiles, 512);
-  const int total = sm.ub[a.batch];
+  plan_tree(a, sm.plan, 2, HQ, kTreeGlobalTiles, 512);
+  const int total = sm.plan.ub[a.batch];
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -234,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     const int page = lane >> 1, tb = lane & 1;
     uint32_t gi = 0, halves = 0;  // bit b: the half of buffer b's last tile
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok && (PT::kApart || !is_v); u += gridDim.x) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+    int wt = 0;
+    for (int u = tree_unit(0); u < total && ok && (PT::kApart || !is_v); u = tree_unit(++wt)) {
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, u);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
       const uint32_t bytes = 128 * (is_v ? PT::kV : w.half ? PT::rest(1) : PT::rest(0));  // of an 8-token block
       for (int t = 0; t < w.nt; ++t, ++gi) {
@@ -293,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     uint32_t i = 0;
     int wt = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, u);
       if (!warp_wait(&sm.q_full, wt & 1, st)) break;
       for (int j = 0; j < w.nt; ++j, ++i) {
         const int b = i % NB, sb = i & 1;
@@ -362,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     uint32_t i = 0;
     int wt = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, u);
       for (int j = 0; j < w.nt; ++j, ++i) {
         const int b = i % NB, sb = i & 1;
         if (j == 0 && wt >= 1 && !warp_wait(&sm.o_free, (wt - 1) & 1, st)) { ok = false; break; }
@@ -414,13 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     uint32_t gi = 0;
     int wt = 0;
     TreeRow next_row{0, 0x7fffffff, 1.f};
-    if (static_cast<int>(blockIdx.x) < total) next_row = row_of(unit_of<HQ, KN>(a, sm.ub, blockIdx.x));
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
+    if (static_cast<int>(blockIdx.x) < total) next_row = row_of(unit_of<HQ, KN>(a, sm.plan, blockIdx.x));
+    for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, u);
       const bool row_ok = qi < w.nq;
       const TreeRow row = next_row;
-      const int next = u + gridDim.x;
-      if (next < total) next_row = row_of(unit_of<HQ, KN>(a, sm.ub, next));  // in flight over this unit
+      const int next = tree_unit(wt + 1);
+      if (next < total) next_row = row_of(unit_of<HQ, KN>(a, sm.plan, next));  // in flight over this unit
       float sc = a.scale_log2;
       float m_ref = -INFINITY;
       float lp[4] = {0.f, 0.f, 0.f, 0.f};
@@ -633,16 +635,16 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
       mbar_arrive(&sm.q_full);
     };
     if (static_cast<int>(blockIdx.x) < total) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, blockIdx.x);
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, blockIdx.x);
       load_q(w, 0);
       store_q(w);
     }
     int wt = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<HQ, KN>(a, sm.ub, u);
-      const int next = u + gridDim.x;
+    for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
+      const Unit w = unit_of<HQ, KN>(a, sm.plan, u);
+      const int next = tree_unit(wt + 1);
       if (next < total) {
-        const Unit wn = unit_of<HQ, KN>(a, sm.ub, next);
+        const Unit wn = unit_of<HQ, KN>(a, sm.plan, next);
         load_q(wn, wt + 1);
         if (!warp_wait(&sm.q_free, wt & 1, st)) break;
         tc::fence_after();

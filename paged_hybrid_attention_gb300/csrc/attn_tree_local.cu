@@ -64,7 +64,7 @@ struct LSmem {
   uint64_t q_full, q_free, o_done, o_free;
   int32_t kmask[kStages], vmask[kStages];  // pages of the tile that were loaded
   uint32_t tmem_base;
-  int32_t ub[kMaxTreeBatch + 1 + 32];
+  TreePlan plan;
 };
 static_assert(sizeof(LSmem<GW_KV_BF16>) <= 232448, "shared memory of one CTA");
 
@@ -104,17 +104,18 @@ struct Unit {
 // Unit u.  Row blocks of a chunk are neighbours, so that its K and V come from
 // L2 for all but the first.
 template <int G>
-__device__ __forceinline__ Unit unit_of(const LocalArgs& a, const int32_t* ub, int u) {
+__device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan, int u) {
   constexpr int BQ = kM / G;
   Unit w;
-  w.s = plan_seq(ub, a.batch, u);
+  const int at = plan_seq(plan.ub, a.batch, u);
+  w.s = plan.seq[at];
   w.row0 = a.cu_q_rows[w.s];
   w.n = a.cu_q_rows[w.s + 1] - w.row0;
   const int L = a.seq_lens[w.s];
   w.base = L - w.n;
   const TreeSpan sp = tree_span(L, w.n, a.window, G, kTreeLocalTiles);
   w.nc = sp.chunks();
-  const int r = u - ub[w.s], gc = r / sp.blocks, c = gc % w.nc;
+  const int r = u - plan.ub[at], gc = r / sp.blocks, c = gc % w.nc;
   w.g = gc / w.nc;
   w.q0 = (r - gc * sp.blocks) * BQ;
   w.rows = min(BQ, w.n - w.q0) * G;
@@ -276,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  plan_tree(a, sm.ub, sm.ub + kMaxTreeBatch + 1, a.kv_heads, G, kTreeLocalTiles, 256);
-  const int total = sm.ub[a.batch];
+  plan_tree(a, sm.plan, a.kv_heads, G, kTreeLocalTiles, 256);
+  const int total = sm.plan.ub[a.batch];
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -292,8 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int j = lane / kC, c = lane % kC;
     uint32_t gi = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x) {
-      const Unit w = unit_of<G>(a, sm.ub, u);
+    int wt = 0;
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<G>(a, sm.plan, u);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
       for (int t = 0; t < w.nt; ++t, ++gi) {
         const int b = gi % kStages;
@@ -331,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<G>(a, sm.ub, u);
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<G>(a, sm.plan, u);
       if (!warp_wait(&sm.q_full, wt & 1, st)) break;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % kStages, sb = gi & 1;
@@ -369,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<G>(a, sm.ub, u);
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<G>(a, sm.plan, u);
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % kStages, sb = gi & 1;
         if (j == 0 && wt >= 1 && !warp_wait(&sm.o_free, (wt - 1) & 1, st)) { ok = false; break; }
@@ -414,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < total && ok; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<G>(a, sm.ub, u);
+    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+      const Unit w = unit_of<G>(a, sm.plan, u);
       const int share = tid / (kM / w.copies);
       // a warp none of whose lanes has a row leaves P as it is: rows do not mix
       const bool idle = row_of(w, 32 * warp) >= w.rows;
@@ -534,15 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sm.q_full);
     };
     if (static_cast<int>(blockIdx.x) < total) {
-      load_q(unit_of<G>(a, sm.ub, blockIdx.x));
+      load_q(unit_of<G>(a, sm.plan, blockIdx.x));
       store_q(0);
     }
     int wt = 0;
-    for (int u = blockIdx.x; u < total; u += gridDim.x, ++wt) {
-      const Unit w = unit_of<G>(a, sm.ub, u);
-      const int next = u + gridDim.x;
+    for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
+      const Unit w = unit_of<G>(a, sm.plan, u);
+      const int next = tree_unit(wt + 1);
       if (next < total) {
-        load_q(unit_of<G>(a, sm.ub, next));
+        load_q(unit_of<G>(a, sm.plan, next));
         if (!warp_wait(&sm.q_free, wt & 1, st)) break;
         tc::fence_after();
         store_q(wt + 1);

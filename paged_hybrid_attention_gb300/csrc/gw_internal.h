@@ -63,7 +63,7 @@ __host__ __device__ __forceinline__ int global_chunks(int L) {
 // 128 rows, chunk of key tiles); a tile is 64 tokens, aligned to 64.  Chunks
 // depend on the sequence's own length, rows and window only, as the decode's.
 constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask word
-constexpr int kMaxTreeBatch = 512;  // sequences of a call: their plan is in shared memory
+constexpr int kMaxTreeBatch = 256;  // sequences of a call: their plan is in shared memory
 constexpr int kTreeTile = 64;
 constexpr int kTreeMaxChunks = 38;
 
@@ -114,7 +114,7 @@ __host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_r
 }
 // Tiles of a chunk, at most (attn_tree_local.cu, attn_tree_global.cu).
 constexpr int kTreeLocalTiles = 18;
-constexpr int kTreeGlobalTiles = 24;
+constexpr int kTreeGlobalTiles = 32;
 
 // Workspace layout (offsets from the 256-byte aligned workspace base):
 //   [0, 256)          reserved

@@ -184,7 +184,7 @@ def test_bad_metadata(layout, kv, window):
 
 
 def test_max_batch_and_idle_slots():
-    plan = [((b * 37) % 150 + 5, b % 4) for b in range(512)]
+    plan = [((b * 37) % 150 + 5, b % 4) for b in range(256)]
     for layout, kv, window in (("local", 1, 40), ("folded", 1, 0)):
         c = Case(layout, plan, 8, kv, window=window, seed=12)
         c.run()

@@ -90,7 +90,7 @@ def test_global_refuses(bad):
 def test_attn_unsupported_workspace_and_empty():
     assert _local(hq=12) == gw.GW_ERR_UNSUPPORTED and _local(hq=64) == gw.GW_ERR_UNSUPPORTED
     assert _global(hq=12) == gw.GW_ERR_UNSUPPORTED and _global(hq=64) == gw.GW_ERR_UNSUPPORTED
-    assert _local(batch=513) == gw.GW_ERR_UNSUPPORTED and _global(batch=513) == gw.GW_ERR_UNSUPPORTED
+    assert _local(batch=257) == gw.GW_ERR_UNSUPPORTED and _global(batch=257) == gw.GW_ERR_UNSUPPORTED
     assert _global(desc=_desc(FOLDED, gw.KV_E4M3)) == gw.GW_ERR_UNSUPPORTED
     assert _local(batch=0, q=0, out=0, cu=0, mask=0, ws=0) == gw.GW_OK
     assert _global(batch=0, q=0, out=0, cu=0, mask=0, ws=0) == gw.GW_OK
@@ -115,7 +115,7 @@ def _chunks(tiles, aim, blocks):
 def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
     """No mix of rows and lengths up to the bounds needs more units than the workspace holds."""
     local = layout == gw.LAYOUT_LOCAL
-    group, copies, aim = (heads // kvh, kvh, 18) if local else (heads, 2, 24)
+    group, copies, aim = (heads // kvh, kvh, 18) if local else (heads, 2, 32)
     got = gw.lib().gw_tree_workspace_bytes(ctypes.byref(_desc(layout, kvh=kvh, base=0)), heads, 3, pages, rows, window)
     cap = group * min(128 // group, rows)
     worst = 0
@@ -136,10 +136,10 @@ def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
 def test_workspace_refuses():
     size = gw.lib().gw_tree_workspace_bytes
     for args in ((0, 2, 64, 16, 32), (8, -1, 64, 16, 32), (8, 2, 0, 16, 32), (8, 2, 1 << 27, 16, 32),
-                 (8, 2, 64, 0, 32), (8, 2, 64, 65, 32), (8, 2, 64, 16, 0), (12, 2, 64, 16, 32), (8, 513, 64, 16, 32)):
+                 (8, 2, 64, 0, 32), (8, 2, 64, 65, 32), (8, 2, 64, 16, 0), (12, 2, 64, 16, 32), (8, 257, 64, 16, 32)):
         assert size(ctypes.byref(_desc()), *args) == 0
         assert gw.last_error().startswith("gw_tree_workspace_bytes:")
-    assert size(ctypes.byref(_desc(FOLDED)), 32, 512, 8192, 64, 0) > 1 << 32
+    assert size(ctypes.byref(_desc(FOLDED)), 32, 256, 8192, 64, 0) > 1 << 32
 
 
 # ---- gw_tree_accept, gw_kv_tree_move ----------------------------------------------

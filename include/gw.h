@@ -639,8 +639,8 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  * [0, num_pages) counts as zeros (GW_DEV_PAGE_RANGE).  An infinity or NaN in
  * the V row of any token from max(0, base - window + 1) to seq_lens[b] reaches
  * the sequence's rows of that KV head, as zero weights multiply it.
- * The chunks of a sequence depend on its length, rows and window only: a row is
- * bit-identical whatever else is in the batch.
+ * A row is bit-identical whatever else is in the batch (for the same window and
+ * max_q_rows).
  * bf16 and e4m3 pools.  batch at most 256.
  * Errors: those of gw_decode_attn_local; GW_ERR_INVALID_ARG (tree_mask or pos
  * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^27 or

@@ -165,7 +165,7 @@ __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan
   w.n = a.cu_q_rows[w.s + 1] - w.row0;
   const int L = a.seq_lens[w.s];
   w.base = L - w.n;
-  const TreeSpan sp = tree_span(L, w.n, a.window, HQ, kTreeGlobalTiles);
+  const TreeSpan sp = tree_span(L, w.n, a.window, QB, kTreeGlobalTiles);
   w.nc = sp.chunks();
   const int r = u - plan.ub[at];
   w.half = r & 1;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   }
   pdl_wait();
   pdl_trigger();
-  plan_tree(a, sm.plan, 2, HQ, kTreeGlobalTiles, 512);
+  plan_tree(a, sm.plan, 2, kM / HQ, kTreeGlobalTiles, 512);
   const int total = sm.plan.ub[a.batch];
   tc::fence_before();
   __syncthreads();
@@ -495,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(__uint_as_float(sv[4 * v + i]), sc, neg_m));
             uint32_t w3[3];
-            lp[v & 3] += tc::split_e5m2(p[0], p[1], p[2], p[3], w3);
+            float held[4];
+            tc::split_e5m2(p[0], p[1], p[2], p[3], w3, held);
+            lp[v & 3] += (held[0] + held[1]) + (held[2] + held[3]);
             pw[v] = w3[0];
             pw[16 + v] = w3[1];
             pl[v] = w3[2];

@@ -654,7 +654,7 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
                               int window) {
   const bool local = pool->layout == GW_LAYOUT_LOCAL;
   const int group = local ? num_q_heads / pool->kv_heads : num_q_heads;
-  const int per = 128 / group, copies = local ? pool->kv_heads : 2;
+  const int per = kTreeRows / group, copies = local ? pool->kv_heads : 2;
   const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff,
                                      local ? kTreeLocalTiles : kTreeGlobalTiles);
   // the most units of a sequence, over its rows n

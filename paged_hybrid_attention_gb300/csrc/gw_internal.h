@@ -59,12 +59,14 @@ __host__ __device__ __forceinline__ int global_chunks(int L) {
 }
 
 // ---- drafted trees (gw_tree_attn_*) ------------------------------------------
-// A work unit is (sequence, KV head or half of the output dims, block of
-// 128 rows, chunk of key tiles); a tile is 64 tokens, aligned to 64.  Chunks
+// A work unit is (sequence, KV head or half of the output dims, block of rows
+// with the heads that share their K and V, chunk of key tiles); a tile is 64 tokens, aligned to 64.  Chunks
 // depend on the sequence's own length, rows and window only, as the decode's.
 constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask word
 constexpr int kMaxTreeBatch = 256;  // sequences of a call: their plan is in shared memory
 constexpr int kTreeTile = 64;
+constexpr int kTreeRows = 128;     // rows x heads of a block
+constexpr int kTreeFewRows = 32;   // rows x heads up to which attn_tree_local.cu serves a call
 constexpr int kTreeMaxChunks = 38;
 
 // Chunks of a sequence at most: units enough for the GPU's 152 SMs (a chunk has a
@@ -87,19 +89,18 @@ __host__ __device__ __forceinline__ int tree_chunk_tiles(int tiles, int aim, int
 struct TreeSpan {
   int first;   // first tile
   int tiles;   // tiles [first, first + tiles)
-  int blocks;  // blocks of 128 rows
+  int blocks;  // blocks of rows
   int ct;      // tiles of a chunk
   __host__ __device__ int chunks() const { return (tiles - 1) / ct + 1; }
 };
 
-// Of n rows over L >= n >= 1 tokens: `group` heads share a tile's rows.  Rows
+// Of n rows over L >= n >= 1 tokens, `per` of them in a block.  Rows
 // sit at tokens L - n and later, so the first key of any is L - n - window + 1.
-__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int group, int aim) {
+__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int per, int aim) {
   TreeSpan s;
   const int lo = L - n - window + 1;
   s.first = lo > 0 ? lo / kTreeTile : 0;
   s.tiles = (L - 1) / kTreeTile - s.first + 1;
-  const int per = 128 / group;
   s.blocks = (n + per - 1) / per;
   s.ct = tree_chunk_tiles(s.tiles, aim, s.blocks);
   return s;
@@ -112,7 +113,7 @@ __host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_r
   const int64_t c = ((all < seen ? all : seen) + aim - 1) / aim;
   return static_cast<int>(c < kTreeMaxChunks ? c : kTreeMaxChunks);
 }
-// Tiles of a chunk, at most (attn_tree_local.cu, attn_tree_global.cu).
+// Tiles of a chunk, at most (attn_tree_local*.cu, attn_tree_global.cu).
 constexpr int kTreeLocalTiles = 18;
 constexpr int kTreeGlobalTiles = 32;
 
@@ -331,7 +332,8 @@ struct TreeAcceptArgs {
 // sequences that have several
 cudaError_t launch_local_tree(int dtype, int group, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_global_tree(int layout, const LocalArgs& a, cudaStream_t st);
-cudaError_t launch_local_tree_tc(int dtype, int group, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_local_tree_few(int dtype, int group, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_local_tree_rows(int dtype, int group, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_global_tree_tc(int layout, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st);
 // gw_kv_tree_move

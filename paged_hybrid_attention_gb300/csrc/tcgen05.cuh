@@ -54,9 +54,9 @@ __host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N, bool a_mn_m
 // e5m2 number is the upper byte of an fp16 one, so the weights, rounded to fp16,
 // are cut by masks and exact differences into terms of three bits, 2^-9 of a
 // weight in all.  Weights of up to 2^15 are in range, down to 2^-16, where two
-// e4m3 terms would end at 2^-10 and lose a long tail.  Returns the sum of the
-// weights as the terms hold them.
-__device__ __forceinline__ float split_e5m2(float p0, float p1, float p2, float p3, uint32_t (&w)[3]) {
+// e4m3 terms would end at 2^-10 and lose a long tail.  `held`: the weights as the
+// terms hold them.
+__device__ __forceinline__ void split_e5m2(float p0, float p1, float p2, float p3, uint32_t (&w)[3], float (&held)[4]) {
   __half2 x[2] = {__floats2half2_rn(p0, p1), __floats2half2_rn(p2, p3)};
   __half2 used[2];
 #pragma unroll
@@ -72,7 +72,7 @@ __device__ __forceinline__ float split_e5m2(float p0, float p1, float p2, float 
     x[1] = __hsub2(x[1], t1);
   }
   const float2 u0 = __half22float2(used[0]), u1 = __half22float2(used[1]);
-  return (u0.x + u0.y) + (u1.x + u1.y);
+  held[0] = u0.x, held[1] = u0.y, held[2] = u1.x, held[3] = u1.y;
 }
 
 __device__ __forceinline__ void alloc(uint32_t* smem_dst, uint32_t ncols) {

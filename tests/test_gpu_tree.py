@@ -14,18 +14,26 @@ pytestmark = pytest.mark.gpu
 EDGES = [(1, 1), (5, 5), (16, 3), (17, 17), (0, 0), (64, 64), (65, 1), (63, 5), (81, 64), (257, 2), (300, 33), (128, 16)]
 
 
+def at_most(plan, rows):
+    return [(L, min(n, rows)) for L, n in plan]
+
+
+# rows x heads of a KV head: up to 16, up to 32, more
+@pytest.mark.parametrize("most", [16, 32, 512])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,kv", [(4, 4), (8, 4), (8, 2), (16, 2), (1, 1), (8, 1)])
-def test_local_edges(heads, kv, dtype):
-    c = Case("local", EDGES, heads, kv, dtype, window=64, seed=heads * 10 + kv)
+def test_local_edges(heads, kv, dtype, most):
+    c = Case("local", at_most(EDGES, most * kv // heads), heads, kv, dtype, window=64, seed=heads * 10 + kv)
     c.run()
     c.check()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window", [1, 2, 5, 17, 64, 100, 1024, 2 ** 31 - 1])
-def test_local_windows(window, dtype):
-    c = Case("local", [(40, 9), (700, 20), (1300, 64), (64, 64), (130, 2)], 4, 2, dtype, window=window, seed=window % 97)
+@pytest.mark.parametrize("rows", [8, 16, 64])
+def test_local_windows(window, dtype, rows):
+    plan = at_most([(40, 9), (700, 20), (1300, 64), (64, 64), (130, 2)], rows)
+    c = Case("local", plan, 4, 2, dtype, window=window, seed=window % 97)
     c.run()
     c.check()
 
@@ -38,11 +46,12 @@ def test_global_edges(layout, heads):
     c.check()
 
 
-@pytest.mark.parametrize("layout", ["local", "folded", "full", "folded_e4m3"])
-def test_any_words(layout):
+@pytest.mark.parametrize("layout,rows", [("local", 4), ("local", 8), ("local", 64), ("folded", 64), ("full", 64),
+                                         ("folded_e4m3", 64)])
+def test_any_words(layout, rows):
     """Words that are no trees, rows that see no draft, and sequences without a cache before them."""
-    c = Case(layout, [(7, 7), (64, 64), (200, 30), (33, 1), (1, 1), (1100, 5)], 8, 2 if layout == "local" else 1,
-             window=90 if layout == "local" else 0, sees="any", seed=5)
+    c = Case(layout, at_most([(7, 7), (64, 64), (200, 30), (33, 1), (1, 1), (1100, 5)], rows), 8,
+             2 if layout == "local" else 1, window=90 if layout == "local" else 0, sees="any", seed=5)
     c.sees[4][:] = False
     c.mask[c.cu[4]] = 0
     c.run()
@@ -59,21 +68,23 @@ def test_global_chunks(layout, heads, n):
     c.check()
 
 
-@pytest.mark.parametrize("layout,dtype", [("local", "bf16"), ("local", "e4m3"), ("folded", "bf16"), ("folded_e4m3", "")])
-def test_doubled_chunks(layout, dtype):
-    """Sequences long enough that chunks double, whose rows share many blocks."""
-    L = 20000 if layout == "local" else 36000
-    c = Case(layout, [(L, 2), (9000, 40)], 8, 1, dtype or "bf16", window=L if layout == "local" else 0, seed=3)
+@pytest.mark.parametrize("layout,dtype,rows", [("local", "bf16", 40), ("local", "bf16", 4), ("local", "e4m3", 40),
+                                               ("local", "e4m3", 4), ("folded", "bf16", 40), ("folded_e4m3", "", 40)])
+def test_long_chunks(layout, dtype, rows):
+    """Sequences with as many chunks as there may be, and longer ones; rows in many blocks."""
+    L = 46000 if layout == "local" else 80000
+    c = Case(layout, [(L, 2), (9000, rows)], 8, 1, dtype or "bf16", window=L if layout == "local" else 0, seed=3)
     c.run()
     c.check()
 
 
 @pytest.mark.parametrize("layout,dtype", [("local", "bf16"), ("local", "e4m3"), ("folded", "bf16"), ("full", "bf16"),
                                           ("folded_e4m3", "")])
-def test_sharp_logits(layout, dtype):
+@pytest.mark.parametrize("rows", [2, 4, 10])
+def test_sharp_logits(layout, dtype, rows):
     """Logits of standard deviation 30: references rise and rows are rescaled."""
-    c = Case(layout, [(600, 10), (1500, 3)], 8, 1, dtype or "bf16", window=1500 if layout == "local" else 0, seed=8,
-             q_sigma=30.0)
+    c = Case(layout, at_most([(600, 10), (1500, 3)], rows), 8, 1, dtype or "bf16",
+             window=1500 if layout == "local" else 0, seed=8, q_sigma=30.0)
     c.run()
     assert int(c.status.item()) == 0
     for b in range(2):
@@ -85,10 +96,11 @@ def test_sharp_logits(layout, dtype):
 
 
 @pytest.mark.parametrize("layout,dtype", [("local", "e4m3"), ("folded_e4m3", ""), ("local", "bf16"), ("folded", "bf16")])
-def test_long_tail(layout, dtype):
+@pytest.mark.parametrize("n", [2, 4, 9])
+def test_long_tail(layout, dtype, n):
     """One token 2^11.5 above each of 1100 others: their weights together are a third of its own, and one
     by one below the smallest e4m3 number."""
-    L, n = 1100, 2
+    L = 1100
     c = Case(layout, [(L, n)], 8, 1, dtype or "bf16", window=L if layout == "local" else 0, seed=4, sigma=0.5)
     first = c.cells.float()
     # K: one direction, 2 for token 100 and 0 elsewhere, so that its logit is 8 (base e) and theirs 0
@@ -126,15 +138,16 @@ def test_decode_rows_agree():
         assert (got - out.float()).norm() <= 2.0 ** -7 * out.float().norm()
 
 
+@pytest.mark.parametrize("plan", [[(700, 6), (1300, 17), (90, 33)], [(700, 6), (1300, 8), (90, 1)]])
 @pytest.mark.parametrize("layout,kv,window", [("local", 2, 300), ("folded", 1, 0), ("folded_e4m3", 1, 0)])
-def test_rows_do_not_depend_on_the_batch(layout, kv, window):
-    plan = [(700, 6), (1300, 17), (90, 33)]
+def test_rows_do_not_depend_on_the_batch(layout, kv, window, plan):
     c = Case(layout, plan, 8, kv, window=window, seed=6)
+    most = max(n for _, n in plan)
     whole = c.run().clone()
     for cap in (1, 7, 0):
         gw.set_max_ctas(cap)
         try:
-            assert torch.equal(c.run(max_q_rows=64), whole)
+            assert torch.equal(c.run(max_q_rows=64 if most > 8 else 8), whole)
         finally:
             gw.set_max_ctas(0)
     for b in range(3):
@@ -143,13 +156,13 @@ def test_rows_do_not_depend_on_the_batch(layout, kv, window):
         i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
         n = plan[b][1]
         table = i32(c.table[b:b + 1].tolist())
-        ws = gw.alloc_workspace_tree(c.pool, 8, 1, table.shape[1], n, window or 1)
+        ws = gw.alloc_workspace_tree(c.pool, 8, 1, table.shape[1], most, window or 1)
         mask = torch.from_numpy(c.mask[rows]).cuda()
         if layout == "local":
             gw.tree_attn_local(c.pool, q, out, i32([0, n]), i32([plan[b][0]]), table, mask, i32(c.pos[rows].tolist()),
-                               ws, window, max_q_rows=n)
+                               ws, window, max_q_rows=most)
         else:
-            gw.tree_attn_global(c.pool, q, out, i32([0, n]), i32([plan[b][0]]), table, mask, ws, max_q_rows=n)
+            gw.tree_attn_global(c.pool, q, out, i32([0, n]), i32([plan[b][0]]), table, mask, ws, max_q_rows=most)
         assert torch.equal(out, whole[rows])
 
 

@@ -117,10 +117,11 @@ def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
     local = layout == gw.LAYOUT_LOCAL
     group, copies, aim = (heads // kvh, kvh, 18) if local else (heads, 2, 32)
     got = gw.lib().gw_tree_workspace_bytes(ctypes.byref(_desc(layout, kvh=kvh, base=0)), heads, 3, pages, rows, window)
-    cap = group * min(128 // group, rows)
+    per = 128 // group
+    cap = group * min(per, rows)
     worst = 0
     for n in range(1, rows + 1):
-        blocks = -(-n // (128 // group))
+        blocks = -(-n // per)
         lens = {min(pages * 16, max(n, x)) for e in range(1, 18) for x in
                 (n, (1 << e) - 1, 1 << e, (1 << e) + 1, 3 << e, window + n, window + n + 63, pages * 16)}
         for L in lens:

@@ -28,8 +28,7 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
 
 template <bool kLocal>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const LocalArgs a, int group, int copies,
-                                                                      int blocks) {
-  const int per = kTreeRows / group;
+                                                                      int blocks, const TreeRule rule, int scale) {
   __shared__ float w[kTreeMaxChunks][32];
   __shared__ float top[kMergeWarps][32], inv_sum[32];
   pdl_wait();
@@ -46,12 +45,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   const int copy = task % copies;  // KV head or half
   const int s = task / copies;
   const int row0 = a.cu_q_rows[s], n = a.cu_q_rows[s + 1] - row0, L = a.seq_lens[s];
-  const int ub = a.unit_base[s];
+  const int64_t ub = static_cast<int64_t>(a.unit_base[s]) * scale;  // `scale` parts a unit
   if (ub < 0) return;
-  const TreeSpan sp = tree_span(L, n, a.window, per, kLocal ? kTreeLocalTiles : kTreeGlobalTiles);
+  const TreeSpan sp = tree_span(L, n, a.window, rule);
   const int nc = sp.chunks();
   if (nc == 1 || qb >= sp.blocks) return;  // the attention kernel has written it
-  const int place = pg * 32 + lane, q = qb * per + place / group;
+  const int place = pg * 32 + lane, q = qb * rule.per + place / group;
   const bool ok = place < a.part_rows && q < n;
   const int64_t u0 = ub + (kLocal ? copy * nc * sp.blocks + qb : qb * 2 + copy);
   const int64_t step = (kLocal ? sp.blocks : 2 * sp.blocks) * static_cast<int64_t>(a.part_rows);
@@ -98,33 +97,38 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
 }
 
 template <bool kLocal>
-cudaError_t launch_merge(const LocalArgs& a, int group, cudaStream_t st) {
-  const int copies = kLocal ? a.kv_heads : 2, per = kTreeRows / group;
-  const int blocks = (a.max_q_rows + per - 1) / per;
-  const int64_t grid = static_cast<int64_t>(a.batch) * copies * blocks * ((a.part_rows + 31) / 32) * (32 / kMergeWarps);
+cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, int scale, cudaStream_t st) {
+  const int copies = kLocal ? a.kv_heads : 2, blocks = (a.max_q_rows + rule.per - 1) / rule.per;
+  const int64_t grid =
+      static_cast<int64_t>(a.batch) * copies * blocks * ((a.part_rows + 31) / 32) * (32 / kMergeWarps);
   return launch_pdl(tree_merge_kernel<kLocal>, dim3(static_cast<unsigned>(grid)), dim3(kMergeWarps * 32), 0, st, a,
-                    group, copies, blocks);
+                    group, copies, blocks, rule, scale);
 }
 
 }  // namespace
 
+// Up to 32 rows x heads lie along the products' N, more along M.  Local, 16
+// sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16: 16 drafts 49.8 us
+// (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows, 100.6); 61 e4m3
+// sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8 heads, 4 drafts
+// 264 us (along M 432).  The rule is the call's bound, so that a captured call stays
+// what it is.
+//
 // The merge is left out where the block table's width allows one chunk only.
 cudaError_t launch_local_tree(int dtype, int group, const LocalArgs& a, cudaStream_t st) {
-  // Up to 32 rows x heads lie along the products' N, more along M: 16 sequences of
-  // 512 to 8192 tokens, 16 KV heads of 2 heads, bf16: 16 drafts 49.8 us (along M
-  // 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows, 100.6); 61 e4m3 sequences,
-  // 7 drafts 91 us (150).  The rule is the call's bound, so that a captured call
-  // stays what it is.
+  const TreeRule rule = tree_rule_local(group);
   cudaError_t e = a.max_q_rows * group <= kTreeFewRows ? launch_local_tree_few(dtype, group, a, st)
                                                        : launch_local_tree_rows(dtype, group, a, st);
-  if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, kTreeLocalTiles) == 1) return e;
-  return launch_merge<true>(a, group, st);
+  if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, rule) == 1) return e;
+  return launch_merge<true>(a, group, rule, 1, st);
 }
 
 cudaError_t launch_global_tree(int layout, const LocalArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_global_tree_tc(layout, a, st);
-  if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, kTreeGlobalTiles) == 1) return e;
-  return launch_merge<false>(a, a.num_q_heads, st);
+  const bool few = a.max_q_rows * a.num_q_heads <= kTreeFewRows;
+  const TreeRule rule = few ? tree_rule_few(a.num_q_heads) : tree_rule_global(a.num_q_heads);
+  cudaError_t e = few ? launch_global_tree_few(layout, a, st) : launch_global_tree_rows(layout, a, st);
+  if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, rule) == 1) return e;
+  return launch_merge<false>(a, a.num_q_heads, rule, few ? 2 : 1, st);
 }
 
 }  // namespace gw

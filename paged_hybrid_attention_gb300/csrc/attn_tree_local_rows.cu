@@ -114,7 +114,7 @@ __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan
   w.n = a.cu_q_rows[w.s + 1] - w.row0;
   const int L = a.seq_lens[w.s];
   w.base = L - w.n;
-  const TreeSpan sp = tree_span(L, w.n, a.window, BQ, kTreeLocalTiles);
+  const TreeSpan sp = tree_span(L, w.n, a.window, tree_rule_local(G));
   w.nc = sp.chunks();
   const int r = u - plan.ub[at], gc = r / sp.blocks, c = gc % w.nc;
   w.g = gc / w.nc;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
   pdl_trigger();
-  plan_tree(a, sm.plan, a.kv_heads, kM / G, kTreeLocalTiles, 256);
+  plan_tree(a, sm.plan, a.kv_heads, tree_rule_local(G), 256);
   const int total = sm.plan.ub[a.batch];
   tc::fence_before();
   __syncthreads();

@@ -655,12 +655,13 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
   const bool local = pool->layout == GW_LAYOUT_LOCAL;
   const int group = local ? num_q_heads / pool->kv_heads : num_q_heads;
   const int per = kTreeRows / group, copies = local ? pool->kv_heads : 2;
-  const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff,
-                                     local ? kTreeLocalTiles : kTreeGlobalTiles);
+  const bool few = !local && max_q_rows * group <= kTreeFewRows;
+  const TreeRule rule = local ? tree_rule_local(group) : few ? tree_rule_few(group) : tree_rule_global(group);
+  const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff, rule);
   // the most units of a sequence, over its rows n
   int64_t units = 0;
   for (int n = 1; n <= max_q_rows; ++n) {
-    const int blocks = ceil_div(n, per), most = tree_most_chunks(blocks);
+    const int blocks = ceil_div(n, per), most = tree_most_chunks(rule, blocks);
     const int64_t u = static_cast<int64_t>(blocks) * (chunks < most ? chunks : most);
     if (u > units) units = u;
   }

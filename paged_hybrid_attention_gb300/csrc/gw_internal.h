@@ -60,62 +60,68 @@ __host__ __device__ __forceinline__ int global_chunks(int L) {
 
 // ---- drafted trees (gw_tree_attn_*) ------------------------------------------
 // A work unit is (sequence, KV head or half of the output dims, block of rows
-// with the heads that share their K and V, chunk of key tiles); a tile is 64 tokens, aligned to 64.  Chunks
-// depend on the sequence's own length, rows and window only, as the decode's.
+// with the heads that share their K and V, chunk of tiles); a tile is 64 tokens,
+// aligned to 64.  Chunks depend on the sequence's own length, rows and window
+// only (and the call's bound on rows), as the decode's.
 constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask word
 constexpr int kMaxTreeBatch = 256;  // sequences of a call: their plan is in shared memory
 constexpr int kTreeTile = 64;
-constexpr int kTreeRows = 128;     // rows x heads of a block
-constexpr int kTreeFewRows = 32;   // rows x heads up to which attn_tree_local.cu serves a call
-constexpr int kTreeMaxChunks = 38;
+constexpr int kTreeRows = 128;    // rows x heads of a block
+constexpr int kTreeFewRows = 32;  // rows x heads up to which a call's rows lie along N
+constexpr int kTreeMaxChunks = 76;
 
-// Chunks of a sequence at most: units enough for the GPU's 152 SMs (a chunk has a
-// unit per row block and KV head or half), few enough that their parts, 128 KB a
-// unit, stay small beside the cache (8 x 131072 tokens, one block: with 64 chunks
-// the merge takes 46 us instead of 30, the call 466 instead of 414).
-__host__ __device__ __forceinline__ int tree_most_chunks(int blocks) {
-  const int most = 2 * kTreeMaxChunks / blocks;
-  return most > kTreeMaxChunks ? kTreeMaxChunks : most > 1 ? most : 1;
-}
+// How a call is cut: `per` rows in a block, chunks of at most `aim` tiles, at most
+// `most` of them unless a block has one.
+struct TreeRule {
+  int per, aim, most;
+};
 
-// Tiles of a chunk: `tiles` tiles in even chunks of at most `aim`, or longer ones
-// where that would be more than tree_most_chunks of them.
-__host__ __device__ __forceinline__ int tree_chunk_tiles(int tiles, int aim, int blocks) {
-  const int most = tree_most_chunks(blocks);
-  const int want = (tiles - 1) / aim + 1, chunks = want < most ? want : most;
-  return (tiles - 1) / chunks + 1;
+// Local layers: a window of 1024 is one chunk (in two, 16 sequences with 16 drafts
+// take 61 us instead of 50, one sequence 18 instead of 21).
+__host__ __device__ constexpr TreeRule tree_rule_local(int group) { return {kTreeRows / group, 18, 38}; }
+// Global layers, rows along M: units (two a chunk and block) enough for the GPU's
+// 152 SMs, few enough that their parts, 128 KB a unit, stay small beside the cache
+// (8 x 131072 tokens, one block: with 64 chunks the merge took 46 us instead of 30,
+// the call 466 instead of 414).
+__host__ __device__ constexpr TreeRule tree_rule_global(int heads) { return {kTreeRows / heads, 32, 38}; }
+// Global layers, rows along N: one unit of 64 KB of parts a chunk.
+__host__ __device__ constexpr TreeRule tree_rule_few(int heads) { return {kTreeRows / heads, 8, kTreeMaxChunks}; }
+
+__host__ __device__ __forceinline__ int tree_most_chunks(const TreeRule& rule, int blocks) {
+  const int shared = kTreeMaxChunks / blocks;
+  const int most = shared < rule.most ? shared : rule.most;
+  return most > 1 ? most : 1;
 }
 
 struct TreeSpan {
   int first;   // first tile
   int tiles;   // tiles [first, first + tiles)
   int blocks;  // blocks of rows
-  int ct;      // tiles of a chunk
+  int ct;      // tiles of a chunk: even chunks
   __host__ __device__ int chunks() const { return (tiles - 1) / ct + 1; }
 };
 
-// Of n rows over L >= n >= 1 tokens, `per` of them in a block.  Rows
-// sit at tokens L - n and later, so the first key of any is L - n - window + 1.
-__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, int per, int aim) {
+// Of n rows over L >= n >= 1 tokens.  Rows sit at tokens L - n and later, so the
+// first key of any is L - n - window + 1.
+__host__ __device__ __forceinline__ TreeSpan tree_span(int L, int n, int window, const TreeRule& rule) {
   TreeSpan s;
   const int lo = L - n - window + 1;
   s.first = lo > 0 ? lo / kTreeTile : 0;
   s.tiles = (L - 1) / kTreeTile - s.first + 1;
-  s.blocks = (n + per - 1) / per;
-  s.ct = tree_chunk_tiles(s.tiles, aim, s.blocks);
+  s.blocks = (n + rule.per - 1) / rule.per;
+  const int most = tree_most_chunks(rule, s.blocks);
+  const int want = (s.tiles - 1) / rule.aim + 1, chunks = want < most ? want : most;
+  s.ct = (s.tiles - 1) / chunks + 1;
   return s;
 }
 // A bound on a sequence's chunks over L <= 16 * max_pages and n <= max_rows.
-__host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_rows, int window, int aim) {
+__host__ __device__ __forceinline__ int tree_max_chunks(int max_pages, int max_rows, int window, const TreeRule& rule) {
   // tokens in sight: all, or window - 1 cached ones and the drafts, in tiles they need not begin
   const int64_t all = (static_cast<int64_t>(max_pages) * 16 + kTreeTile - 1) / kTreeTile;
   const int64_t seen = (static_cast<int64_t>(window) + max_rows + kTreeTile - 3) / kTreeTile + 1;
-  const int64_t c = ((all < seen ? all : seen) + aim - 1) / aim;
-  return static_cast<int>(c < kTreeMaxChunks ? c : kTreeMaxChunks);
+  const int64_t c = ((all < seen ? all : seen) + rule.aim - 1) / rule.aim;
+  return static_cast<int>(c < rule.most ? c : rule.most);
 }
-// Tiles of a chunk, at most (attn_tree_local*.cu, attn_tree_global.cu).
-constexpr int kTreeLocalTiles = 18;
-constexpr int kTreeGlobalTiles = 32;
 
 // Workspace layout (offsets from the 256-byte aligned workspace base):
 //   [0, 256)          reserved
@@ -334,7 +340,8 @@ cudaError_t launch_local_tree(int dtype, int group, const LocalArgs& a, cudaStre
 cudaError_t launch_global_tree(int layout, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_local_tree_few(int dtype, int group, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_local_tree_rows(int dtype, int group, const LocalArgs& a, cudaStream_t st);
-cudaError_t launch_global_tree_tc(int layout, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_global_tree_few(int layout, const LocalArgs& a, cudaStream_t st);
+cudaError_t launch_global_tree_rows(int layout, const LocalArgs& a, cudaStream_t st);
 cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st);
 // gw_kv_tree_move
 struct TreeMoveArgs {

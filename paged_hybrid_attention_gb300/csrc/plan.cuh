@@ -88,14 +88,14 @@ struct TreePlan {
 };
 
 // A sequence's units are `copies` (KV heads, or halves of the output dims) x blocks
-// of `per` rows x chunks.  Sequences stand in the order of their chunks' lengths, the
+// of rows x chunks.  Sequences stand in the order of their chunks' lengths, the
 // longest first, and units are dealt in rounds that run to and fro (tree_unit), so
 // that CTAs get about the same (16 sequences of 512 to 8192 tokens, 16 drafts, a
 // global layer: 138 -> 126 us).  Sequences without rows have no units; nor have
 // those with more rows than max_q_rows, a length below their rows or beyond the
 // block table (GW_DEV_LEN_RANGE), whose output rows become zeros here.  CTA 0
 // stores each sequence's first unit (-1: none) for the merge.
-__device__ __forceinline__ void plan_tree(const LocalArgs& a, TreePlan& plan, int copies, int per, int aim,
+__device__ __forceinline__ void plan_tree(const LocalArgs& a, TreePlan& plan, int copies, const TreeRule& rule,
                                           int head_dim) {
   constexpr int kPer = 2;  // sequences of a thread: at least 128 threads
   const int t = threadIdx.x, nt = blockDim.x;
@@ -107,7 +107,7 @@ __device__ __forceinline__ void plan_tree(const LocalArgs& a, TreePlan& plan, in
     if (s >= a.batch) continue;
     const int n = a.cu_q_rows[s + 1] - a.cu_q_rows[s], L = a.seq_lens[s];
     if (n >= 1 && n <= a.max_q_rows && L >= n && plan_len_ok(a, L)) {
-      const TreeSpan sp = tree_span(L, n, a.window, per, aim);
+      const TreeSpan sp = tree_span(L, n, a.window, rule);
       tiles[i] = sp.ct;
       units[i] = copies * sp.blocks * sp.chunks();
     }

@@ -40,14 +40,15 @@ def test_local_windows(window, dtype, rows):
 
 @pytest.mark.parametrize("layout", ["folded", "full", "folded_e4m3"])
 @pytest.mark.parametrize("heads", [8, 16, 32])
-def test_global_edges(layout, heads):
-    c = Case(layout, EDGES, heads, seed=heads)
+@pytest.mark.parametrize("most", [32, 2048])
+def test_global_edges(layout, heads, most):
+    c = Case(layout, at_most(EDGES, most // heads), heads, seed=heads)
     c.run()
     c.check()
 
 
 @pytest.mark.parametrize("layout,rows", [("local", 4), ("local", 8), ("local", 64), ("folded", 64), ("full", 64),
-                                         ("folded_e4m3", 64)])
+                                         ("folded_e4m3", 64), ("folded", 4), ("full", 4), ("folded_e4m3", 4)])
 def test_any_words(layout, rows):
     """Words that are no trees, rows that see no draft, and sequences without a cache before them."""
     c = Case(layout, at_most([(7, 7), (64, 64), (200, 30), (33, 1), (1, 1), (1100, 5)], rows), 8,
@@ -60,7 +61,8 @@ def test_any_words(layout, rows):
 
 
 @pytest.mark.parametrize("layout,heads,n", [("folded", 32, 5), ("folded", 8, 17), ("full", 16, 9), ("folded_e4m3", 32, 4),
-                                            ("folded_e4m3", 8, 64)])
+                                            ("folded_e4m3", 8, 64), ("folded", 8, 4), ("folded", 32, 1),
+                                            ("full", 16, 2), ("folded_e4m3", 8, 3), ("folded_e4m3", 32, 1)])
 def test_global_chunks(layout, heads, n):
     """Several chunks, an odd last one among them."""
     c = Case(layout, [(511, n), (513, n), (2600, n), (1024 + n, n)], heads, seed=n)
@@ -69,7 +71,8 @@ def test_global_chunks(layout, heads, n):
 
 
 @pytest.mark.parametrize("layout,dtype,rows", [("local", "bf16", 40), ("local", "bf16", 4), ("local", "e4m3", 40),
-                                               ("local", "e4m3", 4), ("folded", "bf16", 40), ("folded_e4m3", "", 40)])
+                                               ("local", "e4m3", 4), ("folded", "bf16", 40), ("folded", "bf16", 3),
+                                               ("full", "bf16", 4), ("folded_e4m3", "", 40), ("folded_e4m3", "", 4)])
 def test_long_chunks(layout, dtype, rows):
     """Sequences with as many chunks as there may be, and longer ones; rows in many blocks."""
     L = 46000 if layout == "local" else 80000
@@ -138,7 +141,7 @@ def test_decode_rows_agree():
         assert (got - out.float()).norm() <= 2.0 ** -7 * out.float().norm()
 
 
-@pytest.mark.parametrize("plan", [[(700, 6), (1300, 17), (90, 33)], [(700, 6), (1300, 8), (90, 1)]])
+@pytest.mark.parametrize("plan", [[(700, 6), (1300, 17), (90, 33)], [(700, 6), (1300, 8), (90, 1)], [(700, 3), (1300, 4), (90, 1)]])
 @pytest.mark.parametrize("layout,kv,window", [("local", 2, 300), ("folded", 1, 0), ("folded_e4m3", 1, 0)])
 def test_rows_do_not_depend_on_the_batch(layout, kv, window, plan):
     c = Case(layout, plan, 8, kv, window=window, seed=6)
@@ -147,7 +150,7 @@ def test_rows_do_not_depend_on_the_batch(layout, kv, window, plan):
     for cap in (1, 7, 0):
         gw.set_max_ctas(cap)
         try:
-            assert torch.equal(c.run(max_q_rows=64 if most > 8 else 8), whole)
+            assert torch.equal(c.run(max_q_rows=64 if most > 8 else most), whole)
         finally:
             gw.set_max_ctas(0)
     for b in range(3):
@@ -167,9 +170,13 @@ def test_rows_do_not_depend_on_the_batch(layout, kv, window, plan):
 
 
 @pytest.mark.parametrize("layout,kv,window", [("local", 2, 64), ("folded", 1, 0), ("full", 1, 0), ("folded_e4m3", 1, 0)])
-def test_bad_metadata(layout, kv, window):
+@pytest.mark.parametrize("few", [False, True])
+def test_bad_metadata(layout, kv, window, few):
     """Sequences that are refused get zeros, pages out of range count as zeros; the others are as ever."""
-    c = Case(layout, [(100, 6), (40, 8), (200, 5), (30, 3)], 8, kv, window=window, seed=9)
+    heads = 8 if not few else kv
+    if few and layout != "local":
+        return bad_few(layout)
+    c = Case(layout, [(100, 6), (40, 8), (200, 5), (30, 3)], heads, kv, window=window, seed=9)
     good = c.run().clone()
     c.check()
     lens = c.lens.copy()
@@ -196,12 +203,25 @@ def test_bad_metadata(layout, kv, window):
         assert (out[15] == 0).all() and torch.equal(out[:14], good[:14])
 
 
+def bad_few(layout):
+    c = Case(layout, [(100, 3), (40, 4), (600, 2), (30, 1)], 8, seed=9)
+    good = c.run().clone()
+    c.check()
+    lens, table = c.lens.copy(), c.table.copy()
+    lens[1], lens[3], table[2, 20] = 3, c.table.shape[1] * 16 + 1, -1
+    out = c.run(lens=torch.from_numpy(lens).cuda(), table=torch.from_numpy(table).cuda())
+    assert int(c.status.item()) == gw.GW_DEV_LEN_RANGE | gw.GW_DEV_PAGE_RANGE
+    assert torch.equal(out[:3], good[:3]) and (out[3:7] == 0).all() and (out[9:] == 0).all()
+    assert torch.isfinite(out[7:9]).all() and not torch.equal(out[7:9], good[7:9])
+
+
 def test_max_batch_and_idle_slots():
     plan = [((b * 37) % 150 + 5, b % 4) for b in range(256)]
     for layout, kv, window in (("local", 1, 40), ("folded", 1, 0)):
         c = Case(layout, plan, 8, kv, window=window, seed=12)
-        c.run()
-        c.check()
+        for most in (3, 20):  # few rows and many
+            c.run(max_q_rows=most)
+            c.check()
 
 
 @pytest.mark.parametrize("layout,dtype", [("local", "bf16"), ("folded", "bf16")])

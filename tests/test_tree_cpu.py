@@ -103,8 +103,8 @@ def test_attn_unsupported_workspace_and_empty():
         assert need > 0 and _global(desc=_desc(layout, dtype), hq=32, pages=512, ws_bytes=need - 1) == gw.GW_ERR_WORKSPACE
 
 
-def _chunks(tiles, aim, blocks):
-    chunks = min(-(-tiles // aim), 38, max(1, 76 // blocks))
+def _chunks(tiles, aim, most, blocks):
+    chunks = min(-(-tiles // aim), most, max(1, 76 // blocks))
     return -(-tiles // -(-tiles // chunks))
 
 
@@ -115,7 +115,9 @@ def _chunks(tiles, aim, blocks):
 def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
     """No mix of rows and lengths up to the bounds needs more units than the workspace holds."""
     local = layout == gw.LAYOUT_LOCAL
-    group, copies, aim = (heads // kvh, kvh, 18) if local else (heads, 2, 32)
+    group, copies, aim, most = (heads // kvh, kvh, 18, 38) if local else (heads, 2, 32, 38)
+    if not local and rows * heads <= 32:
+        aim, most = 8, 76
     got = gw.lib().gw_tree_workspace_bytes(ctypes.byref(_desc(layout, kvh=kvh, base=0)), heads, 3, pages, rows, window)
     per = 128 // group
     cap = group * min(per, rows)
@@ -128,7 +130,7 @@ def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
             if L < n:
                 continue
             first = max(0, L - n - window + 1) // 64 if local else 0
-            nc = _chunks((L - 1) // 64 - first + 1, aim, blocks)
+            nc = _chunks((L - 1) // 64 - first + 1, aim, most, blocks)
             if nc > 1:
                 worst = max(worst, copies * blocks * nc)
     assert got >= 3 * worst * cap * (256 * 4 + 8)  # both kinds write parts of 256 dims

@@ -5,13 +5,15 @@
 // Row r of a sequence's n rows sees the cached tokens [0, L - n) and the drafts of
 // its mask word.  A unit is (sequence, chunk of tiles).  The cached tokens are the
 // products' long side and the rows x heads their columns:
-//   S^T[64 x 32]   = K_tile[64 x 512] . Q^T       (UMMA M = 64)
-//   O^T[512 x 32] += V_tile^T[512 x 64] . P^T     (UMMA M = 128, four times)
+//   S^T[T x 32]    = K_tile[T x 512] . Q^T       (UMMA M = T)
+//   O^T[512 x 32] += V_tile^T[512 x T] . P^T     (UMMA M = 128, four times)
+// with T = 64 tokens, 128 on the e4m3 pool (whose MMAs bound a call: 203 us with
+// tiles of 64 and 193 with 128, at 8 x 131072 tokens, 8 heads, 4 drafts),
 // so that the cache is read once and no logit computed twice: a call is bound by
 // memory (rows along M fill 128 of them and make each half of the output dims
 // compute all logits).
 //
-// A tile is four pages of 8-token x 16-byte blocks, which are UMMA core matrices:
+// A tile is whole pages of 8-token x 16-byte blocks, which are UMMA core matrices:
 // the K-major A operand of Q.K^T, whose K-steps point at k_rot and V on folded
 // pools, and the MN-major A operand of P.V.  On the full layout, whose tile is 128
 // KB, there is room for one, and K and V are copied and released apart.
@@ -31,7 +33,6 @@ namespace {
 
 constexpr int kThreads = 288;
 constexpr int NR = kTreeFewRows;
-constexpr int kTok = 64, kPages = 4;  // a tile
 constexpr int kRowRing = 4;           // units whose rows' keys are in shared memory
 // O is rescaled when a logit exceeds the reference by more than kLazy; on e4m3
 // pools a new reference lies kBelowMax below its logit, so that weights reach
@@ -44,25 +45,29 @@ struct FT;
 template <>
 struct FT<GW_LAYOUT_GLOBAL_FOLDED> {
   static constexpr bool kE4 = false, kApart = false;
+  static constexpr int kPages = 4;  // of a tile
   static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0, kBufs = 2, kSteps = 32;
   __device__ static constexpr int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
 };
 template <>
 struct FT<GW_LAYOUT_GLOBAL_FULL> {
   static constexpr bool kE4 = false, kApart = true;
+  static constexpr int kPages = 4;
   static constexpr int kPageBytes = 32768, kBlk = 128, kVcb = 64, kBufs = 1, kSteps = 32;
   __device__ static constexpr int k_cb(int ks) { return 2 * ks; }
 };
 template <>
 struct FT<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
   static constexpr bool kE4 = true, kApart = false;
-  static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0, kBufs = 4, kSteps = 16;
+  static constexpr int kPages = 8;
+  static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0, kBufs = 2, kSteps = 16;
   __device__ static constexpr int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
 };
 
 template <int LAYOUT>
 struct FL : FT<LAYOUT> {
   using B = FT<LAYOUT>;
+  static constexpr int kTok = B::kPages * kPage;       // tokens of a tile
   static constexpr int kTerms = B::kE4 ? 3 : 1;        // of P
   static constexpr int kNT = NR * kTerms;              // N of P.V
   static constexpr int kSCols = B::kE4 ? 2 * NR : NR;  // N of Q.K^T
@@ -74,9 +79,9 @@ struct FL : FT<LAYOUT> {
 template <int LAYOUT>
 struct FSmem {
   using T = FL<LAYOUT>;
-  uint8_t tiles[T::kBufs][kPages * T::kPageBytes];
+  uint8_t tiles[T::kBufs][T::kPages * T::kPageBytes];
   uint8_t q[NR * 1024];  // bf16 [NR / 8][64][8][16 B]; e4m3 [hi, lo][NR / 8][32][8][16 B]
-  uint8_t p[kTok * T::kNT * (T::kE4 ? 1 : 2)];  // P^T [8 tokens][16-byte block of rows][8][16 B]
+  uint8_t p[T::kTok * T::kNT * (T::kE4 ? 1 : 2)];  // P^T [8 tokens][16-byte block of rows][8][16 B]
   TreeRow rows[kRowRing][NR];
   float m[NR], alpha[NR], inv[NR], red[4][32];
   uint64_t kfull[T::kBufs], kempty[T::kBufs], vfull[T::kBufs], vempty[T::kBufs];
@@ -126,7 +131,7 @@ struct Unit {
   int s, n, nc, base, hi, t0, nt, row0;
 };
 
-template <int HQ>
+template <int LAYOUT, int HQ>
 __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan, int u) {
   Unit w;
   const int at = plan_seq(plan.ub, a.batch, u);
@@ -139,8 +144,9 @@ __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan
   w.nc = sp.chunks();
   const int c = u - plan.ub[at];
   w.t0 = c * sp.ct * kTreeTile;
-  w.nt = min(sp.ct, sp.tiles - c * sp.ct);
-  w.hi = min(L, (c * sp.ct + w.nt) * kTreeTile) - 1;
+  const int tiles = min(sp.ct, sp.tiles - c * sp.ct);
+  w.hi = min(L, (c * sp.ct + tiles) * kTreeTile) - 1;
+  w.nt = (tiles * kTreeTile + FL<LAYOUT>::kTok - 1) / FL<LAYOUT>::kTok;
   return w;
 }
 
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   using T = FL<LAYOUT>;
   using SM = FSmem<LAYOUT>;
   constexpr bool kE4 = T::kE4;
-  constexpr int NB = T::kBufs;
+  constexpr int NB = T::kBufs, kTok = T::kTok, kPages = T::kPages;
   constexpr float kBelow = kE4 ? kBelowMax : 0.f, kRaise = kLazy + kBelow;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
 
   if (warp == 4 || (T::kApart && warp == 5)) {
     // --------------------------------------------------------- page copies
-    // lane j < 4 copies page j of a tile, or its K or V: per 8-token block
+    // lane j copies page j of a tile, or its K or V: per 8-token block
     const bool is_v = warp == 5;
     uint64_t* const fulls = is_v ? sm.vfull : sm.kfull;
     uint64_t* const empties = is_v ? sm.vempty : sm.kempty;
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
       for (int t = 0; t < w.nt; ++t, ++gi) {
         const int b = gi % NB;
@@ -239,14 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   } else if (warp == 6) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s =
-        kE4 ? tc::idesc_e4m3(64, T::kSCols, false, false) : tc::idesc_bf16(64, T::kSCols, false, false);
+        kE4 ? tc::idesc_e4m3(128, T::kSCols, false, false) : tc::idesc_bf16(64, T::kSCols, false, false);
     // Q: 16-byte blocks 128 B apart, then the next 8 rows (of a term, then of the next)
     const uint64_t dq = tc::smem_desc(smem_u32(sm.q), 128, T::kQBlk * 128);
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
       if (!warp_wait(&sm.q_full, wt & 1, st)) break;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % NB, sb = gi & 1;
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
       const uint32_t o = tmem + T::kOBase;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % NB;
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
         tc::fence_after();
 #pragma unroll
-        for (int kk = 0; kk < (kE4 ? 2 : 4); ++kk) {  // 32 (e4m3) or 16 tokens
+        for (int kk = 0; kk < 4; ++kk) {  // 32 (e4m3) or 16 tokens
           const uint64_t bd = dp + ((kk * (kE4 ? 4 : 2) * kGroup) >> 4);
 #pragma unroll
           for (int blk = 0; blk < 4; ++blk) {
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     // sequence's rows x heads lie one after the other
     int wt = 0;
     for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
-      const Unit w = unit_of<HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
       const uint16_t* src = a.q + static_cast<int64_t>(w.row0) * HQ * 512;
       const int count = w.n * HQ;
       // rows behind the last see everything, which costs no masks; nobody reads them
@@ -412,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     }
   } else if (warp < 4) {  // (warp 5 has nothing to do on the folded layouts)
     // ------------------------------------------------- softmax and epilogue
-    const bool active = lane < 16;  // M = 64 uses lanes 0..15 of a quadrant
-    const int tok = 16 * warp + (lane & 15);
+    const bool active = kE4 || lane < 16;  // M = 64 uses lanes 0..15 of a quadrant
+    const int tok = kE4 ? 32 * warp + lane : 16 * warp + (lane & 15);
     const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
       const TreeRow* rows = sm.rows[wt % kRowRing];
       const uint32_t o_addr = tmem + lane_base + T::kOBase;
       float l_acc[NR];
@@ -524,14 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
         // p = 2^(s scale - m), rounded for the product; l sums it as rounded, so
         // that numerator and denominator round alike
-        uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
-        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        constexpr int kRB = NR / T::kRowsPerBlk;
+        uint32_t words[T::kTerms][kRB][4];
 #pragma unroll
-        for (int rb = 0; rb < NR / T::kRowsPerBlk; ++rb) {
-          if constexpr (kE4) {
-            uint32_t words[3][4];
+        for (int rb = 0; rb < kRB; ++rb) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kE4) {
               const int r = 16 * rb + 4 * k;
               float p[4];
 #pragma unroll
@@ -542,27 +547,28 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
 #pragma unroll
               for (int i = 0; i < 4; ++i) l_acc[r + i] += used[i];
 #pragma unroll
-              for (int t = 0; t < 3; ++t) words[t][k] = w3[t];
-            }
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-              if (active)
-                *reinterpret_cast<uint4*>(dst + (t * (NR / 16) + rb) * 128) =
-                    make_uint4(words[t][0], words[t][1], words[t][2], words[t][3]);
-          } else {
-            uint32_t words[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+              for (int t = 0; t < 3; ++t) words[t][rb][k] = w3[t];
+            } else {
               const int r = 8 * rb + 2 * k;
               const float p0 = ex2(fmaf(x[r], a.scale_log2, -sm.m[r]));
               const float p1 = ex2(fmaf(x[r + 1], a.scale_log2, -sm.m[r + 1]));
               __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
               l_acc[r] += __low2float(pb);
               l_acc[r + 1] += __high2float(pb);
-              words[k] = *reinterpret_cast<uint32_t*>(&pb);
+              words[0][rb][k] = *reinterpret_cast<uint32_t*>(&pb);
             }
-            if (active) *reinterpret_cast<uint4*>(dst + rb * 128) = make_uint4(words[0], words[1], words[2], words[3]);
           }
+        }
+        // into shared memory once P.V of the tile before has read its P
+        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
+        if (active) {
+#pragma unroll
+          for (int t = 0; t < T::kTerms; ++t)
+#pragma unroll
+            for (int rb = 0; rb < kRB; ++rb)
+              *reinterpret_cast<uint4*>(dst + (t * kRB + rb) * 128) =
+                  make_uint4(words[t][rb][0], words[t][rb][1], words[t][rb][2], words[t][rb][3]);
         }
         fence_proxy_async_smem();
         tc::fence_before();

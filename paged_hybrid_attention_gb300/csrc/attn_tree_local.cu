@@ -544,14 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // p = 2^(s scale - m), rounded for the product; l sums it as rounded, so
         // that numerator and denominator round alike
-        uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
-        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        constexpr int kRB = NR / T::kRowsPerBlk;
+        uint32_t words[T::kTerms][kRB][4];
 #pragma unroll
-        for (int rb = 0; rb < NR / T::kRowsPerBlk; ++rb) {
-          if constexpr (kE4) {
-            uint32_t words[3][4];
+        for (int rb = 0; rb < kRB; ++rb) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kE4) {
               const int r = 16 * rb + 4 * k;
               float p[4];
 #pragma unroll
@@ -562,26 +561,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) l_acc[r + i] += used[i];
 #pragma unroll
-              for (int t = 0; t < 3; ++t) words[t][k] = w3[t];
-            }
-#pragma unroll
-            for (int t = 0; t < 3; ++t)
-              *reinterpret_cast<uint4*>(dst + (t * (NR / 16) + rb) * 128) =
-                  make_uint4(words[t][0], words[t][1], words[t][2], words[t][3]);
-          } else {
-            uint32_t words[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+              for (int t = 0; t < 3; ++t) words[t][rb][k] = w3[t];
+            } else {
               const int r = 8 * rb + 2 * k;
               const float p0 = ex2(fmaf(x[r], a.scale_log2, -sm.m[r]));
               const float p1 = ex2(fmaf(x[r + 1], a.scale_log2, -sm.m[r + 1]));
               __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
               l_acc[r] += __low2float(pb);
               l_acc[r + 1] += __high2float(pb);
-              words[k] = *reinterpret_cast<uint32_t*>(&pb);
+              words[0][rb][k] = *reinterpret_cast<uint32_t*>(&pb);
             }
-            if (active) *reinterpret_cast<uint4*>(dst + rb * 128) = make_uint4(words[0], words[1], words[2], words[3]);
           }
+        }
+        // into shared memory once P.V of the tile before has read its P
+        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
+        if (active) {
+#pragma unroll
+          for (int t = 0; t < T::kTerms; ++t)
+#pragma unroll
+            for (int rb = 0; rb < kRB; ++rb)
+              *reinterpret_cast<uint4*>(dst + (t * kRB + rb) * 128) =
+                  make_uint4(words[t][rb][0], words[t][rb][1], words[t][rb][2], words[t][rb][3]);
         }
         fence_proxy_async_smem();
         tc::fence_before();

@@ -518,10 +518,10 @@ def norm_rope_append(pool, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out,
             rope_cs is None or out is None):
         _missing(fn, q=q, k=k, v=v, q_weight=q_weight, k_weight=k_weight, slot=slot, pos=pos, rope_cs=rope_cs, out=out)
     handle = _on_device(fn, stream, pool.data, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out, dev_status)
-    dim, rot = pool.desc.head_dim, pool.desc.rot_dim
-    rows = slot.numel()
+    dim, rot = (256, 256) if pool.layout == "local" else (512, 128)
+    rows, max_pos = slot.numel(), rope_cs.shape[0]
     hq = q.shape[1] if q.dim() == 3 else 0
-    bf16, kv = torch.bfloat16, (rows, pool.kv_heads, dim)
+    bf16, f32, kv = torch.bfloat16, torch.float32, (rows, pool.kv_heads, dim)
     if (q.shape != (rows, hq, dim) or k.shape != kv or v.shape != kv or q.dtype != bf16 or k.dtype != bf16 or
             v.dtype != bf16):
         for name, t, heads in (("q", q, "heads"), ("k", k, pool.kv_heads), ("v", v, pool.kv_heads)):
@@ -533,13 +533,19 @@ def norm_rope_append(pool, q, k, v, q_weight, k_weight, slot, pos, rope_cs, out,
     vr, vh, v1 = v.stride()
     if q1 != 1 or k1 != 1 or v1 != 1:
         _invalid(fn, "the last dimension of q, k and v must have stride 1")
-    _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
-    _dense(fn, "q_weight", q_weight, torch.float32, dim)
-    _dense(fn, "k_weight", k_weight, torch.float32, dim)
-    _vector(fn, "slot", slot, rows)
-    _vector(fn, "pos", pos, rows)
-    max_pos = rope_cs.shape[0]
-    _dense(fn, "rope_cs", rope_cs, torch.float32, max_pos, rot // 2, 2)
+    # one expression for what is as it should be; the calls behind it say what is not
+    if (out.dtype != bf16 or out.shape != (rows, hq, dim) or not out.is_contiguous() or q_weight.dtype != f32 or
+            q_weight.shape != (dim,) or not q_weight.is_contiguous() or k_weight.dtype != f32 or
+            k_weight.shape != (dim,) or not k_weight.is_contiguous() or rope_cs.dtype != f32 or
+            rope_cs.shape != (max_pos, rot // 2, 2) or not rope_cs.is_contiguous() or slot.dtype != torch.int32 or
+            slot.shape != (rows,) or not slot.is_contiguous() or pos.dtype != torch.int32 or pos.shape != (rows,) or
+            not pos.is_contiguous()):
+        _dense(fn, "out", out, bf16, rows, hq, dim)
+        _dense(fn, "q_weight", q_weight, f32, dim)
+        _dense(fn, "k_weight", k_weight, f32, dim)
+        _dense(fn, "rope_cs", rope_cs, f32, max_pos, rot // 2, 2)
+        _vector(fn, "slot", slot, rows)
+        _vector(fn, "pos", pos, rows)
     _check(_lib.gw_norm_rope_append(pool.desc, q.data_ptr(), qr, qh, k.data_ptr(), kr, kh, v.data_ptr(), vr, vh, rows,
                                     hq, q_weight.data_ptr(), k_weight.data_ptr(), float(eps), 1 if v_norm else 0,
                                     slot.data_ptr(), pos.data_ptr(), rope_cs.data_ptr(), max_pos, out.data_ptr(),
@@ -567,12 +573,17 @@ def _tree_args(fn, dim, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mas
     batch = seq_lens.numel()
     if q.dim() != 3:
         _invalid(fn, "q must be [rows, heads, %d] (got %s)" % (dim, list(q.shape)))
-    rows, hq = q.shape[0], q.shape[1]
-    _dense(fn, "q", q, torch.bfloat16, rows, hq, dim)
-    _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
-    _dense(fn, "tree_mask", tree_mask, torch.int64, rows)
-    _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
-    _vector(fn, "seq_lens", seq_lens, batch)
+    rows, hq, _ = shape = q.shape
+    if (hq * dim == 0 or shape != (rows, hq, dim) or q.dtype != torch.bfloat16 or not q.is_contiguous() or
+            out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or
+            tree_mask.dtype != torch.int64 or tree_mask.shape != (rows,) or not tree_mask.is_contiguous() or
+            cu_q_rows.dtype != torch.int32 or cu_q_rows.shape != (batch + 1,) or not cu_q_rows.is_contiguous() or
+            seq_lens.dtype != torch.int32 or seq_lens.shape != (batch,) or not seq_lens.is_contiguous()):
+        _dense(fn, "q", q, torch.bfloat16, rows, hq, dim)
+        _dense(fn, "out", out, torch.bfloat16, rows, hq, dim)
+        _dense(fn, "tree_mask", tree_mask, torch.int64, rows)
+        _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
+        _vector(fn, "seq_lens", seq_lens, batch)
     pages = _table(fn, "block_table", block_table, batch)
     if not workspace.is_contiguous():
         _invalid(fn, "workspace must be contiguous")

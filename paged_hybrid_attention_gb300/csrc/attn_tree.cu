@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   if (warp == 0) {
     float den = 0.f;
     for (int c = 0; c < nc; ++c) den = fmaf(w[c][lane], ok ? ml[c * step].y : 0.f, den);
-    inv_sum[lane] = den > 0.f ? 1.f / den : 0.f;
+    inv_sum[lane] = den == 0.f ? 0.f : 1.f / den;  // NaN where a chunk's sum is
   }
   __syncthreads();
   if (!ok) return;

@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
           mq = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mq)));  // not negative: ordered as bits
           const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
           const int e = min(125, max(-125, 7 - ex));
-          if (lane == r) row.scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          // (an infinity, which the terms cannot hold, makes the row's logits NaN)
+          if (lane == r) row.scale = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
         }
       } else {
         // into L2 while the unit before is at work

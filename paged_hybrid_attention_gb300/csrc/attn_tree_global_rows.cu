@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         }
         const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
         const int e = min(125, max(-125, 7 - ex));
-        up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        // (an infinity, which the terms cannot hold, makes the row's logits NaN)
+        up = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : NAN;
         sm.scale[wt % kRowRing][r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
         for (int c = 0; c < 16; ++c)

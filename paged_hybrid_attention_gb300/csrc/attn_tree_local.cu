@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 16));
           const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
           const int e = min(125, max(-125, 7 - ex));
-          const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+          // (an infinity, which the terms cannot hold, makes the row's logits NaN)
+          const float up = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : NAN;
           const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
           const float mine = __shfl_sync(0xffffffffu, down, lane & 7);  // lanes 0..7 have rows 8 rb ..
           if (lane >> 3 == rb) row.scale = mine;

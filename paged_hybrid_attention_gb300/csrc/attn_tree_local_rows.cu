@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
         const int e = min(125, max(-125, 7 - ex));
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        // (an infinity, which the terms cannot hold, makes the row's logits NaN)
+        const float up = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : NAN;
         next_row.scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll 2
         for (int c = 0; c < 16; ++c) {  // 16 dims: 16 bytes of each term; the second reading from L1
@@ -561,12 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ml[c & 3] = sm.stat[wt & 1][(r & (stride - 1)) + c * stride];
         M = fmaxf(M, ml[c & 3].x);
       }
-      for (int c = 0; c < w.copies; ++c)
-        if (ml[c & 3].x != -INFINITY) den = fmaf(ex2(ml[c & 3].x - M), ml[c & 3].y, den);
+      for (int c = 0; c < w.copies; ++c)  // a copy that saw no key has sum 0, one that saw only NaN logits NaN
+        if (ml[c & 3].y != 0.f) den = fmaf(ex2(ml[c & 3].x - M), ml[c & 3].y, den);
       const float own = sm.stat[wt & 1][r].x;
       mbar_arrive(&sm.stat_free[wt & 1]);
       // this lane's factor; a part stays unnormalised
-      const float f = own == -INFINITY ? 0.f : ex2(own - M) * (w.nc > 1 ? 1.f : 1.f / den);
+      const float f = own == -INFINITY && den == den ? 0.f : ex2(own - M) * (w.nc > 1 ? 1.f : 1.f / den);
       if (!warp_wait(&sm.o_done, wt & 1, st)) break;
       tc::fence_after();
       const int64_t part0 = static_cast<int64_t>(u) * a.part_rows;

@@ -579,7 +579,8 @@ gw_status gw_kv_evict_compact(const gw_kv_pool* pool, int32_t batch, const int32
  *   slot, pos, rope_cs, max_pos  as for gw_kv_append.  A row whose slot is out
  *              of range is not written to the pool (GW_DEV_SLOT_RANGE), its q'
  *              is; a row whose pos is out of range writes nothing
- *              (GW_DEV_POS_RANGE).
+ *              (GW_DEV_POS_RANGE).  Slots within range are distinct: of two rows
+ *              with one slot, either's K and V or a mix of both is left there.
  *   q_out      16-byte aligned; q itself if q is contiguous, otherwise it
  *              overlaps none of q, k, v.
  * num_rows 0 is a no-op; num_q_heads in [1, 1024].  A head whose sum of squares
@@ -632,7 +633,8 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  *              before it sees nothing: GW_DEV_POS_RANGE).
  *   max_q_rows  bound on n, in [1, 64].
  *   workspace  of gw_tree_workspace_bytes(...) bytes, 256-byte aligned; needs no
- *              initialisation.
+ *              initialisation.  Calls that share one run one after the other:
+ *              two streams at once need two.
  * A sequence with more than max_q_rows rows, or a length below its rows or
  * beyond the block table, gets zero rows (GW_DEV_LEN_RANGE).  Entries of the
  * block table before base - window + 1 may be anything.  A page outside
@@ -641,9 +643,11 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  * the sequence's rows of that KV head, as zero weights multiply it.
  * A row is bit-identical whatever else is in the batch (for the same window and
  * max_q_rows).
+ * An infinity or NaN in a row of q makes that row and head NaN, one in a K row
+ * the rows that see it.
  * bf16 and e4m3 pools.  batch at most 256.
  * Errors: those of gw_decode_attn_local; GW_ERR_INVALID_ARG (tree_mask or pos
- * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^27 or
+ * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^26 or
  * more).
  */
 gw_status gw_tree_attn_local(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
@@ -689,7 +693,8 @@ size_t gw_tree_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int3
  *              seq_lens itself if gw_kv_tree_move is not called after it (that
  *              call takes the length before).
  * A sequence with n outside [0, max_q_rows] or seq_lens[b] < n has path_lens 0
- * and keeps its length (GW_DEV_LEN_RANGE).
+ * and keeps its length (GW_DEV_LEN_RANGE).  The outputs overlap neither each
+ * other nor an input, except new_lens as said.
  * max_q_rows in [1, 64]; batch in [0, 65535], 0 is a no-op.
  * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
  */
@@ -800,10 +805,11 @@ size_t gw_noalloc_scratch_bytes(void);
  * cannot take the whole GPU.  The decode and prompt-row kernels here are
  * persistent with one CTA per SM (their shared memory allows no second), and
  * deal their work round-robin over the CTAs they have, so a CTA cap is an SM
- * cap (gw_rope_rows keeps to the appends' limit, gw_kv_evict_compact to one
- * block per allowed SM; the combine, with the weights pass beside it,
- * gw_kv_evict_select and gw_rope_cs_scaled take a few to some tens of
- * microseconds and are not capped): a prefill lane launched with a cap of N and
+ * cap (gw_rope_rows and gw_norm_rope_append keep to the appends' limit,
+ * gw_kv_evict_compact to one block per allowed SM; the combine, with the
+ * weights pass beside it, the merge of gw_tree_attn_*, gw_tree_accept,
+ * gw_kv_tree_move, gw_kv_evict_select and gw_rope_cs_scaled take a few to some
+ * tens of microseconds and are not capped): a prefill lane launched with a cap of N and
  * a decode lane with the SM count minus N run side by side on disjoint SMs.  Results do not depend
  * on the cap (a work unit's arithmetic never depends on which CTA runs it).
  * The setting is per host thread and is read when a call launches (for a
@@ -834,8 +840,9 @@ gw_status gw_set_early_launch(int32_t on);
  * predecessor may write.  With 1, the decode kernels compute their split plan
  * from cu_q_rows and seq_lens and fetch their first units' block-table
  * entries before that wait, which takes two dependent round trips off the
- * call; gw_kv_append and gw_rope_rows likewise read slot, pos and the RoPE
- * table rows they select before their wait, and a gw_append_decode_attn_local call the length,
+ * call; gw_kv_append, gw_rope_rows and gw_norm_rope_append likewise read slot,
+ * pos and the RoPE table rows they select before their wait (gw_tree_* and
+ * gw_kv_tree_move read nothing), and a gw_append_decode_attn_local call the length,
  * page and RoPE rows of the first row it appends.  KV pages, q, k, v, the workspace, out and
  * dev_status are still touched only after the wait.  The caller promises
  * that the kernel just before each call in its stream does not write that

@@ -695,8 +695,9 @@ static gw_status check_tree(const char* fn, const gw_kv_pool* pool, int32_t num_
   if (batch > kMaxTreeBatch)
     return fail(GW_ERR_UNSUPPORTED, fn, "batch (%d) exceeds %d sequences per call", batch, kMaxTreeBatch);
   if (local && window < 1) return fail(GW_ERR_INVALID_ARG, fn, "window must be >= 1");
-  if (max_pages_per_seq < 1 || max_pages_per_seq > 0x7fffffff / 16)
-    return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be in [1, 2^27)");
+  // a token's index and the end of its tile fit 31 bits
+  if (max_pages_per_seq < 1 || max_pages_per_seq >= 1 << 26)
+    return fail(GW_ERR_INVALID_ARG, fn, "max_pages_per_seq must be in [1, 2^26)");
   if (max_q_rows < 1 || max_q_rows > kMaxTreeRows)
     return fail(GW_ERR_INVALID_ARG, fn, "max_q_rows (%d) outside [1, %d]", max_q_rows, kMaxTreeRows);
   return GW_OK;
@@ -883,6 +884,11 @@ gw_status gw_tree_accept(int32_t batch, const int32_t* cu_q_rows, const int32_t*
   if (!aligned(next_tokens, 4) || !aligned(new_lens, 4)) return fail(GW_ERR_INVALID_ARG, fn, "next_tokens/new_lens misaligned");
   if (dev_status && !aligned(dev_status, 4)) return fail(GW_ERR_INVALID_ARG, fn, "dev_status misaligned");
   if (seq_lens == path_lens) return fail(GW_ERR_INVALID_ARG, fn, "seq_lens and path_lens are the same array");
+  const void* outs[] = {path, path_lens, next_tokens, new_lens};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (outs[i] && outs[i] == outs[j])
+        return fail(GW_ERR_INVALID_ARG, fn, "two of path, path_lens, next_tokens and new_lens are the same array");
   TreeAcceptArgs a{};
   a.batch = batch;
   a.max_q_rows = max_q_rows;

@@ -69,7 +69,7 @@ def _global(desc=None, q=M, out=M, hq=8, batch=2, cu=M, lens=M, table=M, pages=6
 
 
 COMMON = [dict(batch=-1), dict(q=0), dict(q=M + 8), dict(out=0), dict(out=M + 8), dict(cu=0), dict(cu=M + 2),
-          dict(lens=0), dict(table=M + 1), dict(pages=0), dict(pages=1 << 27), dict(mask=0), dict(mask=M + 4),
+          dict(lens=0), dict(table=M + 1), dict(pages=0), dict(pages=1 << 26), dict(mask=0), dict(mask=M + 4),
           dict(rows=0), dict(rows=65), dict(rows=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")),
           dict(scale=float("nan")), dict(ws=0), dict(ws=256 * M + 128), dict(status=M + 2), dict(hq=0)]
 
@@ -138,7 +138,7 @@ def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
 
 def test_workspace_refuses():
     size = gw.lib().gw_tree_workspace_bytes
-    for args in ((0, 2, 64, 16, 32), (8, -1, 64, 16, 32), (8, 2, 0, 16, 32), (8, 2, 1 << 27, 16, 32),
+    for args in ((0, 2, 64, 16, 32), (8, -1, 64, 16, 32), (8, 2, 0, 16, 32), (8, 2, 1 << 26, 16, 32),
                  (8, 2, 64, 0, 32), (8, 2, 64, 65, 32), (8, 2, 64, 16, 0), (12, 2, 64, 16, 32), (8, 257, 64, 16, 32)):
         assert size(ctypes.byref(_desc()), *args) == 0
         assert gw.last_error().startswith("gw_tree_workspace_bytes:")
@@ -146,8 +146,8 @@ def test_workspace_refuses():
 
 
 # ---- gw_tree_accept, gw_kv_tree_move ----------------------------------------------
-def _accept(batch=2, cu=M, lens=M, rows=16, parent=M, draft=M, target=M, path=M, stride=16, n=2 * M, nxt=M, new=M,
-            status=0):
+def _accept(batch=2, cu=M, lens=M, rows=16, parent=M, draft=M, target=M, path=3 * M, stride=16, n=2 * M, nxt=4 * M,
+            new=M, status=0):
     return gw.lib().gw_tree_accept(batch, _at(cu), _at(lens), rows, _at(parent), _at(draft), _at(target), _at(path),
                                    stride, _at(n), _at(nxt) if nxt else None, _at(new) if new else None,
                                    _at(status) if status else None, None)
@@ -156,7 +156,7 @@ def _accept(batch=2, cu=M, lens=M, rows=16, parent=M, draft=M, target=M, path=M,
 @pytest.mark.parametrize("bad", [
     dict(batch=-1), dict(batch=65536), dict(rows=0), dict(rows=65), dict(stride=15), dict(stride=(1 << 40) + 1),
     dict(cu=0), dict(lens=0), dict(parent=0), dict(draft=M + 2), dict(target=0), dict(path=M + 1), dict(n=0), dict(n=M),
-    dict(nxt=M + 2), dict(new=M + 1), dict(status=M + 3),
+    dict(n=3 * M), dict(nxt=3 * M), dict(nxt=2 * M), dict(new=4 * M), dict(new=2 * M), dict(nxt=M + 2), dict(new=M + 1), dict(status=M + 3),
 ])
 def test_accept_refuses(bad):
     assert _accept(**bad) == gw.GW_ERR_INVALID_ARG

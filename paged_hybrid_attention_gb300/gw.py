@@ -271,6 +271,7 @@ class KVPool:
         off = (-storage.data_ptr()) % 256
         self.data = storage[off:off + num_pages * pb]
         self.desc.base = self.data.data_ptr()
+        self.device_index = storage.get_device()  # -1 on the CPU
 
     @property
     def nbytes(self):
@@ -660,8 +661,9 @@ def kv_tree_move(pools, cu_q_rows, seq_lens, block_table, path, path_lens, dev_s
     fn = "gw_kv_tree_move"
     if cu_q_rows is None or seq_lens is None or block_table is None or path is None or path_lens is None:
         _missing(fn, cu_q_rows=cu_q_rows, seq_lens=seq_lens, block_table=block_table, path=path, path_lens=path_lens)
-    handle = _on_device(fn, stream, cu_q_rows, seq_lens, block_table, path, path_lens, dev_status,
-                        *[p.data for p in pools])
+    handle = _on_device(fn, stream, cu_q_rows, seq_lens, block_table, path, path_lens, dev_status)
+    if pools and {p.device_index for p in pools} != {cu_q_rows.get_device()}:
+        _on_device(fn, stream, cu_q_rows, *[p.data for p in pools])
     batch = seq_lens.numel()
     _vector(fn, "cu_q_rows", cu_q_rows, batch + 1)
     _vector(fn, "seq_lens", seq_lens, batch)
@@ -669,7 +671,7 @@ def kv_tree_move(pools, cu_q_rows, seq_lens, block_table, path, path_lens, dev_s
     pages = _table(fn, "block_table", block_table, batch)
     stride = _row_stride(fn, "path", path, torch.int32, batch)
     # the descriptions side by side, as a C array of them
-    descs = b"".join([bytes(p.desc) for p in pools])
+    descs = b"".join([p.desc for p in pools])
     _check(_lib.gw_kv_tree_move(descs, len(pools), batch, cu_q_rows.data_ptr(), seq_lens.data_ptr(),
                                 block_table.data_ptr(), pages, path.data_ptr(), stride, path_lens.data_ptr(),
                                 _addr(dev_status), handle))

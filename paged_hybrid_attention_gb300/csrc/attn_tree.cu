@@ -1,6 +1,7 @@
 // Attention of drafted trees: launchers, and the merge of the chunks of long
-// sequences.  The attention kernels are attn_tree_local.cu and attn_tree_local_rows.cu (local layers) and
-// attn_tree_global.cu (global layers); both write rows of single-chunk
+// sequences.  The attention kernels are attn_tree_local.cu and
+// attn_tree_local_rows.cu (local layers), attn_tree_global.cu and
+// attn_tree_global_rows.cu (global layers); all write the rows of single-chunk
 // sequences themselves.
 //
 // The rows of a sequence (n <= 64) times its heads are a matrix product's rows,
@@ -15,9 +16,11 @@ namespace {
 // A block merges 32 of the 256 dims of 32 rows of a unit, a lane a row: parts lie
 // as [unit][8-column block 32][row][8], so that what a warp stores or reads at a
 // time is 1 KB in one piece.  The rows' weights are put in shared memory first; a
-// warp then takes a column block.  Chunks are added in order, so a row does not depend
-// on its companions.  kLocal: units are (KV head, chunk, row block), else (chunk,
-// row block, half of the dims).  134 MB of parts (8 x 128 rows in 64 chunks).
+// warp then takes a column block.  Chunks are added in order, so a row does not
+// depend on its companions.  kLocal: units are (KV head, chunk, row block), else
+// (chunk, row block, half of the dims).  Latency-bound: with (m, l) read chunk by
+// chunk instead of at once, 8 x 131072 tokens, 8 heads, 4 drafts took 262 us
+// instead of 252, the full layout at 4 x 131072 196 instead of 183.
 constexpr int kMergeWarps = 4;
 
 __device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
@@ -29,8 +32,8 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
 template <bool kLocal>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const LocalArgs a, int group, int copies,
                                                                       int blocks, const TreeRule rule, int scale) {
-  __shared__ float w[kTreeMaxChunks][32];
-  __shared__ float top[kMergeWarps][32], inv_sum[32];
+  __shared__ float w[kTreeMaxChunks][32], wl[kTreeMaxChunks][32];
+  __shared__ float top[kMergeWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -55,26 +58,39 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   const int64_t u0 = ub + (kLocal ? copy * nc * sp.blocks + qb : qb * 2 + copy);
   const int64_t step = (kLocal ? sp.blocks : 2 * sp.blocks) * static_cast<int64_t>(a.part_rows);
   const float2* ml = a.part_ml + u0 * a.part_rows + place;
+  // a warp takes every fourth chunk's (m, l), all its loads in flight at once
+  constexpr int kMine = (kTreeMaxChunks + kMergeWarps - 1) / kMergeWarps;
+  float2 mine[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int c = warp + kMergeWarps * i;
+    if (kMergeWarps * i >= nc) break;
+    mine[i] = ok && c < nc ? ml[c * step] : make_float2(-INFINITY, 0.f);
+  }
   float M = -INFINITY;
-  for (int c = warp; c < nc; c += kMergeWarps) {
-    const float m = ok ? ml[c * step].x : -INFINITY;
-    w[c][lane] = m;
-    M = fmaxf(M, m);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (kMergeWarps * i >= nc) break;
+    M = fmaxf(M, mine[i].x);
   }
   top[warp][lane] = M;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < kMergeWarps; ++k) M = fmaxf(M, top[k][lane]);
-  for (int c = warp; c < nc; c += kMergeWarps) w[c][lane] = M == -INFINITY ? 0.f : ex2(w[c][lane] - M);
-  __syncthreads();
-  if (warp == 0) {
-    float den = 0.f;
-    for (int c = 0; c < nc; ++c) den = fmaf(w[c][lane], ok ? ml[c * step].y : 0.f, den);
-    inv_sum[lane] = den == 0.f ? 0.f : 1.f / den;  // NaN where a chunk's sum is
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int c = warp + kMergeWarps * i;
+    if (c >= nc) break;
+    const float x = M == -INFINITY ? 0.f : ex2(mine[i].x - M);
+    w[c][lane] = x;
+    wl[c][lane] = x * mine[i].y;
   }
   __syncthreads();
+  float den = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < nc; ++c) den += wl[c][lane];
   if (!ok) return;
-  const float inv = inv_sum[lane];
+  const float inv = den == 0.f ? 0.f : 1.f / den;  // NaN where a chunk's sum is
   const int head = kLocal ? copy * group + place % group : place % group;
   uint16_t* dst = a.out + ((static_cast<int64_t>(row0) + q) * a.num_q_heads + head) * (kLocal ? 256 : 512) +
                   (kLocal ? 0 : 256 * copy);
@@ -111,7 +127,7 @@ cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, in
 // sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16: 16 drafts 49.8 us
 // (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows, 100.6); 61 e4m3
 // sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8 heads, 4 drafts
-// 264 us (along M 432).  The rule is the call's bound, so that a captured call stays
+// 252 us (along M 432).  The rule is the call's bound, so that a captured call stays
 // what it is.
 //
 // The merge is left out where the block table's width allows one chunk only.

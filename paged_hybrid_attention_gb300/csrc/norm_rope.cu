@@ -20,7 +20,7 @@
 // next one's loads as soon as it is unpacked.
 //
 // Memory-bound, by the bytes in flight: 8192 rows of 32 + 2 x 16 heads of 256
-// (e4m3 pool) 78 us, 0.89 of the copy rate; one 16-byte load a lane and the
+// (e4m3 pool) 78 us, 0.90 of the copy rate; one 16-byte load a lane and the
 // pairs' other halves by shuffles 220 us; 3 blocks an SM instead of 4 86 us
 // (more registers, fewer heads in flight), 2 heads at a time 93 us, loads behind
 // the position's 84 us, runs of 8 heads 99 us, of 32 95 us.

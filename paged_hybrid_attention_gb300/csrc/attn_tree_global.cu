@@ -11,7 +11,8 @@
 // tiles of 64 and 193 with 128, at 8 x 131072 tokens, 8 heads, 4 drafts),
 // so that the cache is read once and no logit computed twice: a call is bound by
 // memory (rows along M fill 128 of them and make each half of the output dims
-// compute all logits).
+// compute all logits).  8 x 131072 tokens, 8 heads, 4 drafts: folded 252 us (0.78 of
+// the copy rate), e4m3 188 (0.52); full layout, 4 x 131072, 183 (0.86).
 //
 // A tile is whole pages of 8-token x 16-byte blocks, which are UMMA core matrices:
 // the K-major A operand of Q.K^T, whose K-steps point at k_rot and V on folded

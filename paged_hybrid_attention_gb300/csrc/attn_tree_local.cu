@@ -4,8 +4,9 @@
 //
 // Row r of a sequence's n <= 64 rows, at position pos_r, sees the cached tokens
 // j < L - n with j > pos_r - W and the drafts of its mask word whose positions
-// are in the window.  A unit is (sequence, KV head, chunk of tiles).  A tree has few rows, so that the cached
-// tokens are the products' long side and the rows their columns:
+// are in the window.  A unit is (sequence, KV head, chunk of tiles).  A tree has few
+// rows, so that the cached tokens are the products' long side and the rows their
+// columns:
 //   S^T[T x NR]    = K_tile[T x 256] . Q^T       (UMMA M = T)
 //   O^T[256 x NR] += V_tile^T[256 x T] . P^T     (UMMA M = 128, twice)
 // with T = 64 tokens (bf16) or 128 (e4m3) and NR = 16 or 32 rows: an MMA takes
@@ -25,6 +26,10 @@
 // thread per dim), 4 and 5 copies of K and V, 6 issues Q.K^T (and owns tensor
 // memory), 7 issues P.V, 8 Q rows and what they see.  Every wait is bounded
 // (GW_DEV_TIMEOUT).
+//
+// Bound by memory: 16 sequences of 512 to 8192 tokens, 16 drafts, 16 KV heads of 2,
+// window 1024, 49 us (0.82 of the copy rate); e4m3, 61 sequences, 7 drafts 91 us
+// (0.86); 64 sequences, 4 drafts 158 us (0.99).
 #include "plan.cuh"
 #include "tcgen05.cuh"
 #include "tma.cuh"

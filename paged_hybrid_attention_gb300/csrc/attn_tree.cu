@@ -123,24 +123,26 @@ cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, in
 
 }  // namespace
 
-// Up to 32 rows x heads lie along the products' N, more along M.  Local, 16
-// sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16: 16 drafts 49.8 us
-// (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows, 100.6); 61 e4m3
-// sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8 heads, 4 drafts
-// 252 us (along M 432).  The rule is the call's bound, so that a captured call stays
-// what it is.
+// Up to 32 rows x heads (64 on bf16 global layers) lie along the products' N, more
+// along M.  Local, 16 sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16:
+// 16 drafts 49 us (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows,
+// 100.6); 61 e4m3 sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8
+// heads: 4 drafts 254 us (along M 432), 8 drafts 341 (435); 1 x 8192, 8 drafts 37
+// (54); only with tables of a few tiles is M ahead, 11.6 us against 15.4 at 2
+// sequences of 37 and 100 tokens.  The rule is the call's bound, so that a captured
+// call stays what it is.
 //
 // The merge is left out where the block table's width allows one chunk only.
 cudaError_t launch_local_tree(int dtype, int group, const LocalArgs& a, cudaStream_t st) {
   const TreeRule rule = tree_rule_local(group);
-  cudaError_t e = a.max_q_rows * group <= kTreeFewRows ? launch_local_tree_few(dtype, group, a, st)
+  cudaError_t e = a.max_q_rows * group <= tree_few_rows(GW_LAYOUT_LOCAL) ? launch_local_tree_few(dtype, group, a, st)
                                                        : launch_local_tree_rows(dtype, group, a, st);
   if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, rule) == 1) return e;
   return launch_merge<true>(a, group, rule, 1, st);
 }
 
 cudaError_t launch_global_tree(int layout, const LocalArgs& a, cudaStream_t st) {
-  const bool few = a.max_q_rows * a.num_q_heads <= kTreeFewRows;
+  const bool few = a.max_q_rows * a.num_q_heads <= tree_few_rows(layout);
   const TreeRule rule = few ? tree_rule_few(a.num_q_heads) : tree_rule_global(a.num_q_heads);
   cudaError_t e = few ? launch_global_tree_few(layout, a, st) : launch_global_tree_rows(layout, a, st);
   if (e != cudaSuccess || tree_max_chunks(a.max_pages, a.max_q_rows, a.window, rule) == 1) return e;

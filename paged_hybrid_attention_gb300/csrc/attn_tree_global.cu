@@ -1,39 +1,43 @@
 // Attention of drafted trees on GLOBAL layers (gw_tree_attn_global), on the
-// tensor cores (tcgen05): head dim 512, one KV head, all three pool layouts, trees
-// of up to 32 rows x heads (attn_tree_global_rows.cu has the others).
+// tensor cores (tcgen05): head dim 512, one KV head, all three pool layouts, calls
+// of up to 64 rows x heads (e4m3 pool: 32; attn_tree_global_rows.cu has the others).
 //
 // Row r of a sequence's n rows sees the cached tokens [0, L - n) and the drafts of
 // its mask word.  A unit is (sequence, chunk of tiles).  The cached tokens are the
-// products' long side and the rows x heads their columns:
-//   S^T[T x 32]    = K_tile[T x 512] . Q^T       (UMMA M = T)
-//   O^T[512 x 32] += V_tile^T[512 x T] . P^T     (UMMA M = 128, four times)
-// with T = 64 tokens, 128 on the e4m3 pool (whose MMAs bound a call: 203 us with
-// tiles of 64 and 193 with 128, at 8 x 131072 tokens, 8 heads, 4 drafts),
-// so that the cache is read once and no logit computed twice: a call is bound by
-// memory (rows along M fill 128 of them and make each half of the output dims
-// compute all logits).  8 x 131072 tokens, 8 heads, 4 drafts: folded 252 us (0.78 of
-// the copy rate), e4m3 188 (0.52); full layout, 4 x 131072, 183 (0.86).
+// products' long side and the rows x heads their NR columns, 32 or 64:
+//   S^T[T x NR]    = K_tile[T x 512] . Q^T       (UMMA M = 64, e4m3 128)
+//   O^T[512 x NR] += V_tile^T[512 x T] . P^T     (UMMA M = 128, four times)
+// so that the cache is read once and no logit computed twice (rows along M fill 128
+// of them and make each half of the output dims compute all logits).  T is 64
+// tokens; on folded pools 48 beside 64 rows of Q, two tiles in shared memory; on
+// the e4m3 pool, whose MMAs bound a call, 128 (8 x 131072 tokens, 8 heads, 4 drafts:
+// 203 us with tiles of 64 and 193 with 128).
+//
+// 8 x 131072 tokens, 8 heads, 4 drafts: folded 254 us (0.78 of the copy rate), e4m3
+// 176 (0.56); full layout, 4 x 131072, 183 (0.86).  8 drafts: folded 341 us (0.58;
+// in attn_tree_global_rows.cu 435), full 205 (0.77; 256).
 //
 // A tile is whole pages of 8-token x 16-byte blocks, which are UMMA core matrices:
 // the K-major A operand of Q.K^T, whose K-steps point at k_rot and V on folded
-// pools, and the MN-major A operand of P.V.  On the full layout, whose tile is 128
-// KB, there is room for one, and K and V are copied and released apart.
+// pools, and the MN-major A operand of P.V.  (With T = 48 the last quarter of A's
+// 64 rows is whatever lies behind the tile; nothing reads those rows of S.)  On the
+// full layout, whose tile is 128 KB, there is room for one, and K and V are copied
+// and released apart.
 // On the e4m3 pool q is two e4m3 terms after an exact power-of-two scaling per row,
 // side by side along N, and P three e5m2 terms (tcgen05.cuh), side by side too:
 // S and O have a column per row and term, which the softmax and the epilogue add.
 //
-// Warp roles (288 threads): 0-3 softmax (a thread per token) and epilogue (a thread
-// per dim), 4 copies (of K on the full layout, whose V warp 5 copies), 6 issues
-// Q.K^T (and owns tensor memory), 7 issues P.V, 8 Q rows and what they see.  Every
-// wait is bounded (GW_DEV_TIMEOUT).
+// Warp roles (384 threads, 512 with 64 rows): 0-3 softmax (a thread per token) and
+// epilogue (a thread per dim) of rows 0-31, 12-15 of the others, 4 copies (of K on
+// the full layout, whose V warp 5 copies), 6 issues Q.K^T (and owns tensor memory), 7
+// issues P.V, 8-11 Q rows and what they see (with one warp a sequence of 8192 tokens
+// took 4 us more at 8 drafts, 3 at 4).  Every wait is bounded (GW_DEV_TIMEOUT).
 #include "plan.cuh"
 #include "tcgen05.cuh"
 
 namespace gw {
 namespace {
 
-constexpr int kThreads = 288;
-constexpr int NR = kTreeFewRows;
 constexpr int kRowRing = 4;           // units whose rows' keys are in shared memory
 // O is rescaled when a logit exceeds the reference by more than kLazy; on e4m3
 // pools a new reference lies kBelowMax below its logit, so that weights reach
@@ -41,33 +45,35 @@ constexpr int kRowRing = 4;           // units whose rows' keys are in shared me
 constexpr float kLazy = 8.f, kBelowMax = 7.f;
 constexpr float kUnset = -1e38f;  // reference of a row that has seen no key
 
-template <int LAYOUT>
+template <int LAYOUT, int NR>
 struct FT;
-template <>
-struct FT<GW_LAYOUT_GLOBAL_FOLDED> {
+template <int NR>
+struct FT<GW_LAYOUT_GLOBAL_FOLDED, NR> {
   static constexpr bool kE4 = false, kApart = false;
-  static constexpr int kPages = 4;  // of a tile
+  static constexpr int kPages = NR == 32 ? 4 : 3;  // of a tile: two tiles beside Q
   static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0, kBufs = 2, kSteps = 32;
   __device__ static constexpr int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
 };
-template <>
-struct FT<GW_LAYOUT_GLOBAL_FULL> {
+template <int NR>
+struct FT<GW_LAYOUT_GLOBAL_FULL, NR> {
   static constexpr bool kE4 = false, kApart = true;
   static constexpr int kPages = 4;
   static constexpr int kPageBytes = 32768, kBlk = 128, kVcb = 64, kBufs = 1, kSteps = 32;
   __device__ static constexpr int k_cb(int ks) { return 2 * ks; }
 };
 template <>
-struct FT<GW_LAYOUT_GLOBAL_FOLDED_E4M3> {
+struct FT<GW_LAYOUT_GLOBAL_FOLDED_E4M3, 32> {
   static constexpr bool kE4 = true, kApart = false;
   static constexpr int kPages = 8;
   static constexpr int kPageBytes = 10240, kBlk = 40, kVcb = 0, kBufs = 2, kSteps = 16;
   __device__ static constexpr int k_cb(int ks) { return ks < 4 ? 32 + 2 * ks : 2 * ks; }
 };
 
-template <int LAYOUT>
-struct FL : FT<LAYOUT> {
-  using B = FT<LAYOUT>;
+template <int LAYOUT, int NR>
+struct FL : FT<LAYOUT, NR> {
+  using B = FT<LAYOUT, NR>;
+  static constexpr int kGroups = NR / 32;              // of softmax warps, 32 rows each
+  static constexpr int kThreads = 256 + 128 * kGroups;
   static constexpr int kTok = B::kPages * kPage;       // tokens of a tile
   static constexpr int kTerms = B::kE4 ? 3 : 1;        // of P
   static constexpr int kNT = NR * kTerms;              // N of P.V
@@ -77,29 +83,35 @@ struct FL : FT<LAYOUT> {
   static constexpr int kQBlk = B::kE4 ? 32 : 64;       // 16-byte blocks of a row of Q (of a term)
 };
 
-template <int LAYOUT>
+template <int LAYOUT, int NR>
 struct FSmem {
-  using T = FL<LAYOUT>;
+  using T = FL<LAYOUT, NR>;
   uint8_t tiles[T::kBufs][T::kPages * T::kPageBytes];
   uint8_t q[NR * 1024];  // bf16 [NR / 8][64][8][16 B]; e4m3 [hi, lo][NR / 8][32][8][16 B]
   uint8_t p[T::kTok * T::kNT * (T::kE4 ? 1 : 2)];  // P^T [8 tokens][16-byte block of rows][8][16 B]
   TreeRow rows[kRowRing][NR];
-  float m[NR], alpha[NR], inv[NR], red[4][32];
+  float m[NR], alpha[NR], inv[NR], red[T::kGroups][4][32];
   uint64_t kfull[T::kBufs], kempty[T::kBufs], vfull[T::kBufs], vempty[T::kBufs];
   uint64_t s_ready[2], s_free[2], p_ready, p_free, o_done, q_full, q_free;
   int32_t mask[T::kBufs], vmask[T::kBufs];  // pages of the tile (K, V apart) that were loaded
-  int32_t flag[2];  // by tile parity: index + 1 of the last tile that asked for a new reference
+  // by tile parity: index + 1 of the last tile that asked for a new reference
+  int32_t flag[T::kGroups][2];
   uint32_t tmem_base;
   TreePlan plan;
 };
-static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FOLDED>) <= 232448, "shared memory of one CTA");
-static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FULL>) <= 232448, "shared memory of one CTA");
-static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FOLDED, 32>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FOLDED, 64>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FULL, 32>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FULL, 64>) <= 232448, "shared memory of one CTA");
+static_assert(sizeof(FSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3, 32>) <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
-__device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// of a group of softmax warps
+__device__ __forceinline__ void softmax_bar(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
 __device__ __forceinline__ void zero16(uint32_t dst) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
 }
@@ -132,7 +144,7 @@ struct Unit {
   int s, n, nc, base, hi, t0, nt, row0;
 };
 
-template <int LAYOUT, int HQ>
+template <int LAYOUT, int HQ, int NR>
 __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan, int u) {
   Unit w;
   const int at = plan_seq(plan.ub, a.batch, u);
@@ -147,14 +159,14 @@ __device__ __forceinline__ Unit unit_of(const LocalArgs& a, const TreePlan& plan
   w.t0 = c * sp.ct * kTreeTile;
   const int tiles = min(sp.ct, sp.tiles - c * sp.ct);
   w.hi = min(L, (c * sp.ct + tiles) * kTreeTile) - 1;
-  w.nt = (tiles * kTreeTile + FL<LAYOUT>::kTok - 1) / FL<LAYOUT>::kTok;
+  w.nt = (w.hi - w.t0) / FL<LAYOUT, NR>::kTok + 1;
   return w;
 }
 
-template <int LAYOUT, int HQ>
-__global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArgs a) {
-  using T = FL<LAYOUT>;
-  using SM = FSmem<LAYOUT>;
+template <int LAYOUT, int HQ, int NR>
+__global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kernel(const LocalArgs a) {
+  using T = FL<LAYOUT, NR>;
+  using SM = FSmem<LAYOUT, NR>;
   constexpr bool kE4 = T::kE4;
   constexpr int NB = T::kBufs, kTok = T::kTok, kPages = T::kPages;
   constexpr float kBelow = kE4 ? kBelowMax : 0.f, kRaise = kLazy + kBelow;
@@ -172,13 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.s_ready[b], 1);
-      mbar_init(&sm.s_free[b], 128);
-      sm.flag[b] = 0;
+      mbar_init(&sm.s_free[b], 128 * T::kGroups);
+      for (int g = 0; g < T::kGroups; ++g) sm.flag[g][b] = 0;
     }
-    mbar_init(&sm.p_ready, 128);
+    mbar_init(&sm.p_ready, 128 * T::kGroups);
     mbar_init(&sm.p_free, 1);
     mbar_init(&sm.o_done, 1);
-    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_full, 4);
     mbar_init(&sm.q_free, 1);
     fence_mbar_init();
   }
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       const int32_t* bt = a.block_table + static_cast<int64_t>(w.s) * a.max_pages;
       for (int t = 0; t < w.nt; ++t, ++gi) {
         const int b = gi % NB;
@@ -253,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       if (!warp_wait(&sm.q_full, wt & 1, st)) break;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % NB, sb = gi & 1;
@@ -297,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       const uint32_t o = tmem + T::kOBase;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int b = gi % NB;
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
         tc::fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {  // 32 (e4m3) or 16 tokens
+        for (int kk = 0; kk < kTok / (kE4 ? 32 : 16); ++kk) {
           const uint64_t bd = dp + ((kk * (kE4 ? 4 : 2) * kGroup) >> 4);
 #pragma unroll
           for (int blk = 0; blk < 4; ++blk) {
@@ -336,22 +348,28 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp >= 8 && warp < 12) {
     // -------------------------------------------------------------- Q rows
-    // lane l copies rows l % 8 + 8 rb, every fourth 16-byte block from l / 8 on; a
-    // sequence's rows x heads lie one after the other
+    // a warp copies 8 rows of every 32: lane l row l % 8, every fourth 16-byte block
+    // from l / 8 on; a sequence's rows x heads lie one after the other
     int wt = 0;
     for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
-      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
+      const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       const uint16_t* src = a.q + static_cast<int64_t>(w.row0) * HQ * 512;
-      const int count = w.n * HQ;
+      const int count = w.n * HQ, first = 8 * (warp - 8);
       // rows behind the last see everything, which costs no masks; nobody reads them
-      TreeRow row{~0ull, 0, 1.f};
-      if (lane < count) row = tree_row(a, w.row0, lane / HQ, w.n, w.base, false);
+      TreeRow row[T::kGroups];
+#pragma unroll
+      for (int g = 0; g < T::kGroups; ++g) {
+        const int r = 32 * g + first + (lane & 7);
+        row[g] = r < count ? tree_row(a, w.row0, r / HQ, w.n, w.base, false) : TreeRow{~0ull, 0, 1.f};
+      }
       if constexpr (kE4) {
-        // each row's largest |q| (lane l: row l)
+        // each row's largest |q|
 #pragma unroll 4
-        for (int r = 0; r < count; ++r) {
+        for (int k = 0; k < 8; ++k) {
+          const int r = first + k;
+          if (r >= count) break;
           const uint4 x = *reinterpret_cast<const uint4*>(src + r * 512 + 8 * lane);
           const uint4 y = *reinterpret_cast<const uint4*>(src + r * 512 + 256 + 8 * lane);
           const uint32_t u8[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -363,20 +381,23 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
           const int ex = mq > 0.f ? static_cast<int>((__float_as_uint(mq) >> 23) & 0xFF) - 127 : 7;
           const int e = min(125, max(-125, 7 - ex));
           // (an infinity, which the terms cannot hold, makes the row's logits NaN)
-          if (lane == r) row.scale = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
+          if ((lane & 7) == k)
+            row[0].scale = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
         }
       } else {
         // into L2 while the unit before is at work
-        if (lane < count) prefetch_l2(src + lane * 512, 1024);
+#pragma unroll
+        for (int g = 0; g < T::kGroups; ++g)
+          if (lane < 8 && 32 * g + first + lane < count) prefetch_l2(src + (32 * g + first + lane) * 512, 1024);
       }
       if (wt > 0 && !warp_wait(&sm.q_free, (wt - 1) & 1, st)) break;
-#pragma unroll 1
-      for (int rb = 0; rb < NR / 8; ++rb) {
-        const int r = 8 * rb + (lane & 7);
+#pragma unroll
+      for (int g = 0; g < T::kGroups; ++g) {
+        const int r = 32 * g + first + (lane & 7), rb = r / 8;
         const bool ok_row = r < count;
         const uint16_t* from = src + (ok_row ? r : 0) * 512;
         if constexpr (kE4) {
-          const float up = 1.f / __shfl_sync(0xffffffffu, row.scale, r);  // a power of two: exact
+          const float up = 1.f / row[0].scale;  // a power of two: exact
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int cb = (lane >> 3) + 4 * j;
@@ -408,50 +429,53 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
               zero16(at);
           }
         }
+        if (lane < 8) sm.rows[wt % kRowRing][r] = row[g];
       }
       if constexpr (!kE4) {
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      sm.rows[wt % kRowRing][lane] = row;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full);
     }
-  } else if (warp < 4) {  // (warp 5 has nothing to do on the folded layouts)
+  } else if (warp < 4 || warp >= 12) {  // (warp 5 has nothing to do on the folded layouts)
     // ------------------------------------------------- softmax and epilogue
-    const bool active = kE4 || lane < 16;  // M = 64 uses lanes 0..15 of a quadrant
-    const int tok = kE4 ? 32 * warp + lane : 16 * warp + (lane & 15);
-    const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
+    // warps 0-3 rows 0 to 31, 12-15 the others; a warp reaches quadrant warp % 4
+    const int grp = warp >= 12, quad = warp & 3, row0 = 32 * grp, gtid = 32 * quad + lane;
+    // M = 64 uses lanes 0..15 of a quadrant
+    const int tok = kE4 ? gtid : 16 * quad + (lane & 15);
+    const bool active = (kE4 || lane < 16) && tok < kTok;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     uint32_t gi = 0;
     int wt = 0;
     bool ok = true;
     for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
-      const Unit w = unit_of<LAYOUT, HQ>(a, sm.plan, u);
-      const TreeRow* rows = sm.rows[wt % kRowRing];
-      const uint32_t o_addr = tmem + lane_base + T::kOBase;
-      float l_acc[NR];
+      const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
+      const TreeRow* rows = sm.rows[wt % kRowRing] + row0;
+      const uint32_t o_addr = tmem + lane_base + T::kOBase + row0;
+      float l_acc[32];
 #pragma unroll
-      for (int r = 0; r < NR; ++r) l_acc[r] = 0.f;
+      for (int r = 0; r < 32; ++r) l_acc[r] = 0.f;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int sb = gi & 1;
         if (!warp_wait(&sm.s_ready[sb], (gi >> 1) & 1, st)) { ok = false; break; }
         tc::fence_after();
-        float x[NR];
+        float x[32];
         {
-          const uint32_t s_addr = tmem + lane_base + T::kSCols * sb;
-          uint32_t y[NR];
+          const uint32_t s_addr = tmem + lane_base + T::kSCols * sb + row0;
+          uint32_t y[32];
           tc::ld32(s_addr, y);
           if constexpr (kE4) {
-            uint32_t z[NR];
+            uint32_t z[32];
             tc::ld32(s_addr + NR, z);
             tc::wait_ld();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) x[r] = (__uint_as_float(y[r]) + __uint_as_float(z[r])) * rows[r].scale;
+            for (int r = 0; r < 32; ++r) x[r] = (__uint_as_float(y[r]) + __uint_as_float(z[r])) * rows[r].scale;
           } else {
             tc::wait_ld();
 #pragma unroll
-            for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(y[r]);
+            for (int r = 0; r < 32; ++r) x[r] = __uint_as_float(y[r]);
           }
         }
         tc::fence_before();
@@ -468,13 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
             } else {
               const int d = t - w.base;
 #pragma unroll 4
-              for (int r = 0; r < NR; ++r) vis |= static_cast<uint32_t>((rows[r].drafts >> d) & 1) << r;
+              for (int r = 0; r < 32; ++r) vis |= static_cast<uint32_t>((rows[r].drafts >> d) & 1) << r;
             }
           }
         }
         if (vis != ~0u) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
+          for (int r = 0; r < 32; ++r)
             if (!((vis >> r) & 1)) x[r] = -INFINITY;
         }
         // A thread that asks for a new reference tags the flag of this tile's
@@ -483,32 +507,32 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         const bool first = j == 0;
         if (!first) {
 #pragma unroll
-          for (int r = 0; r < NR; ++r) need |= fmaf(x[r], a.scale_log2, -sm.m[r]) > kRaise;
+          for (int r = 0; r < 32; ++r) need |= fmaf(x[r], a.scale_log2, -sm.m[row0 + r]) > kRaise;
         }
-        if (need) sm.flag[sb] = static_cast<int32_t>(gi + 1);
-        softmax_bar();
+        if (need) sm.flag[grp][sb] = static_cast<int32_t>(gi + 1);
+        softmax_bar(grp);
         bool waited = false;
-        if (first || sm.flag[sb] == static_cast<int32_t>(gi + 1)) {
-          float y[NR];
+        if (first || sm.flag[grp][sb] == static_cast<int32_t>(gi + 1)) {
+          float y[32];
 #pragma unroll
-          for (int r = 0; r < NR; ++r) y[r] = x[r];
-          row_fold<NR, true>(y, lane);
-          if (lane < NR) sm.red[warp][lane] = y[0];
-          softmax_bar();
-          if (tid < NR) {
+          for (int r = 0; r < 32; ++r) y[r] = x[r];
+          row_fold<32, true>(y, lane);
+          sm.red[grp][quad][lane] = y[0];
+          softmax_bar(grp);
+          if (gtid < 32) {
             const float mx =
-                fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]), fmaxf(sm.red[2][tid], sm.red[3][tid])) * a.scale_log2;
-            const float mo = first ? kUnset : sm.m[tid];
+                fmaxf(fmaxf(sm.red[grp][0][gtid], sm.red[grp][1][gtid]), fmaxf(sm.red[grp][2][gtid], sm.red[grp][3][gtid])) * a.scale_log2;
+            const float mo = first ? kUnset : sm.m[row0 + gtid];
             const float mn = mx != -INFINITY && mx > mo + kRaise ? mx - kBelow : mo;
-            sm.m[tid] = mn;
-            sm.alpha[tid] = ex2(mo - mn);
+            sm.m[row0 + gtid] = mn;
+            sm.alpha[row0 + gtid] = ex2(mo - mn);
           }
-          softmax_bar();
+          softmax_bar(grp);
           if (!first) {
             bool rescale = false;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float al = sm.alpha[r];
+            for (int r = 0; r < 32; ++r) {
+              const float al = sm.alpha[row0 + r];
               l_acc[r] *= al;
               rescale |= al != 1.f;
             }
@@ -519,11 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
               tc::fence_after();
 #pragma unroll 1
               for (int c = 0; c < 4 * T::kTerms; ++c) {
-                uint32_t o[NR];
+                uint32_t o[32];
                 tc::ld32(o_addr + NR * c, o);
                 tc::wait_ld();
 #pragma unroll
-                for (int r = 0; r < NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sm.alpha[r]);
+                for (int r = 0; r < 32; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * sm.alpha[row0 + r]);
                 tc::st_cols(o_addr + NR * c, o);
               }
               tc::wait_st();
@@ -532,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
         }
         // p = 2^(s scale - m), rounded for the product; l sums it as rounded, so
         // that numerator and denominator round alike
-        constexpr int kRB = NR / T::kRowsPerBlk;
+        constexpr int kRB = 32 / T::kRowsPerBlk;
         uint32_t words[T::kTerms][kRB][4];
 #pragma unroll
         for (int rb = 0; rb < kRB; ++rb) {
@@ -542,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
               const int r = 16 * rb + 4 * k;
               float p[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(x[r + i], a.scale_log2, -sm.m[r + i]));
+              for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(x[r + i], a.scale_log2, -sm.m[row0 + r + i]));
               uint32_t w3[3];
               float used[4];
               tc::split_e5m2(p[0], p[1], p[2], p[3], w3, used);
@@ -552,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
               for (int t = 0; t < 3; ++t) words[t][rb][k] = w3[t];
             } else {
               const int r = 8 * rb + 2 * k;
-              const float p0 = ex2(fmaf(x[r], a.scale_log2, -sm.m[r]));
-              const float p1 = ex2(fmaf(x[r + 1], a.scale_log2, -sm.m[r + 1]));
+              const float p0 = ex2(fmaf(x[r], a.scale_log2, -sm.m[row0 + r]));
+              const float p1 = ex2(fmaf(x[r + 1], a.scale_log2, -sm.m[row0 + r + 1]));
               __nv_bfloat162 pb = __floats2bfloat162_rn(p0, p1);
               l_acc[r] += __low2float(pb);
               l_acc[r + 1] += __high2float(pb);
@@ -569,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
           for (int t = 0; t < T::kTerms; ++t)
 #pragma unroll
             for (int rb = 0; rb < kRB; ++rb)
-              *reinterpret_cast<uint4*>(dst + (t * kRB + rb) * 128) =
+              *reinterpret_cast<uint4*>(dst + (t * kRB + rb + kRB * grp) * 128) =
                   make_uint4(words[t][rb][0], words[t][rb][1], words[t][rb][2], words[t][rb][3]);
         }
         fence_proxy_async_smem();
@@ -578,50 +602,50 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
       }
       if (!ok) break;
       // ---- epilogue: l over the threads, then O^T by dims
-      row_fold<NR, false>(l_acc, lane);
-      if (lane < NR) sm.red[warp][lane] = l_acc[0];
-      softmax_bar();
-      if (tid < NR) {
-        const float l = ((sm.red[0][tid] + sm.red[1][tid]) + sm.red[2][tid]) + sm.red[3][tid];
-        sm.inv[tid] = w.nc > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
-        if (w.nc > 1 && tid < w.n * HQ)  // once per half of the dims: their parts are apart
+      row_fold<32, false>(l_acc, lane);
+      sm.red[grp][quad][lane] = l_acc[0];
+      softmax_bar(grp);
+      if (gtid < 32) {
+        const float l = ((sm.red[grp][0][gtid] + sm.red[grp][1][gtid]) + sm.red[grp][2][gtid]) + sm.red[grp][3][gtid];
+        sm.inv[row0 + gtid] = w.nc > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
+        if (w.nc > 1 && row0 + gtid < w.n * HQ)  // once per half of the dims: their parts are apart
 #pragma unroll
           for (int half = 0; half < 2; ++half)
-            a.part_ml[(2 * static_cast<int64_t>(u) + half) * a.part_rows + tid] =
-                make_float2(sm.m[tid] == kUnset ? -INFINITY : sm.m[tid], l);
+            a.part_ml[(2 * static_cast<int64_t>(u) + half) * a.part_rows + row0 + gtid] =
+                make_float2(sm.m[row0 + gtid] == kUnset ? -INFINITY : sm.m[row0 + gtid], l);
       }
-      softmax_bar();
+      softmax_bar(grp);
       if (!warp_wait(&sm.o_done, wt & 1, st)) break;
       tc::fence_after();
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {
-        float o[NR];
+        float o[32];
         {
-          uint32_t y[T::kTerms][NR];
+          uint32_t y[T::kTerms][32];
 #pragma unroll
           for (int t = 0; t < T::kTerms; ++t) tc::ld32(o_addr + T::kNT * blk + NR * t, y[t]);
           tc::wait_ld();
 #pragma unroll
-          for (int r = 0; r < NR; ++r) {
+          for (int r = 0; r < 32; ++r) {
             o[r] = __uint_as_float(y[0][r]);
 #pragma unroll
             for (int t = 1; t < T::kTerms; ++t) o[r] += __uint_as_float(y[t][r]);
-            o[r] *= sm.inv[r];
+            o[r] *= sm.inv[row0 + r];
           }
         }
-        const int dim = 128 * blk + 32 * warp + lane, count = w.n * HQ;
+        const int dim = 128 * blk + gtid, count = w.n * HQ;
         if (w.nc > 1) {
           // a part's columns by eights, [8-column block 32][row][8]
           float* part =
               a.part_o + ((2 * static_cast<int64_t>(u) + dim / 256) * 32 + dim % 256 / 8) * a.part_rows * 8 + dim % 8;
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (r < count) part[8 * r] = o[r];
+          for (int r = 0; r < 32; ++r)
+            if (row0 + r < count) part[8 * (row0 + r)] = o[r];
         } else {
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(w.row0) * HQ * 512 + dim;
 #pragma unroll
-          for (int r = 0; r < NR; ++r)
-            if (r < count) out[r * 512] = __float2bfloat16_rn(o[r]);
+          for (int r = 0; r < 32; ++r)
+            if (row0 + r < count) out[(row0 + r) * 512] = __float2bfloat16_rn(o[r]);
         }
       }
     }
@@ -635,13 +659,20 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_kernel(const LocalArg
   }
 }
 
-template <int LAYOUT, int HQ>
-cudaError_t launch_lh(const LocalArgs& a, cudaStream_t st) {
-  auto kern = global_tree_kernel<LAYOUT, HQ>;
-  const size_t smem = sizeof(FSmem<LAYOUT>);
+template <int LAYOUT, int HQ, int NR>
+cudaError_t launch_nr(const LocalArgs& a, cudaStream_t st) {
+  auto kern = global_tree_kernel<LAYOUT, HQ, NR>;
+  const size_t smem = sizeof(FSmem<LAYOUT, NR>);
   cudaError_t e = set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid_ctas()), dim3(kThreads), smem, st, a);
+  return launch_pdl(kern, dim3(grid_ctas()), dim3(FL<LAYOUT, NR>::kThreads), smem, st, a);
+}
+
+template <int LAYOUT, int HQ>
+cudaError_t launch_lh(const LocalArgs& a, cudaStream_t st) {
+  if constexpr (tree_few_rows(LAYOUT) == 64)
+    if (a.max_q_rows * HQ > 32) return launch_nr<LAYOUT, HQ, 64>(a, st);
+  return launch_nr<LAYOUT, HQ, 32>(a, st);
 }
 
 template <int LAYOUT>

@@ -655,7 +655,7 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
   const bool local = pool->layout == GW_LAYOUT_LOCAL;
   const int group = local ? num_q_heads / pool->kv_heads : num_q_heads;
   const int per = kTreeRows / group, copies = local ? pool->kv_heads : 2;
-  const bool few = !local && max_q_rows * group <= kTreeFewRows;
+  const bool few = !local && max_q_rows * group <= tree_few_rows(pool->layout);
   const TreeRule rule = local ? tree_rule_local(group) : few ? tree_rule_few(group) : tree_rule_global(group);
   const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff, rule);
   // the most units of a sequence, over its rows n

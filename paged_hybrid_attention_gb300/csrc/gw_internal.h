@@ -67,7 +67,11 @@ constexpr int kMaxTreeRows = 64;    // rows of a sequence: the bits of a mask wo
 constexpr int kMaxTreeBatch = 256;  // sequences of a call: their plan is in shared memory
 constexpr int kTreeTile = 64;
 constexpr int kTreeRows = 128;    // rows x heads of a block
-constexpr int kTreeFewRows = 32;  // rows x heads up to which a call's rows lie along N
+// Rows x heads up to which a call's rows lie along N: what the accumulators of all
+// dims leave room for, three terms of P wide on e4m3 pools.
+__host__ __device__ constexpr int tree_few_rows(int layout) {
+  return layout == GW_LAYOUT_GLOBAL_FOLDED || layout == GW_LAYOUT_GLOBAL_FULL ? 64 : 32;
+}
 constexpr int kTreeMaxChunks = 76;
 
 // How a call is cut: `per` rows in a block, chunks of at most `aim` tiles, at most

@@ -40,7 +40,7 @@ def test_local_windows(window, dtype, rows):
 
 @pytest.mark.parametrize("layout", ["folded", "full", "folded_e4m3"])
 @pytest.mark.parametrize("heads", [8, 16, 32])
-@pytest.mark.parametrize("most", [32, 2048])
+@pytest.mark.parametrize("most", [32, 64, 2048])
 def test_global_edges(layout, heads, most):
     c = Case(layout, at_most(EDGES, most // heads), heads, seed=heads)
     c.run()
@@ -48,7 +48,8 @@ def test_global_edges(layout, heads, most):
 
 
 @pytest.mark.parametrize("layout,rows", [("local", 4), ("local", 8), ("local", 64), ("folded", 64), ("full", 64),
-                                         ("folded_e4m3", 64), ("folded", 4), ("full", 4), ("folded_e4m3", 4)])
+                                         ("folded_e4m3", 64), ("folded", 4), ("full", 4), ("folded_e4m3", 4),
+                                         ("folded", 8), ("full", 8), ("folded_e4m3", 8)])
 def test_any_words(layout, rows):
     """Words that are no trees, rows that see no draft, and sequences without a cache before them."""
     c = Case(layout, at_most([(7, 7), (64, 64), (200, 30), (33, 1), (1, 1), (1100, 5)], rows), 8,
@@ -62,7 +63,9 @@ def test_any_words(layout, rows):
 
 @pytest.mark.parametrize("layout,heads,n", [("folded", 32, 5), ("folded", 8, 17), ("full", 16, 9), ("folded_e4m3", 32, 4),
                                             ("folded_e4m3", 8, 64), ("folded", 8, 4), ("folded", 32, 1),
-                                            ("full", 16, 2), ("folded_e4m3", 8, 3), ("folded_e4m3", 32, 1)])
+                                            ("full", 16, 2), ("folded_e4m3", 8, 3), ("folded_e4m3", 32, 1),
+                                            ("folded", 32, 2), ("folded", 8, 7), ("full", 16, 4), ("full", 32, 2),
+                                            ("folded", 16, 3), ("folded_e4m3", 32, 2)])
 def test_global_chunks(layout, heads, n):
     """Several chunks, an odd last one among them."""
     c = Case(layout, [(511, n), (513, n), (2600, n), (1024 + n, n)], heads, seed=n)
@@ -72,7 +75,8 @@ def test_global_chunks(layout, heads, n):
 
 @pytest.mark.parametrize("layout,dtype,rows", [("local", "bf16", 40), ("local", "bf16", 4), ("local", "e4m3", 40),
                                                ("local", "e4m3", 4), ("folded", "bf16", 40), ("folded", "bf16", 3),
-                                               ("full", "bf16", 4), ("folded_e4m3", "", 40), ("folded_e4m3", "", 4)])
+                                               ("full", "bf16", 4), ("folded_e4m3", "", 40), ("folded_e4m3", "", 4),
+                                               ("folded", "bf16", 8), ("full", "bf16", 7)])
 def test_long_chunks(layout, dtype, rows):
     """Sequences with as many chunks as there may be, and longer ones; rows in many blocks."""
     L = 46000 if layout == "local" else 80000
@@ -83,7 +87,7 @@ def test_long_chunks(layout, dtype, rows):
 
 @pytest.mark.parametrize("layout,dtype", [("local", "bf16"), ("local", "e4m3"), ("folded", "bf16"), ("full", "bf16"),
                                           ("folded_e4m3", "")])
-@pytest.mark.parametrize("rows", [2, 4, 10])
+@pytest.mark.parametrize("rows", [2, 4, 8, 10])
 def test_sharp_logits(layout, dtype, rows):
     """Logits of standard deviation 30: references rise and rows are rescaled."""
     c = Case(layout, at_most([(600, 10), (1500, 3)], rows), 8, 1, dtype or "bf16",
@@ -99,7 +103,7 @@ def test_sharp_logits(layout, dtype, rows):
 
 
 @pytest.mark.parametrize("layout,dtype", [("local", "e4m3"), ("folded_e4m3", ""), ("local", "bf16"), ("folded", "bf16")])
-@pytest.mark.parametrize("n", [2, 4, 9])
+@pytest.mark.parametrize("n", [2, 4, 8, 9])
 def test_long_tail(layout, dtype, n):
     """One token 2^11.5 above each of 1100 others: their weights together are a third of its own, and one
     by one below the smallest e4m3 number."""
@@ -219,7 +223,7 @@ def test_max_batch_and_idle_slots():
     plan = [((b * 37) % 150 + 5, b % 4) for b in range(256)]
     for layout, kv, window in (("local", 1, 40), ("folded", 1, 0)):
         c = Case(layout, plan, 8, kv, window=window, seed=12)
-        for most in (3, 20):  # few rows and many
+        for most in (3, 8, 20):  # few rows and many
             c.run(max_q_rows=most)
             c.check()
 

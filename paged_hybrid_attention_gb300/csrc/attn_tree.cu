@@ -13,15 +13,23 @@
 namespace gw {
 namespace {
 
-// A block merges 32 of the 256 dims of 32 rows of a unit, a lane a row: parts lie
-// as [unit][8-column block 32][row][8], so that what a warp stores or reads at a
-// time is 1 KB in one piece.  The rows' weights are put in shared memory first; a
-// warp then takes a column block.  Chunks are added in order, so a row does not
-// depend on its companions.  kLocal: units are (KV head, chunk, row block), else
-// (chunk, row block, half of the dims).  Latency-bound: with (m, l) read chunk by
-// chunk instead of at once, 8 x 131072 tokens, 8 heads, 4 drafts took 262 us
-// instead of 252, the full layout at 4 x 131072 196 instead of 183.
-constexpr int kMergeWarps = 4;
+// A warp merges 8 of the 256 dims of 32 rows of a unit, a lane a row: parts lie as
+// [unit][8-column block 32][row][8], so that what a warp stores or reads at a time
+// is 1 KB in one piece.  The rows' weights are put in shared memory first.  Every
+// fourth chunk has a sum of its own and the four are added in a fixed order, so that
+// a row depends neither on its companions nor on kSplit: 4, a warp to each sum, where
+// the warps of kSplit = 1 would be few.  kLocal: units are (KV head, chunk, row
+// block), else (chunk, row block, half of the dims).
+//
+// 8 x 131072 tokens, 8 heads, 4 drafts (512 warps with kSplit = 1, 76 chunks): the
+// call 231 us with 4, 254 with 1; 4 x 131072, full layout, 169 and 183.  16 sequences
+// of 512 to 8192 tokens, 16 drafts, 32 heads (16384 warps, up to 4 chunks): 173 and
+// 129.
+template <int kSplit>
+struct Merge {
+  static constexpr int kWarps = kSplit == 1 ? 4 : 8;
+  static constexpr int kCols = kWarps / kSplit;  // 8-column blocks of a block
+};
 
 __device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
   asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -29,18 +37,19 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
                : "l"(p));
 }
 
-template <bool kLocal>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const LocalArgs a, int group, int copies,
-                                                                      int blocks, const TreeRule rule, int scale) {
+template <bool kLocal, int kSplit>
+__global__ void __launch_bounds__(Merge<kSplit>::kWarps * 32, kSplit == 1 ? 1 : 2)
+    tree_merge_kernel(const LocalArgs a, int group, int copies, int blocks, const TreeRule rule, int scale) {
+  constexpr int kMergeWarps = Merge<kSplit>::kWarps, kMergeCols = Merge<kSplit>::kCols;
   __shared__ float w[kTreeMaxChunks][32], wl[kTreeMaxChunks][32];
-  __shared__ float top[kMergeWarps][32];
+  __shared__ float top[kMergeWarps][32], sums[kSplit == 1 ? 1 : kMergeWarps][8][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int groups = (a.part_rows + 31) / 32;  // of 32 rows, in a unit
   int task = blockIdx.x;
-  const int c8 = task % (32 / kMergeWarps) * kMergeWarps + warp;
-  task /= 32 / kMergeWarps;
+  const int c8 = task % (32 / kMergeCols) * kMergeCols + warp / kSplit;
+  task /= 32 / kMergeCols;
   const int pg = task % groups;
   task /= groups;
   const int qb = task % blocks;
@@ -58,7 +67,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   const int64_t u0 = ub + (kLocal ? copy * nc * sp.blocks + qb : qb * 2 + copy);
   const int64_t step = (kLocal ? sp.blocks : 2 * sp.blocks) * static_cast<int64_t>(a.part_rows);
   const float2* ml = a.part_ml + u0 * a.part_rows + place;
-  // a warp takes every fourth chunk's (m, l), all its loads in flight at once
+  // a warp takes every kMergeWarps-th chunk's (m, l), all its loads in flight at once
   constexpr int kMine = (kTreeMaxChunks + kMergeWarps - 1) / kMergeWarps;
   float2 mine[kMine];
 #pragma unroll
@@ -89,36 +98,76 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Loca
   float den = 0.f;
 #pragma unroll 4
   for (int c = 0; c < nc; ++c) den += wl[c][lane];
-  if (!ok) return;
   const float inv = den == 0.f ? 0.f : 1.f / den;  // NaN where a chunk's sum is
+  constexpr int kMine4 = 4 / kSplit;  // of the four sums
+  float acc[kMine4][8];
+#pragma unroll
+  for (int i = 0; i < kMine4; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
+  if (ok) {
+    const float* po = a.part_o + ((u0 * 32 + c8) * a.part_rows + place) * 8;
+    auto add = [&](int c, float (&to)[8]) {
+      float x[8];
+      load_f32x8(po + c * step * 256, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) to[k] = fmaf(w[c][lane], x[k], to[k]);
+    };
+    if constexpr (kSplit == 1) {
+      int c = 0;
+#pragma unroll 4
+      for (; c + 4 <= nc; c += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add(c + i, acc[i]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (c + i < nc) add(c + i, acc[i]);
+    } else {
+#pragma unroll 8
+      for (int c = warp % 4; c < nc; c += 4) add(c, acc[0]);
+    }
+  }
+  float sum[8];
+  if constexpr (kSplit == 1) {
+    if (!ok) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = (acc[0][k] + acc[1][k]) + (acc[2][k] + acc[3][k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[warp][k][lane] = acc[0][k];
+    __syncthreads();
+    if (!ok || warp % 4) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      sum[k] = (acc[0][k] + sums[warp + 1][k][lane]) + (sums[warp + 2][k][lane] + sums[warp + 3][k][lane]);
+  }
   const int head = kLocal ? copy * group + place % group : place % group;
   uint16_t* dst = a.out + ((static_cast<int64_t>(row0) + q) * a.num_q_heads + head) * (kLocal ? 256 : 512) +
                   (kLocal ? 0 : 256 * copy);
-  const float* po = a.part_o + ((u0 * 32 + c8) * a.part_rows + place) * 8;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 16
-  for (int c = 0; c < nc; ++c) {
-    float x[8];
-    load_f32x8(po + c * step * 256, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[c][lane], x[k], acc[k]);
-  }
   uint32_t pk[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    __nv_bfloat162 b = __floats2bfloat162_rn(sum[2 * k] * inv, sum[2 * k + 1] * inv);
     pk[k] = *reinterpret_cast<uint32_t*>(&b);
   }
   *reinterpret_cast<uint4*>(dst + 8 * c8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
 }
 
+template <bool kLocal, int kSplit>
+cudaError_t launch_merge_split(const LocalArgs& a, int group, int copies, int blocks, int64_t columns,
+                               const TreeRule& rule, int scale, cudaStream_t st) {
+  using M = Merge<kSplit>;
+  return launch_pdl(tree_merge_kernel<kLocal, kSplit>, dim3(static_cast<unsigned>(columns / M::kCols)),
+                    dim3(M::kWarps * 32), 0, st, a, group, copies, blocks, rule, scale);
+}
+
 template <bool kLocal>
 cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, int scale, cudaStream_t st) {
   const int copies = kLocal ? a.kv_heads : 2, blocks = (a.max_q_rows + rule.per - 1) / rule.per;
-  const int64_t grid =
-      static_cast<int64_t>(a.batch) * copies * blocks * ((a.part_rows + 31) / 32) * (32 / kMergeWarps);
-  return launch_pdl(tree_merge_kernel<kLocal>, dim3(static_cast<unsigned>(grid)), dim3(kMergeWarps * 32), 0, st, a,
-                    group, copies, blocks, rule, scale);
+  // column blocks of 32 rows in the call: split where they are fewer than about 27 an SM
+  const int64_t columns = static_cast<int64_t>(a.batch) * copies * blocks * ((a.part_rows + 31) / 32) * 32;
+  return columns < 4096 ? launch_merge_split<kLocal, 4>(a, group, copies, blocks, columns, rule, scale, st)
+                        : launch_merge_split<kLocal, 1>(a, group, copies, blocks, columns, rule, scale, st);
 }
 
 }  // namespace

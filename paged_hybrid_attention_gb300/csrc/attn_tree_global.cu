@@ -322,10 +322,16 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         if (key0 + kTok - 1 > w.hi || vmask != (1 << kPages) - 1) {
           // V rows behind the last key (K rows there only made logits that were
           // masked) or of pages not loaded: zero weights must meet finite values
-          for (int k = 0; k < kTok; ++k)
-            if (key0 + k > w.hi || !((vmask >> (k / kPage)) & 1))
-              for (int cb = lane; cb < 4 * kDimBlks; cb += 32)
-                zero16(ta + ((k >> 3) * T::kBlk + T::kVcb + cb) * 128 + (k & 7) * 16);
+          // (8-token blocks from their 16-byte pieces' start: a row's pieces share banks)
+          const int k = lane & 7;
+          for (int blk = 0; blk < kTok / 8; ++blk) {
+            const bool page_ok = (vmask >> (blk / 2)) & 1;
+            if (page_ok && key0 + 8 * blk + 7 <= w.hi) continue;
+            if (!page_ok || key0 + 8 * blk + k > w.hi)
+#pragma unroll
+              for (int cb = 0; cb < 4 * kDimBlks; cb += 4)
+                zero16(ta + (blk * T::kBlk + T::kVcb + cb + (lane >> 3)) * 128 + k * 16);
+          }
           fence_proxy_async_smem();
           __syncwarp();
         }

@@ -382,9 +382,13 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         if (key0 + KN > w.k1) {
           // V rows behind the last key (K rows there only made logits that were
           // masked): zero weights must meet finite values
-          for (int k = max(w.k1 - key0, 0); k < KN; ++k)
-            for (int cb = lane; cb < Parts<LAYOUT>::kV; cb += 32)
-              zero16(ta + ((k >> 3) * T::kBlk + Parts<LAYOUT>::v0(w.half) + cb) * 128 + (k & 7) * 16);
+          // (8-token blocks from their 16-byte pieces' start: a row's pieces share banks)
+          const int k = lane & 7;
+          for (int blk = max(w.k1 - key0, 0) / 8; blk < KN / 8; ++blk)
+            if (key0 + 8 * blk + k >= w.k1)
+#pragma unroll
+              for (int cb = 0; cb < Parts<LAYOUT>::kV; cb += 4)
+                zero16(ta + (blk * T::kBlk + Parts<LAYOUT>::v0(w.half) + cb + (lane >> 3)) * 128 + k * 16);
           fence_proxy_async_smem();
           __syncwarp();
         }

@@ -363,13 +363,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
       const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       const uint16_t* src = a.q + static_cast<int64_t>(w.row0) * HQ * 512;
       const int count = w.n * HQ, first = 8 * (warp - 8);
-      // rows behind the last see everything, which costs no masks; nobody reads them
-      TreeRow row[T::kGroups];
-#pragma unroll
-      for (int g = 0; g < T::kGroups; ++g) {
-        const int r = 32 * g + first + (lane & 7);
-        row[g] = r < count ? tree_row(a, w.row0, r / HQ, w.n, w.base, false) : TreeRow{~0ull, 0, 1.f};
-      }
+      float scale = 1.f;
       if constexpr (kE4) {
         // each row's largest |q|
 #pragma unroll 4
@@ -388,13 +382,13 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
           const int e = min(125, max(-125, 7 - ex));
           // (an infinity, which the terms cannot hold, makes the row's logits NaN)
           if ((lane & 7) == k)
-            row[0].scale = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
+            scale = mq < INFINITY ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : NAN;
         }
       } else {
         // into L2 while the unit before is at work
 #pragma unroll
         for (int g = 0; g < T::kGroups; ++g)
-          if (lane < 8 && 32 * g + first + lane < count) prefetch_l2(src + (32 * g + first + lane) * 512, 1024);
+          if (wt > 0 && lane < 8 && 32 * g + first + lane < count) prefetch_l2(src + (32 * g + first + lane) * 512, 1024);
       }
       if (wt > 0 && !warp_wait(&sm.q_free, (wt - 1) & 1, st)) break;
 #pragma unroll
@@ -403,7 +397,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         const bool ok_row = r < count;
         const uint16_t* from = src + (ok_row ? r : 0) * 512;
         if constexpr (kE4) {
-          const float up = 1.f / row[0].scale;  // a power of two: exact
+          const float up = 1.f / scale;  // a power of two: exact
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int cb = (lane >> 3) + 4 * j;
@@ -435,8 +429,18 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
               zero16(at);
           }
         }
-        if (lane < 8) sm.rows[wt % kRowRing][r] = row[g];
       }
+      // what the rows see, its load beside those of Q; rows behind the last see
+      // everything, which costs no masks: nobody reads them
+      if (lane < 8)
+#pragma unroll
+        for (int g = 0; g < T::kGroups; ++g) {
+          const int r = 32 * g + first + lane;
+          TreeRow row{~0ull, 0, 1.f};
+          if (r < count) row = tree_row(a, w.row0, r / HQ, w.n, w.base, false);
+          row.scale = scale;
+          sm.rows[wt % kRowRing][r] = row;
+        }
       if constexpr (!kE4) {
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -496,9 +500,10 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
             if (t < w.base) {
               vis = ~0u;
             } else {
-              const int d = t - w.base;
-#pragma unroll 4
-              for (int r = 0; r < 32; ++r) vis |= static_cast<uint32_t>((rows[r].drafts >> d) & 1) << r;
+              const int d = t - w.base;  // a draft's heads see the same
+              constexpr uint32_t kHeads = HQ == 32 ? ~0u : (1u << (HQ % 32)) - 1;
+#pragma unroll
+              for (int r = 0; r < 32; r += HQ) vis |= ((rows[r].drafts >> d) & 1 ? kHeads : 0u) << r;
             }
           }
         }

@@ -480,13 +480,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = key0 + tok;
           vis = 0;
           if (active && t >= w.lo && t <= w.hi) {
+            constexpr uint32_t kHeads = (1u << G) - 1;  // a draft's heads see the same
             if (t < w.base) {
-#pragma unroll 4
-              for (int r = 0; r < NR; ++r) vis |= static_cast<uint32_t>(t >= rows[r].kmin) << r;
+#pragma unroll 8
+              for (int r = 0; r < NR; r += G) vis |= (t >= rows[r].kmin ? kHeads : 0u) << r;
             } else {
               const int d = t - w.base;
-#pragma unroll 4
-              for (int r = 0; r < NR; ++r) vis |= static_cast<uint32_t>((rows[r].drafts >> d) & 1) << r;
+#pragma unroll 8
+              for (int r = 0; r < NR; r += G) vis |= ((rows[r].drafts >> d) & 1 ? kHeads : 0u) << r;
             }
           }
         }

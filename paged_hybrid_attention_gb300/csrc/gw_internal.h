@@ -85,10 +85,14 @@ struct TreeRule {
 __host__ __device__ constexpr TreeRule tree_rule_local(int group) { return {kTreeRows / group, 18, 38}; }
 // Global layers, rows along M: units (two a chunk and block) enough for the GPU's
 // 152 SMs, few enough that their parts, 128 KB a unit, stay small beside the cache
-// (8 x 131072 tokens, one block: with 64 chunks the merge took 46 us instead of 30,
-// the call 466 instead of 414).
-__host__ __device__ constexpr TreeRule tree_rule_global(int heads) { return {kTreeRows / heads, 32, 38}; }
-// Global layers, rows along N: one unit of 64 KB of parts a chunk.
+// (8 x 131072 tokens, one block: 367 us with up to 38 chunks, 404 with 76; 344 with
+// 19, which would leave a lone sequence a fourth of the SMs).  Chunks of 40 tiles: 16
+// sequences of 512 to 8192 tokens, four blocks, 121 us, of 32 130, of 24 131, of 56 133.
+__host__ __device__ constexpr TreeRule tree_rule_global(int heads) { return {kTreeRows / heads, 40, 38}; }
+// Global layers, rows along N: one unit of 64 or 128 KB of parts a chunk (8 x 131072
+// tokens, 4 drafts of 8 heads: 224 us with up to 38 chunks instead of 231, but a lone
+// sequence has as many SMs as chunks).  One sequence of 8192 tokens: chunks of 8
+// tiles 23 us, of 6 20, of 12 26; 16 of 512 to 8192: 30, 40 and 35.
 __host__ __device__ constexpr TreeRule tree_rule_few(int heads) { return {kTreeRows / heads, 8, kTreeMaxChunks}; }
 
 __host__ __device__ __forceinline__ int tree_most_chunks(const TreeRule& rule, int blocks) {

@@ -115,7 +115,7 @@ def _chunks(tiles, aim, most, blocks):
 def test_workspace_holds_every_step(layout, heads, kvh, window, pages, rows):
     """No mix of rows and lengths up to the bounds needs more units than the workspace holds."""
     local = layout == gw.LAYOUT_LOCAL
-    group, copies, aim, most = (heads // kvh, kvh, 18, 38) if local else (heads, 2, 32, 38)
+    group, copies, aim, most = (heads // kvh, kvh, 18, 38) if local else (heads, 2, 40, 38)
     if not local and rows * heads <= 64:
         aim, most = 8, 76
     got = gw.lib().gw_tree_workspace_bytes(ctypes.byref(_desc(layout, kvh=kvh, base=0)), heads, 3, pages, rows, window)

@@ -13,9 +13,10 @@
 // the e4m3 pool, whose MMAs bound a call, 128 (8 x 131072 tokens, 8 heads, 4 drafts:
 // 203 us with tiles of 64 and 193 with 128).
 //
-// 8 x 131072 tokens, 8 heads, 4 drafts: folded 254 us (0.78 of the copy rate), e4m3
-// 176 (0.56); full layout, 4 x 131072, 183 (0.86).  8 drafts: folded 341 us (0.58;
-// in attn_tree_global_rows.cu 435), full 205 (0.77; 256).
+// 8 x 131072 tokens, 8 heads, 4 drafts: folded 230 us with the merge (0.86 of the copy
+// rate), e4m3 143 (0.69); full layout, 4 x 131072, 167 (0.94).  8 drafts: folded 309
+// us (0.64, bound by the MMAs' and the softmax's chain over two tiles; in
+// attn_tree_global_rows.cu 435), full 176 (0.90; 256).
 //
 // A tile is whole pages of 8-token x 16-byte blocks, which are UMMA core matrices:
 // the K-major A operand of Q.K^T, whose K-steps point at k_rot and V on folded

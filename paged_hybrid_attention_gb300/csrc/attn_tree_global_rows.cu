@@ -21,8 +21,8 @@
 //
 // What bounds it: the chain copy, Q.K^T, softmax, P.V over two tile buffers, 1.40 us a
 // tile of which the MMAs are 1.15 (folded); on the e4m3 pool the MMAs of q's two
-// terms, 43 ns each, 1.45 us a tile.  8 x 131072 tokens, 4 rows x 32 heads: 376 us
-// (one block; the cache alone 197); 33 rows x 16 heads, e4m3, 8 x 16384 to 32768: 412.
+// terms, 43 ns each, 1.45 us a tile.  8 x 131072 tokens, 4 rows x 32 heads: 366 us
+// (one block; the cache alone 197); 33 rows x 16 heads, e4m3, 8 x 16384 to 32768: 408.
 //
 // Warp roles (384 threads): warps 0-3 softmax (a thread owns a row), 4-7 Q rows
 // and epilogue, 8 and 11 copies, 9 issues Q.K^T and owns tensor memory, 10 issues

@@ -176,7 +176,7 @@ cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, in
 // along M.  Local, 16 sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16:
 // 16 drafts 49 us (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows,
 // 100.6); 61 e4m3 sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8
-// heads: 4 drafts 230 us (along M 432), 8 drafts 309 (435); 1 x 8192, 8 drafts 32
+// heads: 4 drafts 222 us (along M 432), 8 drafts 309 (435); 1 x 8192, 8 drafts 32
 // (54); 2 sequences of 37 and 100 tokens, full layout, 5 drafts 11.7 both ways.  The
 // rule is the call's bound, so that a captured call stays what it is.
 //

@@ -8,12 +8,14 @@
 //   S^T[T x NR]    = K_tile[T x 512] . Q^T       (UMMA M = 64, e4m3 128)
 //   O^T[512 x NR] += V_tile^T[512 x T] . P^T     (UMMA M = 128, four times)
 // so that the cache is read once and no logit computed twice (rows along M fill 128
-// of them and make each half of the output dims compute all logits).  T is 64
-// tokens; on folded pools 48 beside 64 rows of Q, two tiles in shared memory; on
-// the e4m3 pool, whose MMAs bound a call, 128 (8 x 131072 tokens, 8 heads, 4 drafts:
-// 203 us with tiles of 64 and 193 with 128).
+// of them and make each half of the output dims compute all logits).  T is 48 tokens
+// on folded pools, three tiles in shared memory beside 32 rows of Q (8 x 131072
+// tokens, 8 heads, 4 drafts: 222 us, two tiles of 64 tokens 231) and two beside 64
+// (309 us with 8 drafts, three of 32 tokens 316); on the full layout 64; on the e4m3
+// pool, whose MMAs bound a call, 128 (203 us with tiles of 64 and 193 with 128 at
+// that step).
 //
-// 8 x 131072 tokens, 8 heads, 4 drafts: folded 230 us with the merge (0.86 of the copy
+// 8 x 131072 tokens, 8 heads, 4 drafts: folded 222 us with the merge (0.89 of the copy
 // rate), e4m3 143 (0.69); full layout, 4 x 131072, 167 (0.94).  8 drafts: folded 309
 // us (0.64, bound by the MMAs' and the softmax's chain over two tiles; in
 // attn_tree_global_rows.cu 435), full 176 (0.90; 256).
@@ -51,8 +53,8 @@ struct FT;
 template <int NR>
 struct FT<GW_LAYOUT_GLOBAL_FOLDED, NR> {
   static constexpr bool kE4 = false, kApart = false;
-  static constexpr int kPages = NR == 32 ? 4 : 3;  // of a tile: two tiles beside Q
-  static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0, kBufs = 2, kSteps = 32;
+  static constexpr int kPages = 3;  // of a tile
+  static constexpr int kPageBytes = 20480, kBlk = 80, kVcb = 0, kBufs = NR == 32 ? 3 : 2, kSteps = 32;
   __device__ static constexpr int k_cb(int ks) { return ks < 8 ? 64 + 2 * ks : 2 * ks; }
 };
 template <int NR>

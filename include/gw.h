@@ -667,7 +667,10 @@ gw_status gw_tree_attn_global(const gw_kv_pool* pool, const void* q, void* out, 
                               void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* Workspace bytes of a gw_tree_attn_local (window >= 1) or gw_tree_attn_global
- * (window ignored) call of at most this size; 0 on an invalid description. */
+ * (window ignored) call of at most this size, on this pool: no more heads,
+ * sequences, pages a sequence, rows and window.  0 on an invalid description.
+ * (A call may need less: with fewer rows a global one cuts the cache into more
+ * chunks, which is counted here.) */
 size_t gw_tree_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int32_t batch, int32_t max_pages_per_seq,
                                int32_t max_q_rows, int32_t window);
 

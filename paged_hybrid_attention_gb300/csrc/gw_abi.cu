@@ -658,10 +658,10 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
   const bool few = !local && max_q_rows * group <= tree_few_rows(pool->layout);
   const TreeRule rule = local ? tree_rule_local(group) : few ? tree_rule_few(group) : tree_rule_global(group);
   const int chunks = tree_max_chunks(max_pages, max_q_rows, local ? window : 0x7fffffff, rule);
-  // the most units of a sequence, over its rows n
+  // the most units of a sequence, over the blocks of its rows
   int64_t units = 0;
-  for (int n = 1; n <= max_q_rows; ++n) {
-    const int blocks = ceil_div(n, per), most = tree_most_chunks(rule, blocks);
+  for (int blocks = 1; blocks <= ceil_div(max_q_rows, per); ++blocks) {
+    const int most = tree_most_chunks(rule, blocks);
     const int64_t u = static_cast<int64_t>(blocks) * (chunks < most ? chunks : most);
     if (u > units) units = u;
   }
@@ -677,6 +677,27 @@ static TreeLayout tree_layout(const gw_kv_pool* pool, int num_q_heads, int batch
   l.o = l.ml + round_up(static_cast<size_t>(units) * l.part_rows * 8, 256);
   l.total = l.o + round_up(static_cast<size_t>(units) * l.part_rows * 256 * 4, 256);
   return l;
+}
+
+// What a call of this size or any smaller one needs.  With fewer rows or heads a
+// global call takes the kernel that has them along N, whose chunks are shorter and
+// more: 8 heads over 2560 tokens, 64 rows have one chunk and 4 rows 5.  For one
+// count of heads and one kernel the need grows with the rows, so that the most rows
+// of each kernel are enough.
+static size_t tree_bytes(const gw_kv_pool* pool, int num_q_heads, int batch, int max_pages, int max_q_rows,
+                         int window) {
+  const bool local = pool->layout == GW_LAYOUT_LOCAL;
+  const int kv = local ? pool->kv_heads : 1, few = tree_few_rows(pool->layout);
+  size_t most = 0;
+  for (int group = local ? 1 : 8; group <= num_q_heads / kv; group *= 2) {
+    auto need = [&](int rows) {
+      const size_t n = tree_layout(pool, group * kv, batch, max_pages, rows, window).total;
+      if (n > most) most = n;
+    };
+    need(max_q_rows);
+    if (!local && max_q_rows * group > few) need(few / group);
+  }
+  return most;
 }
 
 // The geometry that a gw_tree_attn_* call and its workspace share.
@@ -709,7 +730,7 @@ size_t gw_tree_workspace_bytes(const gw_kv_pool* pool, int32_t num_q_heads, int3
   g_err[0] = 0;
   if (check_pool(pool, fn, false) != GW_OK) return 0;
   if (check_tree(fn, pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window) != GW_OK) return 0;
-  return tree_layout(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window).total;
+  return tree_bytes(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window);
 }
 
 static gw_status tree_attn(const char* fn, bool local, const gw_kv_pool* pool, const void* q, void* out,

@@ -643,8 +643,11 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  * the sequence's rows of that KV head, as zero weights multiply it.
  * A row is bit-identical whatever else is in the batch (for the same window and
  * max_q_rows).
- * An infinity or NaN in a row of q makes that row and head NaN, one in a K row
- * the rows that see it.
+ * Logits that are not finite: a NaN or plus infinity that a row sees makes that
+ * row and head NaN; minus infinity has weight 0, and a row all of whose logits
+ * are minus infinity is zeros, as one that sees nothing.  So an infinity in q or
+ * K acts by its sign and the other's (times 0 it is NaN); on e4m3 pools, whose
+ * products cannot hold it, one in q makes that row and head NaN.
  * bf16 and e4m3 pools.  batch at most 256.
  * Errors: those of gw_decode_attn_local; GW_ERR_INVALID_ARG (tree_mask or pos
  * NULL or misaligned, max_q_rows outside [1, 64], max_pages_per_seq of 2^26 or

@@ -34,20 +34,14 @@
 // Every wait is bounded (GW_DEV_TIMEOUT).
 #include <type_traits>
 
-#include "plan.cuh"
-#include "tcgen05.cuh"
+#include "attn_tree.cuh"
 
 namespace gw {
 namespace {
 
 constexpr int kM = 128;
 constexpr int kThreads = 384;
-// O is rescaled when a logit exceeds the reference by more than kLazy; on the
-// e4m3 pool a new reference lies kBelowMax below its logit, so that weights
-// reach 2^15 and a long tail counts down to 2^-23 of the largest.
-constexpr float kLazy = 8.f, kBelowMax = 7.f;
 constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
-constexpr int kRowRing = 4;  // units whose rows' keys are in shared memory
 
 template <int LAYOUT>
 struct TL;
@@ -128,9 +122,6 @@ static_assert(sizeof(TSmem<GW_LAYOUT_GLOBAL_FOLDED_E4M3>) <= 232448, "shared mem
 __device__ __forceinline__ uint32_t cm_off(int r, int c, int chunks) {
   return static_cast<uint32_t>(((r >> 3) * chunks + c) * 128 + (r & 7) * 16);
 }
-__device__ __forceinline__ void zero16(uint32_t dst) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
-}
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -138,18 +129,6 @@ __device__ __forceinline__ void store_f32x8(float* dst, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
                "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                : "memory");
-}
-
-// x as two e4m3 terms, hi = e4m3(x) and lo = e4m3(x - hi), two values at a time.
-__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-  const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3)));
-  hi = h2;
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
 struct Unit {

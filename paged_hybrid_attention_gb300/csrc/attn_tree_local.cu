@@ -30,8 +30,7 @@
 // Bound by memory: 16 sequences of 512 to 8192 tokens, 16 drafts, 16 KV heads of 2,
 // window 1024, 49 us (0.82 of the copy rate); e4m3, 61 sequences, 7 drafts 91 us
 // (0.86); 64 sequences, 4 drafts 158 us (0.99).
-#include "plan.cuh"
-#include "tcgen05.cuh"
+#include "attn_tree.cuh"
 #include "tma.cuh"
 
 namespace gw {
@@ -39,12 +38,7 @@ namespace {
 
 constexpr int kThreads = 288;
 constexpr int kStages = 3;   // K and V tiles in shared memory, each
-constexpr int kRowRing = 4;  // units whose rows' keys are in shared memory
 constexpr int kTileBytes = 32768;
-// O is rescaled when a logit exceeds the reference by more than kLazy; on e4m3
-// pools a new reference lies kBelowMax below its logit, so that weights reach
-// 2^15 and a long tail counts down to 2^-23 of the largest.
-constexpr float kLazy = 8.f, kBelowMax = 7.f;
 constexpr float kUnset = -1e38f;  // reference of a row that has seen no key
 
 template <int DT, int NR>
@@ -81,13 +75,7 @@ struct LSmem {
 static_assert(sizeof(LSmem<GW_KV_BF16, 32>) <= 232448, "shared memory of one CTA");
 static_assert(sizeof(LSmem<GW_KV_E4M3, 32>) <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
-}
 __device__ __forceinline__ void softmax_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ void zero16(uint32_t dst) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
-}
 // Zero the rows r of a K or V stage for which want(r).
 template <class T, class Want>
 __device__ __forceinline__ void zero_rows(uint32_t base, int lane, Want want) {
@@ -98,32 +86,9 @@ __device__ __forceinline__ void zero_rows(uint32_t base, int lane, Want want) {
   }
 }
 
-// x as two e4m3 terms, hi = e4m3(x) and lo = e4m3(x - hi), two values at a time.
-__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-  const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3)));
-  hi = h2;
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
-}
-
 // x[r] of row r reduced over a warp's lanes, lane l getting row l % NR's: lanes
 // 16 apart first, then, each lane keeping half of its rows, 8, 4, 2 and 1, so that
 // the order is the same for 16 rows and 32.  x is used up.
-template <int N, bool kMax>
-__device__ __forceinline__ void row_fold(float* x, int lane) {
-  if constexpr (N > 1) {
-    constexpr int H = N / 2;
-    const bool up = lane & H;
-#pragma unroll
-    for (int i = 0; i < H; ++i) {
-      const float send = up ? x[i] : x[i + H];
-      const float keep = up ? x[i + H] : x[i];
-      const float recv = __shfl_xor_sync(0xffffffffu, send, H);
-      x[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-    }
-    row_fold<H, kMax>(x, lane);
-  }
-}
 template <int NR, bool kMax>
 __device__ __forceinline__ float row_reduce(float (&x)[NR], int lane) {
   if constexpr (NR == 16) {

@@ -33,8 +33,7 @@
 // Warp roles (384 threads): 0-3 softmax, 4-7 Q rows and epilogue, 8 and 9 copies
 // of K and V, 10 issues Q.K^T (and owns tensor memory), 11 issues P.V.  Every
 // wait is bounded (GW_DEV_TIMEOUT).
-#include "plan.cuh"
-#include "tcgen05.cuh"
+#include "attn_tree.cuh"
 #include "tma.cuh"
 
 namespace gw {
@@ -45,11 +44,6 @@ constexpr int kThreads = 384;
 constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
 constexpr uint32_t kPlane = kN * 128;  // one 128-byte chunk column of a tile
 constexpr int kStages = 3;             // K and V tiles in shared memory, each
-constexpr int kRowRing = 4;            // units whose rows' keys are in shared memory
-// O is rescaled when a logit exceeds the reference by more than kLazy; on e4m3
-// pools a new reference lies kBelowMax below its logit, so that weights reach
-// 2^15 and a long tail counts down to 2^-23 of the largest.
-constexpr float kLazy = 8.f, kBelowMax = 7.f;
 
 template <int DT>
 struct LSmem {
@@ -71,12 +65,6 @@ struct LSmem {
 };
 static_assert(sizeof(LSmem<GW_KV_BF16>) <= 232448, "shared memory of one CTA");
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
-}
-__device__ __forceinline__ void zero16(uint32_t dst) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
-}
 // Zero the rows r of a K or V stage for which want(r).
 template <int DT, class Want>
 __device__ __forceinline__ void zero_rows(uint32_t base, int lane, Want want) {
@@ -90,14 +78,6 @@ __device__ __forceinline__ void store_f32x8(float* dst, const float* x) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(x[0]), "f"(x[1]), "f"(x[2]),
                "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
                : "memory");
-}
-
-// x as two e4m3 terms, hi = e4m3(x) and lo = e4m3(x - hi), two values at a time.
-__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __nv_fp8x2_storage_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
-  const float2 hf = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(h2, __NV_E4M3)));
-  hi = h2;
-  lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 - hf.x, x1 - hf.y), __NV_SATFINITE, __NV_E4M3);
 }
 
 struct Unit {

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
   using SM = FSmem<LAYOUT, NR>;
   constexpr bool kE4 = T::kE4;
   constexpr int NB = T::kBufs, kTok = T::kTok, kPages = T::kPages;
-  constexpr float kBelow = kE4 ? kBelowMax : 0.f, kRaise = kLazy + kBelow;
+  constexpr float kBelow = Reference<kE4>::kBelow, kRaise = Reference<kE4>::kRaise;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;

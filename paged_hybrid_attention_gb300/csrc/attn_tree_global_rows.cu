@@ -444,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
 #pragma unroll
         for (int g8 = 1; g8 < KN / 8; ++g8) mraw = fmaxf(mraw, mg[g8]);
         const float mx = mraw * sc;
-        const bool raise = mx > m_ref + kLazy + (kE4 ? kBelowMax : 0.f);
+        const bool raise = mx > m_ref + Reference<kE4>::kRaise;
         if (__any_sync(0xffffffffu, raise)) {
-          const float m_new = raise ? mx - (kE4 ? kBelowMax : 0.f) : m_ref;
+          const float m_new = raise ? mx - Reference<kE4>::kBelow : m_ref;
           const float alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
           if (__any_sync(0xffffffffu, raise && m_ref != -INFINITY)) {
             // O *= alpha for this warp's rows once P.V of the tile before is done

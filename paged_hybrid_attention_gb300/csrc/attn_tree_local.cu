@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using T = LT<DT, NR>;
   using SM = LSmem<DT, NR>;
   constexpr bool kE4 = T::kE4;
-  constexpr float kBelow = kE4 ? kBelowMax : 0.f, kRaise = kLazy + kBelow;
+  constexpr float kBelow = Reference<kE4>::kBelow, kRaise = Reference<kE4>::kRaise;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   SM& sm = *reinterpret_cast<SM*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;

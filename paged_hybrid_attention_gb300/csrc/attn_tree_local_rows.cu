@@ -147,8 +147,8 @@ __device__ __forceinline__ bool softmax_tile(uint32_t s_addr, uint32_t o_addr, i
     for (int c = 4 + i; c < KN; c += 4) mg[i] = fmaxf(mg[i], __uint_as_float(sv[c]));
   }
   const float mx = fmaxf(fmaxf(mg[0], mg[1]), fmaxf(mg[2], mg[3])) * sc;  // -inf stays -inf (sc > 0)
-  constexpr float kBelow = kE4 ? kBelowMax : 0.f;
-  const bool raise = mx > m_ref + (kLazy + kBelow);  // false while the copy has no key
+  constexpr float kBelow = Reference<kE4>::kBelow;
+  const bool raise = mx > m_ref + Reference<kE4>::kRaise;  // false while the copy has no key
   if (__any_sync(0xffffffffu, raise)) {
     const float m_new = raise ? mx - kBelow : m_ref;
     const float alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);

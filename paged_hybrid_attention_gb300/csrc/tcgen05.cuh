@@ -53,11 +53,13 @@ __host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N, bool a_mn_m
 // Four softmax weights in three e5m2 terms each, w[term] holding their bytes: an
 // e5m2 number is the upper byte of an fp16 one, so the weights, rounded to fp16,
 // are cut by masks and exact differences into terms of three bits, 2^-9 of a
-// weight in all.  Weights of up to 2^15 are in range, down to 2^-16, where two
-// e4m3 terms would end at 2^-10 and lose a long tail.  `held`: the weights as the
-// terms hold them.
+// weight in all, or 2^-16, the smallest step, which small weights are rounded to
+// (half of it is added before the cut: a cut alone would take up to all of a long
+// tail).  Weights of up to 2^15 are in range; two e4m3 terms would end at 2^-10.
+// `held`: the weights as the terms hold them.
 __device__ __forceinline__ void split_e5m2(float p0, float p1, float p2, float p3, uint32_t (&w)[3], float (&held)[4]) {
-  __half2 x[2] = {__floats2half2_rn(p0, p1), __floats2half2_rn(p2, p3)};
+  const __half2 half_step = __half2half2(__ushort_as_half(0x0080));  // 2^-17
+  __half2 x[2] = {__hadd2(__floats2half2_rn(p0, p1), half_step), __hadd2(__floats2half2_rn(p2, p3), half_step)};
   __half2 used[2];
 #pragma unroll
   for (int term = 0; term < 3; ++term) {

@@ -602,6 +602,8 @@ def tree_attn_local(pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, p
     handle, rows, hq, batch, pages = _tree_args(fn, 256, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask,
                                                 pos, workspace, dev_status, stream)
     _vector(fn, "pos", pos, rows)
+    if rows == 0:  # every slot is idle; an empty tensor has no address
+        return
     scale = 1.0 / math.sqrt(256) if scale is None else scale
     _check(_lib.gw_tree_attn_local(pool.desc, q.data_ptr(), out.data_ptr(), hq, batch, cu_q_rows.data_ptr(),
                                    seq_lens.data_ptr(), block_table.data_ptr(), pages, tree_mask.data_ptr(),
@@ -613,8 +615,10 @@ def tree_attn_global(pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, 
                      dev_status=None, stream=None):
     """gw_tree_attn_global: tree_attn_local over a global pool, without a window."""
     fn = "gw_tree_attn_global"
-    handle, _, hq, batch, pages = _tree_args(fn, 512, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, None,
-                                             workspace, dev_status, stream)
+    handle, rows, hq, batch, pages = _tree_args(fn, 512, pool, q, out, cu_q_rows, seq_lens, block_table, tree_mask, None,
+                                                workspace, dev_status, stream)
+    if rows == 0:
+        return
     scale = 1.0 / math.sqrt(512) if scale is None else scale
     _check(_lib.gw_tree_attn_global(pool.desc, q.data_ptr(), out.data_ptr(), hq, batch, cu_q_rows.data_ptr(),
                                     seq_lens.data_ptr(), block_table.data_ptr(), pages, tree_mask.data_ptr(),
@@ -650,6 +654,8 @@ def tree_accept(cu_q_rows, seq_lens, parent, draft, target, path, path_lens, nex
     most = min(path.shape[1], 64) if max_q_rows is None else int(max_q_rows)
     if path.shape[1] < most:
         _invalid(fn, "path has %d columns, max_q_rows is %d" % (path.shape[1], most))
+    if rows == 0:  # every slot is idle: these are not read, but an empty tensor has no address
+        parent = draft = target = cu_q_rows
     _check(_lib.gw_tree_accept(batch, cu_q_rows.data_ptr(), seq_lens.data_ptr(), most, parent.data_ptr(),
                                draft.data_ptr(), target.data_ptr(), path.data_ptr(), stride, path_lens.data_ptr(),
                                _addr(next_tokens), _addr(new_lens), _addr(dev_status), handle))

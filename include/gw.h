@@ -630,7 +630,8 @@ gw_status gw_norm_rope_append(const gw_kv_pool* pool, const void* q, int64_t q_r
  *              dev_status, stream  as for gw_decode_attn_local.
  *   tree_mask  uint64 [total_rows], 8-byte aligned; bits from n on are ignored.
  *   pos        int32 [total_rows]: the rows' positions, at least base (a row
- *              before it sees nothing: GW_DEV_POS_RANGE).
+ *              before it sees nothing, GW_DEV_POS_RANGE, and may be seen by rows
+ *              whose window ends behind it).
  *   max_q_rows  bound on n, in [1, 64].
  *   workspace  of gw_tree_workspace_bytes(...) bytes, 256-byte aligned; needs no
  *              initialisation.  Calls that share one run one after the other:
@@ -662,7 +663,9 @@ gw_status gw_tree_attn_local(const gw_kv_pool* pool, const void* q, void* out, i
 /*
  * gw_tree_attn_global - attention of drafted trees on a global pool, all three
  * layouts: as gw_tree_attn_local without a window (every row sees the cached
- * tokens [0, base)) and without positions.  num_q_heads 8, 16 or 32.
+ * tokens [0, base)) and without positions.  num_q_heads 8, 16 or 32.  out
+ * overlaps no input: a row's halves are computed apart, each from all of q (out
+ * the same as q: GW_ERR_INVALID_ARG).
  */
 gw_status gw_tree_attn_global(const gw_kv_pool* pool, const void* q, void* out, int32_t num_q_heads, int32_t batch,
                               const int32_t* cu_q_rows, const int32_t* seq_lens, const int32_t* block_table,

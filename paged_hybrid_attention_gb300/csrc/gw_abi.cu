@@ -758,6 +758,8 @@ static gw_status tree_attn(const char* fn, bool local, const gw_kv_pool* pool, c
   const TreeLayout w = tree_layout(pool, num_q_heads, batch, max_pages_per_seq, max_q_rows, window);
   if (workspace_bytes < w.total)
     return fail(GW_ERR_WORKSPACE, fn, "workspace_bytes %zu < %zu needed", workspace_bytes, w.total);
+  // one half of a row may be written while the other half's unit has yet to read q
+  if (!local && q == out) return fail(GW_ERR_INVALID_ARG, fn, "out is q: a global call's rows are not computed in place");
   LocalArgs a{};
   a.pool = static_cast<const uint8_t*>(pool->base);
   a.num_pages = pool->num_pages;

@@ -86,9 +86,15 @@ __host__ __device__ constexpr TreeRule tree_rule_local(int group) { return {kTre
 // Global layers, rows along M: units (two a chunk and block) enough for the GPU's
 // 152 SMs, few enough that their parts, 128 KB a unit, stay small beside the cache
 // (8 x 131072 tokens, one block: 367 us with up to 38 chunks, 404 with 76; 344 with
-// 19, which would leave a lone sequence a fourth of the SMs).  Chunks of 40 tiles: 16
-// sequences of 512 to 8192 tokens, four blocks, 121 us, of 32 130, of 24 131, of 56 133.
-__host__ __device__ constexpr TreeRule tree_rule_global(int heads) { return {kTreeRows / heads, 40, 38}; }
+// 19, which would leave a lone sequence a fourth of the SMs).  Short chunks serve
+// few sequences, long ones many: over 124 calls of 1 to 32 sequences of 2048 to 32768
+// tokens (some with lengths 1 : 16 apart), 1, 2 and 4 blocks, all layouts, chunks of
+// 8, 16, 24, 32 and 40 tiles took 1.14, 1.16, 1.23, 1.31 and 1.34 times the best of
+// the five in the geometric mean and 1.81, 1.55, 1.82, 2.46 and 2.45 times at worst.
+// One sequence of 8192 tokens, four blocks, 32, 41, 49, 61 and 61 us; 16 of 512 to
+// 8192, one block 52, 45, 53, 62 and 72, four 182, 139, 131, 130 and 121; 32 of
+// 8192, four blocks 579, 458, 443, 395 and 395.
+__host__ __device__ constexpr TreeRule tree_rule_global(int heads) { return {kTreeRows / heads, 16, 38}; }
 // Global layers, rows along N: one unit of 64 or 128 KB of parts a chunk (8 x 131072
 // tokens, 4 drafts of 8 heads: 224 us with up to 38 chunks instead of 231, but a lone
 // sequence has as many SMs as chunks).  One sequence of 8192 tokens: chunks of 8

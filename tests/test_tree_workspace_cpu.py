@@ -76,3 +76,9 @@ def test_the_default_bound_holds_a_small_step():
     for layout, dtype in GLOBAL:
         d = desc(layout, dtype)
         assert size(d, 8, 4, 160, 64) >= need(d, 8, 4, 160, 4) > 1 << 20
+
+
+@pytest.mark.parametrize("layout,dtype", GLOBAL)
+def test_a_lone_sequence_is_cut(layout, dtype):
+    """2560 tokens, 16 drafts of 32 heads: three chunks of four blocks, two halves each, whose parts are 128 KB."""
+    assert need(desc(layout, dtype), 32, 1, 160, 16) >= 3 * 4 * 2 << 17

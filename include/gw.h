@@ -903,12 +903,14 @@ gw_status gw_bw_probe_tma(const void* buf, size_t bytes, int32_t* dev_status, vo
  * completes is waited on first (must succeed); then a phase that nothing
  * ever completes, whose wait must give up after limit_ns, OR GW_DEV_TIMEOUT
  * into *dev_status and return, so that the kernel ends normally and the
- * context stays usable.  This is how the kernels' timeout path is tested
+ * context stays usable.  Three more warps learn of it at the vote by which the
+ * kernels' groups of warps leave together.  This is how the kernels' timeout path is tested
  * without hanging a GPU.  The pages this library follows have no
  * counterpart of this entry point.
  *   dev_status  device int32, caller-zeroed.
  *   result      device int32[3]: {first wait succeeded (1), second wait gave
- *               up (1), microseconds spent in the second wait}.
+ *               up and all four warps saw it (1), microseconds spent in the
+ *               second wait}.
  *   limit_ns    in [1e3, 1e9].
  * Errors: GW_ERR_INVALID_ARG, GW_ERR_CUDA.  Asynchronous on `stream`.
  */

@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     uint32_t gi = 0;
     int wt = 0;
-    bool ok = true;
-    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+    bool ok = true, all = true;  // this warp's waits; those of the four, as last voted
+    for (int u = tree_unit(0); u < total && all; u = tree_unit(++wt)) {
       const Unit w = unit_of<LAYOUT, HQ, NR>(a, sm.plan, u);
       const TreeRow* rows = sm.rows[wt % kRowRing] + row0;
       const uint32_t o_addr = tmem + lane_base + T::kOBase + row0;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
       for (int r = 0; r < 32; ++r) l_acc[r] = 0.f;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int sb = gi & 1;
-        if (!warp_wait(&sm.s_ready[sb], (gi >> 1) & 1, st)) { ok = false; break; }
+        ok = ok && warp_wait(&sm.s_ready[sb], (gi >> 1) & 1, st);
         tc::fence_after();
         float x[32];
         {
@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
           for (int r = 0; r < 32; ++r) need |= fmaf(x[r], a.scale_log2, -sm.m[row0 + r]) > kRaise;
         }
         if (need) sm.flag[grp][sb] = static_cast<int32_t>(gi + 1);
-        softmax_bar(grp);
+        all = group_all(1 + grp, ok);
+        if (!all) break;
         bool waited = false;
         if (first || sm.flag[grp][sb] == static_cast<int32_t>(gi + 1)) {
           float y[32];
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
             }
             if (rescale) {
               // O^T *= alpha per row, once P.V of the tile before is done
-              if (!warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+              ok = ok && warp_wait(&sm.p_free, (gi - 1) & 1, st);
               waited = true;
               tc::fence_after();
 #pragma unroll 1
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
           }
         }
         // into shared memory once P.V of the tile before has read its P
-        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        if (gi >= 1 && !waited) ok = ok && warp_wait(&sm.p_free, (gi - 1) & 1, st);
         uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
         if (active) {
 #pragma unroll
@@ -578,11 +579,12 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         tc::fence_before();
         mbar_arrive(&sm.p_ready);
       }
-      if (!ok) break;
+      if (!all) break;
       // ---- epilogue: l over the threads, then O^T by dims
       row_fold<32, false>(l_acc, lane);
       sm.red[grp][quad][lane] = l_acc[0];
-      softmax_bar(grp);
+      all = group_all(1 + grp, ok);
+      if (!all) break;
       if (gtid < 32) {
         const float l = ((sm.red[grp][0][gtid] + sm.red[grp][1][gtid]) + sm.red[grp][2][gtid]) + sm.red[grp][3][gtid];
         sm.inv[row0 + gtid] = w.nc > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
@@ -593,7 +595,8 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
                 make_float2(sm.m[row0 + gtid] == kUnset ? -INFINITY : sm.m[row0 + gtid], l);
       }
       softmax_bar(grp);
-      if (!warp_wait(&sm.o_done, wt & 1, st)) break;
+      ok = warp_wait(&sm.o_done, wt & 1, st);
+      if (!ok) continue;  // to the next unit's vote
       tc::fence_after();
 #pragma unroll 1
       for (int blk = 0; blk < 4; ++blk) {

@@ -407,8 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
     uint32_t gi = 0;
     int wt = 0;
-    bool ok = true;
-    for (int u = tree_unit(0); u < total && ok; u = tree_unit(++wt)) {
+    bool ok = true, all = true;  // this warp's waits; those of the four, as last voted
+    for (int u = tree_unit(0); u < total && all; u = tree_unit(++wt)) {
       const Unit w = unit_of<DT, G>(a, sm.plan, u);
       const TreeRow* rows = sm.rows[wt % kRowRing];
       const uint32_t o_addr = tmem + lane_base + T::kOBase;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r = 0; r < NR; ++r) l_acc[r] = 0.f;
       for (int j = 0; j < w.nt; ++j, ++gi) {
         const int sb = gi & 1;
-        if (!warp_wait(&sm.s_ready[sb], (gi >> 1) & 1, st)) { ok = false; break; }
+        ok = ok && warp_wait(&sm.s_ready[sb], (gi >> 1) & 1, st);
         tc::fence_after();
         float x[NR];
         {
@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int r = 0; r < NR; ++r) need |= fmaf(x[r], a.scale_log2, -sm.m[r]) > kRaise;
         }
         if (need) sm.flag[sb] = static_cast<int32_t>(gi + 1);
-        softmax_bar();
+        all = group_all(1, ok);
+        if (!all) break;
         bool waited = false;
         if (first || sm.flag[sb] == static_cast<int32_t>(gi + 1)) {
           float y[NR];
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (rescale) {
               // O^T *= alpha per row, once P.V of the tile before is done
-              if (!warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+              ok = ok && warp_wait(&sm.p_free, (gi - 1) & 1, st);
               waited = true;
               tc::fence_after();
 #pragma unroll 1
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // into shared memory once P.V of the tile before has read its P
-        if (gi >= 1 && !waited && !warp_wait(&sm.p_free, (gi - 1) & 1, st)) { ok = false; break; }
+        if (gi >= 1 && !waited) ok = ok && warp_wait(&sm.p_free, (gi - 1) & 1, st);
         uint8_t* dst = sm.p + (tok >> 3) * (T::kNT / T::kRowsPerBlk * 128) + (tok & 7) * 16;
         if (active) {
 #pragma unroll
@@ -560,11 +561,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before();
         mbar_arrive(&sm.p_ready);
       }
-      if (!ok) break;
+      if (!all) break;
       // ---- epilogue: l over the threads, then O^T by dims
       const float sum = row_reduce<NR, false>(l_acc, lane);
       if (lane < NR) sm.red[warp][lane] = sum;
-      softmax_bar();
+      all = group_all(1, ok);
+      if (!all) break;
       if (tid < NR) {
         const float l = ((sm.red[0][tid] + sm.red[1][tid]) + sm.red[2][tid]) + sm.red[3][tid];
         sm.inv[tid] = w.nc > 1 ? 1.f : l > 0.f ? 1.f / l : 0.f;
@@ -573,7 +575,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_float2(sm.m[tid] == kUnset ? -INFINITY : sm.m[tid], l);
       }
       softmax_bar();
-      if (!warp_wait(&sm.o_done, wt & 1, st)) break;
+      ok = warp_wait(&sm.o_done, wt & 1, st);
+      if (!ok) continue;  // to the next unit's vote
       tc::fence_after();
 #pragma unroll 1
       for (int blk = 0; blk < 2; ++blk) {

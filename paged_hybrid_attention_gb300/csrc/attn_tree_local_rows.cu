@@ -529,14 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = tree_unit(0); u < total; u = tree_unit(++wt)) {
       const Unit w = unit_of<G>(a, sm.plan, u);
       const int next = tree_unit(wt + 1);
+      bool ok = true;
       if (next < total) {
         load_q(unit_of<G>(a, sm.plan, next));
-        if (!warp_wait(&sm.q_free, wt & 1, st)) break;
+        ok = warp_wait(&sm.q_free, wt & 1, st);
         tc::fence_after();
-        store_q(wt + 1);
+        if (ok) store_q(wt + 1);
       }
       // ---- epilogue: the copies' rows merged, as output rows or a chunk's part
-      if (!warp_wait(&sm.stat_full[wt & 1], (wt >> 1) & 1, st)) break;
+      ok = ok && warp_wait(&sm.stat_full[wt & 1], (wt >> 1) & 1, st);
       const int stride = kM / w.copies;
       float2 ml[4];
       float M = -INFINITY, den = 0.f;
@@ -550,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sm.stat_free[wt & 1]);
       // this lane's factor; a part stays unnormalised
       const float f = own == -INFINITY && den == den ? 0.f : ex2(own - M) * (w.nc > 1 ? 1.f : 1.f / den);
-      if (!warp_wait(&sm.o_done, wt & 1, st)) break;
+      ok = ok && warp_wait(&sm.o_done, wt & 1, st);
+      if (!group_all(1, ok)) break;  // before the barriers below
       tc::fence_after();
       const int64_t part0 = static_cast<int64_t>(u) * a.part_rows;
       if (w.nc > 1 && r < w.rows && r < stride) a.part_ml[part0 + r] = make_float2(M, den);

@@ -127,26 +127,37 @@ __global__ void __launch_bounds__(kTmaWarps * 32, 1) bw_probe_tma_kernel(int64_t
 // gw_wait_selftest: one warp, one mbarrier of arrival count 1.  Phase 0 is
 // completed by an arrival, then waited on (must succeed); phase 1 is never
 // arrived on, so its wait must give up after limit_ns, raise GW_DEV_TIMEOUT
-// and return.  result = {phase-0 wait succeeded, phase-1 wait gave up,
-// microseconds spent in the phase-1 wait}.
+// and return.  Three more warps, whose waits are fine, meet the first at the vote
+// that groups of warps leave by (group_all).  result = {phase-0 wait succeeded,
+// phase-1 wait gave up and all four warps saw it, microseconds spent in the
+// phase-1 wait}.
 __global__ void wait_selftest_kernel(int32_t* status, int32_t* result, uint64_t limit_ns) {
   __shared__ uint64_t bar;
+  __shared__ int32_t left;
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
     fence_mbar_init();
+    left = 0;
   }
-  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x >= 32) {
+    if (!group_all(1, true)) atomicAdd(&left, 1);
+    __syncthreads();
+    return;
+  }
   if (threadIdx.x == 0) mbar_arrive(&bar);
   __syncwarp();
   const bool ok0 = __all_sync(0xffffffffu, mbar_wait(&bar, 0, status, limit_ns));
   const uint64_t t0 = global_ns();
   const bool ok1 = __all_sync(0xffffffffu, mbar_wait(&bar, 1, status, limit_ns));
   const uint64_t dt = global_ns() - t0;
+  if (!group_all(1, ok1)) atomicAdd(&left, 1);
+  __syncthreads();
   if (threadIdx.x == 0) {
     result[0] = ok0 ? 1 : 0;
-    result[1] = ok1 ? 0 : 1;
+    result[1] = !ok1 && left == 128 ? 1 : 0;
     result[2] = static_cast<int32_t>(dt / 1000 < 0x7fffffffull ? dt / 1000 : 0x7fffffffull);
   }
 }
@@ -154,7 +165,7 @@ __global__ void wait_selftest_kernel(int32_t* status, int32_t* result, uint64_t 
 }  // namespace
 
 cudaError_t launch_wait_selftest(int32_t* status, int32_t* result, int64_t limit_ns, cudaStream_t st) {
-  return launch_pdl(wait_selftest_kernel, dim3(1), dim3(32), 0, st, status, result,
+  return launch_pdl(wait_selftest_kernel, dim3(1), dim3(128), 0, st, status, result,
                     static_cast<uint64_t>(limit_ns));
 }
 

@@ -80,6 +80,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
   return true;
 }
 
+// Barrier `id` of four warps, and whether `ok` held in all of them.  A warp whose
+// bounded wait gives up goes on to the group's next one of these instead of leaving
+// alone, so that its companions, whose waits end too, are not left at a barrier
+// (which has no limit) and all four leave together.
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"(id), "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
 // Orders this thread's earlier global writes (generic proxy) before later
 // asynchronous-proxy accesses, such as a tensor copy of the same bytes.
 __device__ __forceinline__ void fence_proxy_async_global() {

@@ -1,0 +1,53 @@
+"""The tree kernels' way out when a bounded wait gives up, read in their sources (it
+cannot be provoked on a GPU without a kernel that is broken on purpose): a warp that
+shares a named barrier with others leaves by the group's vote only."""
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_hybrid_attention_gb300", "csrc")
+FILES = ["attn_tree_local.cu", "attn_tree_local_rows.cu", "attn_tree_global.cu", "attn_tree_global_rows.cu"]
+BARRIER = re.compile(r"softmax_bar\(|bar\.sync|group_all\(")
+
+
+def roles(name):
+    """The kernel's warp roles: the text between the ruled headings, helpers left out."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    parts = re.split(r"// -{5,} ?([A-Z][^\n]*)\n", text[text.index("__global__"):])
+    return dict(zip(parts[1::2], parts[2::2]))
+
+
+def block(text, start):
+    """The braces' block that begins at or after `start`."""
+    at, depth = text.index("{", start), 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i + 1]
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_groups_leave_together(name):
+    found = 0
+    for role, text in roles(name).items():
+        text = text.split("\n  tc::fence_before();\n  __syncthreads();")[0]
+        if not BARRIER.search(text):
+            continue
+        found += 1
+        loops = [block(text, m.start()) for m in re.finditer(r"for \(int u = tree_unit", text)]
+        body = loops[-1]
+        assert "group_all(" in body, role
+        # no wait that gives up leaves the loop by itself
+        assert not re.search(r"!\s*warp_wait\([^;]*\)\s*\)?\s*(\{[^}]*)?break", body), role
+        for m in re.finditer(r"if \(([^\n]*)\) break;", body):
+            assert m.group(1).strip() in ("!all", "!group_all(1, ok)"), (role, m.group(0))
+        # the first barrier of the loop is a vote
+        assert BARRIER.search(body).group(0) == "group_all(", role
+        # and so is the first one behind every wait
+        for m in re.finditer(r"warp_wait\(", body):
+            after = BARRIER.search(body, m.end())
+            assert after is None or after.group(0) == "group_all(", (role, body[m.start():m.start() + 60])
+    assert found == (0 if name == "attn_tree_global_rows.cu" else 1)

@@ -27,6 +27,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int32_
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
+// Waits for a role's own copies or products before its CTA may end: the last use of
+// each of a ring of N barriers that `issued` of them complete, in turn.  They are
+// complete already unless a wait gave up.
+template <int N>
+__device__ __forceinline__ void drain(uint64_t* bars, uint32_t issued) {
+  for (uint32_t k = issued > N ? issued - N : 0; k < issued; ++k) mbar_wait(&bars[k % N], (k / N) & 1, nullptr);
+}
+
 __device__ __forceinline__ void zero16(uint32_t dst) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(dst), "r"(0) : "memory");
 }

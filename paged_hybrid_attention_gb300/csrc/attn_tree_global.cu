@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         }
       }
     }
+    drain<NB>(fulls, gi);
   } else if (warp == 6) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s =
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
     }
+    drain<2>(sm.s_ready, gi);
   } else if (warp == 7) {
     // ------------------------------------------------------- P.V issue
     const uint32_t id_o =
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(FL<LAYOUT, NR>::kThreads, 1) global_tree_kerne
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
+    drain<1>(&sm.p_free, gi);
   } else if (warp >= 8 && warp < 12) {
     // -------------------------------------------------------------- Q rows
     // a warp copies 8 rows of every 32: lane l row l % 8, every fourth 16-byte block

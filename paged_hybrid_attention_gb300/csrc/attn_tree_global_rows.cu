@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         }
       }
     }
+    drain<NB>(fulls, gi);
   } else if (warp == 9) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s = kE4 ? tc::idesc_e4m3(kM, KN, false, false) : tc::idesc_bf16(kM, KN, false, false);
@@ -334,7 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         };
         issue(false);
         if (Parts<LAYOUT>::kApart && LAYOUT != GW_LAYOUT_GLOBAL_FULL) {
-          if (!warp_wait(&sm.vfull[b], (i / NB) & 1, st)) { ok = false; break; }
+          if (!warp_wait(&sm.vfull[b], (i / NB) & 1, st)) {
+            tc::commit_warp(&sm.s_ready[sb]);  // those issued above, for drain
+            ++i;
+            ok = false;
+            break;
+          }
           tc::fence_after();
           issue(true);
         }
@@ -343,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
     }
+    drain<2>(sm.s_ready, i);
   } else if (warp == 10) {
     // ------------------------------------------------------- P.V issue
     const uint32_t id_o = kE4 ? tc::idesc_e5m2_e4m3(kM, 256, false, true) : tc::idesc_bf16(kM, 256, false, true);
@@ -395,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_tree_rows_kernel(const Loc
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
+    drain<2>(sm.pfree, i);
   } else if (warp < 4) {
     // ------------------------------------------------------------ softmax
     const int r = tid, qi = r / HQ;

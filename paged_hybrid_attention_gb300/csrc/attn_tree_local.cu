@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_rows(smem_u32(is_v ? sm.v[b] : sm.k[b]) + c * T::kPlane + j * 2048, &kv_map, c, row, full, pol);
       }
     }
+    drain<kStages>(is_v ? sm.vfull : sm.kfull, gi);
   } else if (warp == 6) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s =
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
     }
+    drain<2>(sm.s_ready, gi);
   } else if (warp == 7) {
     // ------------------------------------------------------- P.V issue
     const uint32_t id_o =
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
+    drain<1>(&sm.p_free, gi);
   } else if (warp == 8) {
     // -------------------------------------------------------------- Q rows
     // The next unit's rows wait in registers as Q wants them: lane l has rows

@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_rows(smem_u32(is_v ? sm.v[b] : sm.k[b]) + c * kPlane + j * 2048, &kv_map, c, row, full, pol);
       }
     }
+    drain<kStages>(is_v ? sm.vfull : sm.kfull, gi);
   } else if (warp == 10) {
     // ---------------------------------------------------- Q.K^T issue
     const uint32_t id_s = kE4 ? tc::idesc_e4m3(kM, kN, false, false) : tc::idesc_bf16(kM, kN, false, false);
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == w.nt - 1) tc::commit_warp(&sm.q_free);
       }
     }
+    drain<2>(sm.s_ready, gi);
   } else if (warp == 11) {
     // ------------------------------------------------------- P.V issue
     const uint32_t id_o = kE4 ? tc::idesc_e5m2_e4m3(kM, 256, false, true) : tc::idesc_bf16(kM, 256, false, true);
@@ -396,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == w.nt - 1) tc::commit_warp(&sm.o_done);
       }
     }
+    drain<2>(sm.pfree, gi);
   } else if (warp < 4) {
     // ------------------------------------------------------------ softmax
     uint32_t gi = 0;

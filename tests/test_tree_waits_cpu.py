@@ -16,7 +16,7 @@ def roles(name):
     """The kernel's warp roles: the text between the ruled headings, helpers left out."""
     with open(os.path.join(CSRC, name)) as f:
         text = f.read()
-    parts = re.split(r"// -{5,} ?([A-Z][^\n]*)\n", text[text.index("__global__"):])
+    parts = re.split(r"// -{5,} ?([A-Za-z][^\n]*)\n", text[text.index("__global__"):])
     return dict(zip(parts[1::2], parts[2::2]))
 
 
@@ -51,3 +51,18 @@ def test_groups_leave_together(name):
             after = BARRIER.search(body, m.end())
             assert after is None or after.group(0) == "group_all(", (role, body[m.start():m.start() + 60])
     assert found == (0 if name == "attn_tree_global_rows.cu" else 1)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_roles_wait_for_what_they_issued(name):
+    """Copies and products that are in flight when a role ends are waited for, before the CTA's memory goes."""
+    found = {}
+    for role, text in roles(name).items():
+        loops = [(m.start(), block(text, m.start())) for m in re.finditer(r"for \(int u = tree_unit", text)]
+        for start, body in loops:
+            behind = text[text.index(body, start) + len(body):].lstrip()
+            if re.search(r"tma_rows\(|bulk_g2s\(", body):
+                found["copies"] = behind.startswith(("drain<kStages>(", "drain<NB>("))
+            elif "commit_warp(" in body:
+                found[role.split()[0]] = behind.startswith("drain<")
+    assert found == {"copies": True, "Q.K^T": True, "P.V": True}, found

@@ -148,7 +148,9 @@ struct GSmem {
   uint64_t full[T::kNumBuf], slot_empty[T::kNumBuf][kTilePages];
   uint64_t s_ready[2], p_ready[2], pfree[2], o_done[2], o_free[2], q_ready[2], q_free[2], qs_ready[4];
   uint32_t tmem_base;
-  int32_t flag[2];  // per tile parity: index + 1 of the last tile that asked for a new max
+  // per tile parity: index + 1 of the last tile that asked for a new max; a warp
+  // whose wait gave up leaves here (read by all four behind the tile's barrier)
+  int2 flag[2];
   int32_t app_done;  // fused append: units of this CTA (in order) whose rows are written
   int32_t ub[kMaxBatch + 1 + 32];  // split plan (+ scan scratch)
 };
@@ -313,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       mbar_init(&sm.pfree[b], 1);
       mbar_init(&sm.o_done[b], 1);
       mbar_init(&sm.o_free[b], 128);
-      sm.flag[b] = 0;
+      sm.flag[b] = make_int2(0, 0);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.q_ready[b], 1);
@@ -696,16 +698,23 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       l_acc[h] = 0.f;
     }
     int uidx = -1;
+    // This thread's waits.  The four warps meet at a barrier without a limit, so none
+    // leaves alone: once a tile by the flag above (bar.red with the vote in it cost a
+    // long call 1.4 %), once a unit by group_all.
+    bool ok = true;
     for (uint32_t n = 0;; ++n) {
       const int b = n % NB;
-      if (!mbar_wait(&sm.full[b], (n / NB) & 1, st)) break;
-      const TileDesc d = sm.ring[n % kRing];
-      if (d.flags & kEnd) break;
+      ok = ok && mbar_wait(&sm.full[b], (n / NB) & 1, st);
+      const TileDesc d = sm.ring[n % kRing];  // (an older one if the wait gave up: nothing is done with it)
+      if (d.flags & kEnd) {
+        softmax_bar();  // a warp that gave up stands at the tile's
+        break;
+      }
       const bool first = d.flags & kFirst;
       if (first) ++uidx;
       // e4m3: the unit's per-head descale of q is published with qs_ready
-      if (kE4 && first && !mbar_wait(&sm.qs_ready[uidx & 3], (uidx >> 2) & 1, st)) break;
-      if (!mbar_wait(&sm.s_ready[n & 1], (n >> 1) & 1, st)) break;
+      if (kE4 && first) ok = ok && mbar_wait(&sm.qs_ready[uidx & 3], (uidx >> 2) & 1, st);
+      ok = ok && mbar_wait(&sm.s_ready[n & 1], (n >> 1) & 1, st);
       tc::fence_after();
       uint32_t r[32];
       const uint32_t s_addr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kSCols * (n & 1);
@@ -742,9 +751,12 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       // the next tile (whose QK^T can complete before this softmax ends), and
       // this parity is not written again before every thread has passed the
       // barrier below on the next tile.
-      if (need) sm.flag[n & 1] = static_cast<int32_t>(n + 1);
+      if (need) sm.flag[n & 1].x = static_cast<int32_t>(n + 1);
+      if (!ok) sm.flag[n & 1].y = 1;
       softmax_bar();
-      if (first || sm.flag[n & 1] == static_cast<int32_t>(n + 1)) {
+      const int2 flag = sm.flag[n & 1];
+      if (flag.y) break;
+      if (first || flag.x == static_cast<int32_t>(n + 1)) {
         // ---- slow path: tile max per head, maybe rescale
         float x[HQ];
 #pragma unroll
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
         }
         if (rescale) {
           // O^T *= alpha per head column, once P.V of the previous tile is done
-          if (!mbar_wait(&sm.pfree[(n - 1) & 1], ((n - 1) >> 1) & 1, st)) break;
+          ok = ok && mbar_wait(&sm.pfree[(n - 1) & 1], ((n - 1) >> 1) & 1, st);
           tc::fence_after();
           const uint32_t ob = uidx & 1;
 #pragma unroll 1
@@ -787,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
         }
       }
       // ---- P^T (bf16) for this tile; wait until P.V two tiles back released the buffer
-      if (n >= 2 && !mbar_wait(&sm.pfree[n & 1], ((n >> 1) - 1) & 1, st)) break;
+      if (n >= 2) ok = ok && mbar_wait(&sm.pfree[n & 1], ((n >> 1) - 1) & 1, st);
       if (active && kE4 && kAcc) {
         uint8_t* pdst = sm.p[n & 1] + ((t >> 3) * (NP / 16)) * 128 + (t & 7) * 16;
 #pragma unroll
@@ -900,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
       if (d.flags & kLast) {
         // ---- epilogue: unnormalised partial (m, l, o) of this unit
         const uint32_t ob = uidx & 1;
-        if (!mbar_wait(&sm.o_done[ob], (uidx >> 1) & 1, st)) break;
+        ok = ok && mbar_wait(&sm.o_done[ob], (uidx >> 1) & 1, st);
         tc::fence_after();
         float* po = a.part_o + static_cast<int64_t>(d.unit) * HQ * 512;
 #pragma unroll 1
@@ -917,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) global_decode_kernel(const LocalA
         for (int h = 0; h < HQ; ++h) x[h] = l_acc[h];
         const float wl = head_reduce<HQ, false>(x, lane);
         if (lane < HQ) sm.red[warp][lane] = wl;
-        softmax_bar();
+        if (!group_all(1, ok)) break;
         if (tid < HQ) {
           const float l = ((sm.red[0][tid] + sm.red[1][tid]) + sm.red[2][tid]) + sm.red[3][tid];
           a.part_ml[static_cast<int64_t>(d.unit) * HQ + tid] = make_float2(sm.mvec[tid], l);

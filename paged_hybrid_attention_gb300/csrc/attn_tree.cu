@@ -22,9 +22,9 @@ namespace {
 // block), else (chunk, row block, half of the dims).
 //
 // 8 x 131072 tokens, 8 heads, 4 drafts (512 warps with kSplit = 1, 76 chunks): the
-// call 231 us with 4, 254 with 1 and 262 with (m, l) read chunk by chunk; 4 x 131072, full layout, 169 and 183.  16 sequences
-// of 512 to 8192 tokens, 16 drafts, 32 heads (16384 warps, up to 4 chunks): 173 and
-// 129.
+// call 221 us with 4 and 237 with 1 (254 at a step when 262 with (m, l) read chunk by
+// chunk); 4 x 131072, full layout, 167 and 174.  16 sequences of 512 to 8192 tokens,
+// 16 drafts, 32 heads (16384 warps, up to 8 chunks): 194 and 140.
 template <int kSplit>
 struct Merge {
   static constexpr int kWarps = kSplit == 1 ? 4 : 8;
@@ -174,10 +174,10 @@ cudaError_t launch_merge(const LocalArgs& a, int group, const TreeRule& rule, in
 
 // Up to 32 rows x heads (64 on bf16 global layers) lie along the products' N, more
 // along M.  Local, 16 sequences of 512 to 8192 tokens, 16 KV heads of 2 heads, bf16:
-// 16 drafts 49 us (along M 55.4), 33 drafts 55.0 (along N, in blocks of 32 rows,
-// 100.6); 61 e4m3 sequences, 7 drafts 91 us (150).  Global, 8 x 131072 tokens, 8
-// heads: 4 drafts 222 us (along M 432), 8 drafts 309 (435); 1 x 8192, 8 drafts 32
-// (54); 2 sequences of 37 and 100 tokens, full layout, 5 drafts 11.7 both ways.  The
+// 16 drafts 49 us (along M 55), 33 drafts 55.0 (along N, in blocks of 32 rows,
+// 100.6); 61 e4m3 sequences, 7 drafts 91 us (177).  Global, 8 x 131072 tokens, 8
+// heads: 4 drafts 222 us (along M 389), 8 drafts 314 (381); 1 x 8192, 8 drafts 32
+// (36); 2 sequences of 37 and 100 tokens, full layout, 5 drafts 11.8 (11.0).  The
 // rule is the call's bound, so that a captured call stays what it is.
 //
 // The merge is left out where the block table's width allows one chunk only.

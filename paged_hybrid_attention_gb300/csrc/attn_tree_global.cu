@@ -11,14 +11,14 @@
 // of them and make each half of the output dims compute all logits).  T is 48 tokens
 // on folded pools, three tiles in shared memory beside 32 rows of Q (8 x 131072
 // tokens, 8 heads, 4 drafts: 222 us, two tiles of 64 tokens 231) and two beside 64
-// (309 us with 8 drafts, three of 32 tokens 316); on the full layout 64; on the e4m3
+// (309 us with 8 drafts at that step, three of 32 tokens 316); on the full layout 64; on the e4m3
 // pool, whose MMAs bound a call, 128 (203 us with tiles of 64 and 193 with 128 at
 // that step).
 //
 // 8 x 131072 tokens, 8 heads, 4 drafts: folded 222 us with the merge (0.89 of the copy
-// rate), e4m3 143 (0.69); full layout, 4 x 131072, 167 (0.94).  8 drafts: folded 309
-// us (0.64, bound by the MMAs' and the softmax's chain over two tiles; in
-// attn_tree_global_rows.cu 435), full 176 (0.90; 256).
+// rate), e4m3 148 (0.67); full layout, 4 x 131072, 167 (0.94).  8 drafts: folded 314
+// us (0.63, bound by the MMAs' and the softmax's chain over two tiles; in
+// attn_tree_global_rows.cu 381), full 176 (0.90; 247).
 //
 // A tile is whole pages of 8-token x 16-byte blocks, which are UMMA core matrices:
 // the K-major A operand of Q.K^T, whose K-steps point at k_rot and V on folded

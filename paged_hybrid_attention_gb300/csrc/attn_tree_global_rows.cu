@@ -1,6 +1,7 @@
 // Attention of drafted trees on GLOBAL layers (gw_tree_attn_global), on the
 // tensor cores (tcgen05): head dim 512, one KV head, all three pool layouts,
-// calls of up to more than 32 rows x heads (attn_tree_global.cu has the others).
+// calls whose sequences may have more than 64 rows x heads, on the e4m3 pool more
+// than 32 (attn_tree_global.cu has the others).
 //
 // Row r of a sequence's n <= 64 rows sees the cached tokens [0, L - n) and the
 // drafts of its mask word.  All heads share the KV head, so 128 / HQ rows x HQ
@@ -21,8 +22,8 @@
 //
 // What bounds it: the chain copy, Q.K^T, softmax, P.V over two tile buffers, 1.40 us a
 // tile of which the MMAs are 1.15 (folded); on the e4m3 pool the MMAs of q's two
-// terms, 43 ns each, 1.45 us a tile.  8 x 131072 tokens, 4 rows x 32 heads: 366 us
-// (one block; the cache alone 197); 33 rows x 16 heads, e4m3, 8 x 16384 to 32768: 408.
+// terms, 43 ns each, 1.45 us a tile.  8 x 131072 tokens, 4 rows x 32 heads: 367 us
+// (one block; the cache alone 197); 33 rows x 16 heads, e4m3, 8 x 16384 to 32768: 433.
 //
 // Warp roles (384 threads): warps 0-3 softmax (a thread owns a row), 4-7 Q rows
 // and epilogue, 8 and 11 copies, 9 issues Q.K^T and owns tensor memory, 10 issues

@@ -29,7 +29,7 @@
 //
 // Bound by memory: 16 sequences of 512 to 8192 tokens, 16 drafts, 16 KV heads of 2,
 // window 1024, 49 us (0.82 of the copy rate); e4m3, 61 sequences, 7 drafts 91 us
-// (0.86); 64 sequences, 4 drafts 158 us (0.99).
+// (0.85); 64 sequences, 4 drafts 155 us (1.0).
 #include "attn_tree.cuh"
 #include "tma.cuh"
 

@@ -1,6 +1,6 @@
 // Attention of drafted trees on LOCAL layers (gw_tree_attn_local), on the
-// tensor cores (tcgen05): head dim 256, bf16 or e4m3 pools, calls of up to more
-// than 32 rows x heads of a KV head (attn_tree_local.cu has the others).
+// tensor cores (tcgen05): head dim 256, bf16 or e4m3 pools, calls whose sequences
+// may have more than 32 rows x heads of a KV head (attn_tree_local.cu has the others).
 //
 // Row r of a sequence's n <= 64 rows, at position pos_r, sees the cached tokens
 // j < L - n with j > pos_r - W and the drafts of its mask word whose positions
@@ -10,8 +10,9 @@
 //   O[128 x 256] += P[128 x 64] . V         (UMMA M = 128, N = 256)
 // The cache is read once for all rows of a KV head: 64 drafts of 2 heads are 128
 // flop/B, so a call should stream at the memory's rate.  16 sequences of 512 to
-// 8192 tokens, 64 drafts, 16 KV heads of 2: 58 us, 0.78 of the copy rate; e4m3 57 us
-// (0.44), which waits on the MMAs of q's two terms and P's three.  What stands in
+// 8192 tokens, 64 drafts, 16 KV heads of 2: 58 us, 0.78 of the copy rate; e4m3 71 us
+// (0.35), which waits on the MMAs of q's two terms and P's three and rescales O more
+// often (Reference).  What stands in
 // the way:
 //
 // - Softmax.  A sequence's n G rows need not fill the 128, and a warp reaches only
